@@ -1,0 +1,538 @@
+"""The operators that stand beside KDA in a hybrid stack, as measured workloads.
+
+A hybrid model interleaves KDA layers with layers of attention over a paged
+cache and with gated linear recurrences, and serves them from packed batches
+of requests.  The operators are
+
+    plan        cumulative offsets, block tables and slot maps of one serving
+                step, built on the GPU from the requests' lengths
+    append      new keys and values written into a paged cache of 4-bit values
+                (e2m1, a power-of-two scale for each 32 channels), read back
+    attend      causal grouped-query attention over that cache, for one new
+                token a request and for many, with the read-out gate
+    recurrence  h_t = e^l_t h_(t-1) + x_t per channel with l_t = max(log_alpha_t, floor),
+                out_t = h_t sigmoid(g_t), over uniform and packed batches
+    train       the same with its gradients
+    step        the same for one token of each sequence, the state in place
+
+`own` false: `run` computes the plain forms below, elementary torch operations
+in 32 bits.  `own` true: `run` makes the framework's calls.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+FLOOR = -0.5          # of the recurrence's log decay
+GROUP = 32            # channels that share a scale
+LOW, HIGH = -125, 125  # exponents of the scales: all values are normal numbers in bf16 and fp32
+
+
+# ---- cases ------------------------------------------------------------------------------------
+
+def listed():
+    return [
+        # a decode step of a full serving batch: one new token for each of 256 requests
+        dict(name="plan-step", op="plan", requests=256, past=8192, new=1, page=64),
+        # a step that admits prompts: many requests, small pages
+        dict(name="plan-prompts", op="plan", requests=512, past=1000, new=509, page=16),
+        # the new token of each of 256 requests
+        dict(name="append-step", op="append", tokens=256, kv_heads=8, d=128, page=64, io="bf16"),
+        # the prompt of the 64K prefill
+        dict(name="append-prompt", op="append", tokens=65536, kv_heads=8, d=128, page=64, io="bf16"),
+        # one user, one token: latency
+        dict(name="attend-one", op="attend", requests=1, longest=4097, new=1, heads=32, kv_heads=8, d=128, page=64, io="bf16", gate=True),
+        # a decode step of a full serving batch of ragged contexts
+        dict(name="attend-step", op="attend", requests=256, longest=8192, new=1, heads=32, kv_heads=8, d=128, page=64, io="bf16", gate=True),
+        # two long contexts, six heads to a shared one, 32-bit activations
+        dict(name="attend-long-f32", op="attend", requests=2, longest=131072, new=1, heads=24, kv_heads=4, d=64, page=16, io="f32", gate=False),
+        # prompts processed a piece at a time over what is cached already
+        dict(name="attend-prompts", op="attend", requests=4, longest=8192, new=1000, heads=32, kv_heads=8, d=128, page=64, io="bf16", gate=True),
+        # the 64K prefill, as wide as 32 heads of 128
+        dict(name="recurrence-64k", op="recurrence", rows=1, tokens=65536, requests=0, width=4096, io="bf16", gate=True),
+        # a packed batch in 32 bits of an odd width
+        dict(name="recurrence-packed-f32", op="recurrence", rows=1, tokens=16384, requests=24, width=515, io="f32", gate=False),
+        # a training step: 4 x 4096 tokens, as wide as 16 heads of 128
+        dict(name="train-4x4096", op="train", rows=4, tokens=4096, requests=0, width=2048, io="bf16", gate=True),
+        # one token of each of 256 sequences, as wide as 32 heads of 128
+        dict(name="step-256", op="step", rows=256, width=4096, io="bf16", gate=True),
+    ]
+
+
+def _log_uniform(rng, low, high):
+    return max(low, min(high, int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))))
+
+
+def draw(rng):
+    op = rng.choice(["plan", "append", "attend", "attend", "recurrence", "recurrence", "train", "step"])
+    io, gate = rng.choice(["bf16", "bf16", "f32"]), rng.random() < 0.6
+    if op == "plan":
+        n = _log_uniform(rng, 1, 2000)
+        return dict(op=op, requests=n, past=_log_uniform(rng, 1, 30000), new=_log_uniform(rng, 1, max(1, 200000 // n)), page=rng.choice([16, 32, 64, 128, 256]))
+    heads = dict(kv_heads=rng.choice([1, 2, 3, 4, 8]), d=rng.choice([64, 128]), page=rng.choice([16, 32, 64, 128, 256]))
+    if op == "append":
+        return dict(op=op, tokens=_log_uniform(rng, 1, 60000), io=io, **heads)
+    if op == "attend":
+        shared = rng.choice([1, 2, 3, 4, 6, 8, 12, 16])
+        if rng.random() < 0.6:   # one token each
+            longest = _log_uniform(rng, 1, 100000)
+            n, new = _log_uniform(rng, 1, max(1, min(300, 1500000 // longest))), 1
+        else:
+            longest, new = _log_uniform(rng, 64, 12000), _log_uniform(rng, 2, 1500)
+            new = min(new, longest)
+            n = _log_uniform(rng, 1, max(1, min(16, 30000000 // (longest * new))))
+        return dict(op=op, requests=n, longest=longest, new=new, heads=heads["kv_heads"] * shared, io=io, gate=gate, **heads)
+    width = _log_uniform(rng, 16, 6000)
+    if rng.random() < 0.5:       # whole vectors, as models have them
+        width = max(64, width // 64 * 64)
+    if op == "step":
+        return dict(op=op, rows=_log_uniform(rng, 1, 500), width=width, io=io, gate=gate)
+    most = (100 if op == "recurrence" else 30) * 1000000 // width
+    tokens = _log_uniform(rng, 1, min(60000, most))
+    if rng.random() < 0.5:
+        return dict(op=op, rows=1, tokens=tokens, requests=_log_uniform(rng, 1, min(300, tokens)), width=width, io=io, gate=gate)
+    return dict(op=op, rows=_log_uniform(rng, 1, max(1, min(64, most // tokens))), tokens=tokens, requests=0, width=width, io=io, gate=gate)
+
+
+def _lengths(n, longest, shortest, salt):
+    """n ragged lengths that go by the sizes alone, the first the longest."""
+    rng = random.Random(salt * 1000003 + n * 8191 + longest)
+    return [longest] + [_log_uniform(rng, shortest, longest) if longest > shortest else shortest for _ in range(n - 1)]
+
+
+def _plan_lengths(c):
+    past = [p - 1 for p in _lengths(c["requests"], c["past"] + 1, 1, 1)]   # some requests have nothing cached
+    return past, _lengths(c["requests"], c["new"], 1, 2)
+
+
+def _attend_lengths(c):
+    total = _lengths(c["requests"], c["longest"], 1, 3)
+    return total, [min(t, m) for t, m in zip(total, _lengths(c["requests"], c["new"], 1, 4))]
+
+
+def _packed_offsets(c):
+    """Cumulative offsets of `requests` ragged sequences over `tokens` tokens."""
+    rng = random.Random(5 * 1000003 + c["requests"] * 8191 + c["tokens"])
+    cuts = sorted(rng.randrange(c["tokens"] + 1) for _ in range(c["requests"] - 1))
+    return [0] + cuts + [c["tokens"]]
+
+
+def _pages(tokens, page):
+    return (tokens + page - 1) // page
+
+
+# ---- inputs -----------------------------------------------------------------------------------
+
+def _generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _ints(values, dtype=torch.int32):
+    return torch.tensor(values, dtype=dtype).cuda()
+
+
+def _cache_pair(gen, pages, page, heads, d):
+    """Codes and scales of normal values, as a cache holds them."""
+    codes = torch.empty(pages, heads, page, d // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(pages, heads, page, d // GROUP, dtype=torch.uint8, device="cuda")
+    step = max(1, (1 << 26) // (heads * page * d))
+    for p in range(0, pages, step):
+        x = torch.randn(min(step, pages - p), heads, page, d, generator=gen, device="cuda")
+        codes[p:p + step], scales[p:p + step] = _quantize(x)
+    return codes, scales
+
+
+def prepare(case, seed):
+    c, gen = case, _generator(seed)
+
+    def normal(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+
+    s = dict(op=c["op"])
+    if c["op"] == "plan":
+        past, new = _plan_lengths(c)
+        page, n = c["page"], c["requests"]
+        held = [_pages(p, page) for p in past]
+        need = [_pages(p + m, page) - h for p, m, h in zip(past, new, held)]
+        order = torch.randperm(sum(held) + sum(need) + 7, generator=gen, device="cuda").to(torch.int32)
+        width = _pages(c["past"] + c["new"], page)
+        has = torch.arange(width, device="cuda") < _ints(held)[:, None]
+        table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+        table[has] = order[:sum(held)]
+        return dict(s, past=_ints(past), new=_ints(new), table=table, free=order[sum(held):].contiguous(), page=page, tokens=sum(new))
+    if c["op"] in ("append", "attend"):
+        io, heads, page, d = DTYPES[c["io"]], c["kv_heads"], c["page"], c["d"]
+    if c["op"] == "append":
+        T = c["tokens"]
+        pages = _pages(T, page) + 3
+        # the requests' pages lie anywhere in the cache
+        table = torch.randperm(pages, generator=gen, device="cuda")
+        at = torch.arange(T, device="cuda")
+        slots = table[at // page] * page + at % page
+        cache = dict(k=torch.zeros(pages, heads, page, d // 2, dtype=torch.uint8, device="cuda"), k_scale=torch.zeros(pages, heads, page, d // GROUP, dtype=torch.uint8, device="cuda"))
+        cache.update(v=cache["k"].clone(), v_scale=cache["k_scale"].clone())
+        # keys have a few channels far larger than the others
+        loud = 1 + 7 * (torch.rand(heads, d, generator=gen, device="cuda") < 0.03)
+        return dict(s, k=(normal(T, heads, d) * loud).to(io), v=normal(T, heads, d, dtype=io), slots=slots, cache=cache)
+    if c["op"] == "attend":
+        total, new = _attend_lengths(c)
+        need = [_pages(t, page) for t in total]
+        order = torch.randperm(sum(need) + 1, generator=gen, device="cuda").to(torch.int32)
+        has = torch.arange(max(need), device="cuda") < _ints(need)[:, None]
+        table = torch.full((len(need), max(need)), -1, dtype=torch.int32, device="cuda")
+        table[has] = order[:sum(need)]
+        cache = {}
+        cache["k"], cache["k_scale"] = _cache_pair(gen, sum(need) + 1, page, heads, d)
+        cache["v"], cache["v_scale"] = _cache_pair(gen, sum(need) + 1, page, heads, d)
+        T = sum(new)
+        cu = [0]
+        for m in new:
+            cu.append(cu[-1] + m)
+        return dict(s, q=(1.5 * normal(T, c["heads"], d)).to(io), g=normal(T, c["heads"], d, dtype=io) if c["gate"] else None, cache=cache, table=table,
+                    total=_ints(total), cu=_ints(cu) if c["new"] > 1 else None, most_new=max(new), longest=max(total))
+    io, D = DTYPES[c["io"]], c["width"]
+    B, T = c["rows"], c.get("tokens", 1)
+    shape = (B, D) if c["op"] == "step" else (B, T, D)
+    # channels remember from a few tokens to some thousands; the fastest reach the floor
+    slow = torch.rand(D, generator=gen, device="cuda") * 9 - 9
+    s["log_alpha"] = -torch.exp(slow + 0.5 * normal(*shape))
+    s["x"] = normal(*shape, dtype=io)
+    s["g"] = normal(*shape, dtype=io) if c["gate"] else None
+    n = B
+    if c["op"] != "step":
+        n = c["requests"] or B
+        s["cu"] = _ints(_packed_offsets(c)) if c["requests"] else None
+    s["state"] = normal(n, D)
+    if c["op"] == "train":
+        s["d_out"], s["d_state"] = normal(*shape, dtype=io), normal(n, D)
+    return s
+
+
+# ---- plain forms ------------------------------------------------------------------------------
+
+def _quantize(x):
+    """(codes, scales): two 4-bit e2m1 values a byte, the even channel in the low half, and a biased exponent for each GROUP channels."""
+    y = x.float().reshape(*x.shape[:-1], -1, GROUP)
+    most = y.abs().amax(-1)
+    e = torch.frexp(most)[1] - 3                       # most / 2^e lies in [4, 8)
+    e = e + (torch.ldexp(most, -e) > 7)                # 6 is the largest value: up to 7 rounds to it, beyond the next scale is nearer
+    e = torch.where(most > 0, e, LOW).clamp(LOW, HIGH)
+    y = torch.ldexp(y, -e[..., None]).reshape(x.shape)
+    a = y.abs()
+    # halfway values go to the even code
+    code = ((a > 0.25).int() + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5)) + 8 * torch.signbit(y)
+    code = code.to(torch.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), (e + 127).to(torch.uint8)
+
+
+def _dequantize(codes, scales):
+    value = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device=codes.device)
+    x = torch.stack([value[(codes & 15).long()], value[(codes >> 4).long()]], -1).reshape(*codes.shape[:-1], -1, GROUP)
+    return torch.ldexp(x, scales[..., None].int() - 127).reshape(*codes.shape[:-1], -1)
+
+
+def _plan(s):
+    past, new, page, table = s["past"].long(), s["new"].long(), s["page"], s["table"]
+    total = past + new
+    cu = torch.cat([torch.zeros_like(new[:1]), new.cumsum(0)])
+    held = (past + page - 1) // page
+    need = (total + page - 1) // page - held
+    first = need.cumsum(0) - need
+    j = torch.arange(table.shape[1], device=table.device)
+    at = first[:, None] + j - held[:, None]
+    fresh = (j >= held[:, None]) & (j < (held + need)[:, None])
+    table.copy_(torch.where(fresh, s["free"][at.clamp(0, s["free"].numel() - 1)], table))
+    t = torch.arange(s["tokens"], device=table.device)
+    r = torch.searchsorted(cu[1:], t, right=True)
+    pos = past[r] + t - cu[r]
+    slots = table[r, pos // page].long() * page + pos % page
+    return dict(cu=cu.int(), total=total.int(), slots=slots, table=table, taken=need.sum().int().reshape(1))
+
+
+def _append(s):
+    cache, slots = s["cache"], s["slots"]
+    page = cache["k"].shape[2]
+    p, o = slots // page, slots % page
+    back = {}
+    for n in ("k", "v"):
+        cache[n][p, :, o], cache[n + "_scale"][p, :, o] = _quantize(s[n])
+        back[n] = _dequantize(cache[n][p, :, o], cache[n + "_scale"][p, :, o]).to(s[n].dtype)
+    return back
+
+
+def _attend(s):
+    q, cache, total, table = s["q"], s["cache"], s["total"].long(), s["table"]
+    T, Hq, d = q.shape
+    n, L, most = len(total), s["longest"], s["most_new"]
+    heads, page = cache["k"].shape[1:3]
+    at = table[:, :_pages(L, page)].clamp(min=0).long()
+
+    def gathered(name):   # [n, heads, L, d]
+        x = _dequantize(cache[name][at], cache[name + "_scale"][at])
+        return x.transpose(1, 2).reshape(n, heads, -1, d)[:, :, :L]
+
+    cu = s["cu"].long() if s["cu"] is not None else torch.arange(n + 1, device=q.device)
+    new = cu[1:] - cu[:-1]
+    i = torch.arange(most, device=q.device)
+    row = (cu[:-1, None] + i).clamp(max=T - 1)                    # [n, most]
+    rows = q.float()[row].reshape(n, most, heads, -1, d).permute(0, 2, 3, 1, 4).reshape(n, heads, -1, d)
+    scores = torch.matmul(rows, gathered("k").transpose(2, 3).contiguous()) / math.sqrt(d)
+    scores = scores.view(n, heads, Hq // heads, most, L)
+    seen = torch.arange(L, device=q.device) <= (total - new)[:, None, None] + i[:, None]   # [n, most, L]
+    scores = scores.masked_fill(~seen[:, None, None], -math.inf)
+    p = torch.exp(scores - scores.amax(-1, keepdim=True))
+    p = (p / p.sum(-1, keepdim=True)).view(n, heads, -1, L)
+    o = torch.matmul(p, gathered("v")).view(n, heads, -1, most, d).permute(0, 3, 1, 2, 4).reshape(n, most, Hq, d)
+    out = o[i < new[:, None]]                                     # packed again, in order
+    if s["g"] is not None:
+        out = out / (1 + torch.exp(-s["g"].float()))
+    return out.to(q.dtype)
+
+
+def _scan(a, x):
+    """h_t = a_t h_(t-1) + x_t along the second axis, h_(-1) = 0, by doubling the stretch that each h_t covers."""
+    step = 1
+    while step < x.shape[1]:
+        x = torch.cat([x[:, :step], x[:, step:] + a[:, step:] * x[:, :-step]], 1)
+        a = torch.cat([a[:, :step], a[:, step:] * a[:, :-step]], 1)
+        step *= 2
+    return x
+
+
+def _starts(s):
+    """(row, token) of the first and the last token of each sequence that has any, and which sequences these are."""
+    B, T = s["x"].shape[:2]
+    if s["cu"] is None:
+        row = torch.arange(B, device="cuda")
+        return row, torch.zeros_like(row), torch.full_like(row, T - 1), row
+    cu = s["cu"].long()
+    seq = torch.nonzero(cu[1:] > cu[:-1])[:, 0]
+    return torch.zeros_like(seq), cu[seq], cu[seq + 1] - 1, seq
+
+
+def _forward(s):
+    # in 64 bits: channels that remember thousands of tokens multiply as many factors next to 1, and in 32 bits lose 3e-5
+    a = torch.exp(s["log_alpha"].double().clamp(min=FLOOR))
+    x = s["x"].double()
+    row, first, last, seq = _starts(s)
+    x = x.index_put((row, first), a[row, first] * s["state"][seq].double(), accumulate=True)
+    cut = a.index_put((row, first), torch.zeros((), dtype=a.dtype, device="cuda"))     # a sequence takes nothing from the one before it
+    h = _scan(cut, x)
+    state = s["state"].clone()
+    state[seq] = h[row, last].float()
+    return a, cut, h, state
+
+
+def _gate(g):
+    return 1 / (1 + torch.exp(-g.float())) if g is not None else 1.0
+
+
+def _recurrence(s):
+    _, _, h, state = _forward(s)
+    return dict(out=(h * _gate(s["g"])).to(s["x"].dtype), state=state)
+
+
+def _train(s):
+    a, cut, h, state = _forward(s)
+    io, sig, d_out = s["x"].dtype, _gate(s["g"]), s["d_out"].float()
+    got = dict(out=(h * sig).to(io), state=state)
+    row, first, last, seq = _starts(s)
+    d = (d_out * sig).double().index_put((row, last), s["d_state"][seq].double(), accumulate=True)
+    # dh_t = d_t + a_(t+1) dh_(t+1): the same scan from the end
+    after = torch.cat([cut[:, 1:], torch.zeros_like(cut[:, :1])], 1)
+    dh = _scan(after.flip(1), d.flip(1)).flip(1)
+    before = torch.cat([torch.zeros_like(h[:, :1]), h[:, :-1]], 1).index_put((row, first), s["state"][seq].double())
+    got["dx"] = dh.to(io)
+    got["dlog_alpha"] = torch.where(s["log_alpha"] > FLOOR, dh * a * before, 0).float()
+    if s["g"] is not None:
+        got["dg"] = (d_out * h * sig * (1 - sig)).to(io)
+    got["dstate"] = s["d_state"].clone()
+    got["dstate"][seq] = (a[row, first] * dh[row, first]).float()
+    return got
+
+
+def _step(s):
+    h = torch.exp(s["log_alpha"].clamp(min=FLOOR)) * s["state"] + s["x"].float()
+    s["state"].copy_(h)
+    return dict(out=(h * _gate(s["g"])).to(s["x"].dtype), state=s["state"])
+
+
+def _own(s):
+    import gated_delta_rule_91_amd as kda
+    op = s["op"]
+    if op == "plan":
+        cu, total, slots, taken = kda.plan_requests(s["past"], s["new"], s["table"], s["free"], s["page"], s["tokens"])
+        return dict(cu=cu, total=total, slots=slots, table=s["table"], taken=taken)
+    if op in ("append", "attend"):
+        cache = kda.Cache4(**s["cache"])
+    if op == "append":
+        kda.cache4_append(cache, s["k"], s["v"], s["slots"])
+        k, v = kda.cache4_read(cache, s["slots"], s["k"].dtype)
+        return dict(k=k, v=v)
+    if op == "attend":
+        return kda.cache4_attention(s["q"], cache, s["table"], s["total"], cu_seqlens=s["cu"], g=s["g"], max_q=s["most_new"], max_len=s["longest"])
+    if op == "step":
+        out = kda.recurrence_step(s["x"], s["log_alpha"], s["state"], FLOOR, g=s["g"])
+        return dict(out=out, state=s["state"])
+    if op == "recurrence":
+        out, state = kda.recurrence_prefill(s["x"], s["log_alpha"], FLOOR, g=s["g"], state_in=s["state"], cu_seqlens=s["cu"])
+        return dict(out=out, state=state)
+    out, state, kept = kda.recurrence_prefill_for_backward(s["x"], s["log_alpha"], FLOOR, g=s["g"], state_in=s["state"], cu_seqlens=s["cu"])
+    r = kda.recurrence_backward(s["x"], s["log_alpha"], FLOOR, kept, g=s["g"], d_out=s["d_out"], d_state=s["d_state"], cu_seqlens=s["cu"])
+    got = dict(out=out, state=state, dx=r["dx"], dlog_alpha=r["dlog_alpha"], dstate=r["dstate0"])
+    if s["g"] is not None:
+        got["dg"] = r["dg"]
+    return got
+
+
+PLAIN = dict(plan=_plan, append=_append, attend=_attend, recurrence=_recurrence, train=_train, step=_step)
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return PLAIN[state["op"]](state)
+
+
+# ---- what a pass cannot do without ------------------------------------------------------------
+
+def work(case):
+    c = case
+    if c["op"] == "plan":
+        past, new = _plan_lengths(c)
+        fresh = sum(_pages(p + m, c["page"]) - _pages(p, c["page"]) for p, m in zip(past, new))
+        # lengths, offsets and totals; free pages to the table; one held page of each request; slots
+        return dict(bytes=c["requests"] * (8 + 8 + 4) + fresh * 8 + sum(new) * 8, flops=4 * sum(new))
+    if c["op"] in ("append", "attend"):
+        size, heads, d = DTYPES[c["io"]].itemsize, c["kv_heads"], c["d"]
+        row = 2 * heads * (d // 2 + d // GROUP)     # a token's codes and scales, keys and values
+    if c["op"] == "append":
+        return dict(bytes=c["tokens"] * (2 * row + 4 * heads * d * size + 16), flops=c["tokens"] * 2 * heads * d * 12)
+    if c["op"] == "attend":
+        total, new = _attend_lengths(c)
+        pairs = sum(m * (2 * t - m + 1) // 2 for t, m in zip(total, new))
+        arrays = 3 if c["gate"] else 2
+        return dict(bytes=sum(total) * row + sum(new) * c["heads"] * d * size * arrays + sum(_pages(t, c["page"]) for t in total) * 4, flops=4 * pairs * c["heads"] * d)
+    size, n = DTYPES[c["io"]].itemsize, c["rows"] * c.get("tokens", 1) * c["width"]
+    states = (c.get("requests", 0) or c["rows"]) * c["width"] * 4
+    gate = 1 if c["gate"] else 0
+    if c["op"] == "train":
+        # x, log_alpha, g, d_out read; out, dx, dlog_alpha, dg written; both states and both gradients of states
+        return dict(bytes=n * (size * (4 + 2 * gate) + 8) + 4 * states, flops=n * 20)
+    return dict(bytes=n * (size * (2 + gate) + 4) + 2 * states, flops=n * 8)
+
+
+# ---- the definitions in 64 bits ---------------------------------------------------------------
+
+def _exact_plan(c, seed):
+    s = prepare(c, seed)
+    page, free = c["page"], s["free"].tolist()
+    table, cu, total, slots, taken = s["table"].tolist(), [0], [], [], 0
+    for row, p, m in zip(table, *_plan_lengths(c)):
+        for at in range(p, p + m):
+            if at % page == 0:          # the first token of a page takes it off the list
+                row[at // page] = free[taken]
+                taken += 1
+            slots.append(row[at // page] * page + at % page)
+        cu.append(len(slots))
+        total.append(p + m)
+    return dict(cu=_ints(cu), total=_ints(total), slots=_ints(slots, torch.int64), table=_ints(table), taken=_ints([taken]))
+
+
+def _exact_quantized(x):
+    """The values that 4 bits hold: for each, the nearest of the sixteen, the even one where two are as near."""
+    y = x.double().reshape(-1, GROUP)
+    most = y.abs().amax(1, keepdim=True)
+    e = torch.floor(torch.log2(most)) - 2
+    e = torch.where(most * torch.pow(2.0, -e) > 7, e + 1, e).clamp(LOW, HIGH)
+    unit = torch.pow(torch.tensor(2.0, dtype=torch.float64, device=x.device), e)
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=x.device)
+    best, far = torch.zeros_like(y), torch.full_like(y, math.inf)
+    for k in (0, 2, 4, 6, 1, 3, 5, 7):     # even codes first: an odd one has to be nearer
+        off = (y.abs() / unit - grid[k]).abs()
+        best, far = torch.where(off < far, grid[k], best), torch.minimum(off, far)
+    return (best * unit * torch.sign(y)).reshape(x.shape)
+
+
+def _exact_values(codes, scales):
+    half = torch.stack([codes % 16, codes // 16], -1).reshape(*codes.shape[:-1], -1).double()
+    size, sign = half % 8, 1 - 2 * (half >= 8).double()
+    # 0 and 1/2, then (2 + m) 2^(x - 2) for exponent x and mantissa m
+    value = torch.where(size < 2, size / 2, (2 + size % 2) * torch.pow(2.0, torch.floor(size / 2) - 2))
+    unit = torch.pow(torch.tensor(2.0, dtype=torch.float64, device=codes.device), scales.double() - 127)
+    return sign * value * unit.repeat_interleave(GROUP, -1)
+
+
+def _exact_attend(c, seed):
+    s = prepare(c, seed)
+    page, heads, d = c["page"], c["kv_heads"], c["d"]
+    outs, at = [], 0
+    for r, (t, m) in enumerate(zip(*_attend_lengths(c))):
+        pages = s["table"][r, :_pages(t, page)].long()
+
+        def rows(n):
+            return _exact_values(s["cache"][n][pages], s["cache"][n + "_scale"][pages]).transpose(1, 2).reshape(-1, heads, d)[:t]
+
+        k, v, q = rows("k"), rows("v"), s["q"][at:at + m].double()
+        out = torch.empty_like(q)
+        hidden = torch.arange(t, device="cuda") > (t - m + torch.arange(m, device="cuda"))[:, None]
+        for h in range(c["heads"]):
+            kv = h * heads // c["heads"]
+            w = torch.softmax(((q[:, h] @ k[:, kv].T) / d ** 0.5).masked_fill(hidden, -math.inf), -1)
+            out[:, h] = w @ v[:, kv]
+        outs.append(out)
+        at += m
+    out = torch.cat(outs)
+    return out * torch.sigmoid(s["g"].double()) if c["gate"] else out
+
+
+def _exact_recurrence(c, seed):
+    s = prepare(c, seed)
+    one = c["op"] == "step"
+    x, la = (s[n].double().unsqueeze(1) if one else s[n].double() for n in ("x", "log_alpha"))
+    cu = None if one or s["cu"] is None else s["cu"].tolist()
+    spans = [(0, x.shape[1])] if cu is None else list(zip(cu, cu[1:]))
+    a = torch.maximum(la, torch.tensor(FLOOR, dtype=torch.float64, device="cuda")).exp()
+    h, state = torch.zeros_like(x), s["state"].double().clone()
+    before = torch.zeros_like(x)
+    for r, (b, e) in enumerate(spans):
+        at = state if cu is None else state[r:r + 1]
+        now = at.clone()
+        for t in range(b, e):
+            before[:, t] = now
+            now = torch.addcmul(x[:, t], a[:, t], now)
+            h[:, t] = now
+        at.copy_(now)
+    g = None if s["g"] is None else (s["g"].double().unsqueeze(1) if one else s["g"].double())
+    sig = torch.sigmoid(g) if g is not None else torch.ones_like(h)
+    got = dict(out=h * sig, state=state)
+    if one:
+        return dict(out=got["out"].squeeze(1), state=state)
+    if c["op"] == "train":
+        d_out, dstate = s["d_out"].double(), s["d_state"].double().clone()
+        d, dh = d_out * sig, torch.zeros_like(h)
+        for r, (b, e) in enumerate(spans):
+            at = dstate if cu is None else dstate[r:r + 1]
+            now = at.clone()
+            for t in range(e - 1, b - 1, -1):
+                dh[:, t] = d[:, t] + now
+                now = a[:, t] * dh[:, t]
+            at.copy_(now)
+        got.update(dx=dh, dlog_alpha=dh * a * before * (la > FLOOR), dstate=dstate)
+        if g is not None:
+            got["dg"] = d * h * (1 - sig)
+    return got
+
+
+def exact(case, seed):
+    if case["op"] == "plan":
+        return _exact_plan(case, seed)
+    if case["op"] == "append":
+        s = prepare(case, seed)
+        return dict(k=_exact_quantized(s["k"]), v=_exact_quantized(s["v"]))
+    if case["op"] == "attend":
+        return _exact_attend(case, seed)
+    return _exact_recurrence(case, seed)
