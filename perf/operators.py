@@ -381,7 +381,7 @@ def _own(s):
         out, state = kda.recurrence_prefill(s["x"], s["log_alpha"], FLOOR, g=s["g"], state_in=s["state"], cu_seqlens=s["cu"])
         return dict(out=out, state=state)
     out, state, kept = kda.recurrence_prefill_for_backward(s["x"], s["log_alpha"], FLOOR, g=s["g"], state_in=s["state"], cu_seqlens=s["cu"])
-    r = kda.recurrence_backward(s["x"], s["log_alpha"], FLOOR, kept, g=s["g"], d_out=s["d_out"], d_state=s["d_state"], cu_seqlens=s["cu"])
+    r = kda.recurrence_backward(s["x"], s["log_alpha"], FLOOR, kept, g=s["g"], state_in=s["state"], d_out=s["d_out"], d_state=s["d_state"], cu_seqlens=s["cu"])
     got = dict(out=out, state=state, dx=r["dx"], dlog_alpha=r["dlog_alpha"], dstate=r["dstate0"])
     if s["g"] is not None:
         got["dg"] = r["dg"]
