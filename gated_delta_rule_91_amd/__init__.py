@@ -17,6 +17,11 @@ prefill_autograd (a torch.autograd.Function over the split training pair).
 prefill_pipelined calls kda_prefill_pipelined (chunk ranges, the next range's
 cards prepared on a second stream during the current range's scan);
 prefill_noalloc calls kda_prefill_noalloc, which needs no workspace.
+
+The operators beside KDA in a hybrid stack (``include/kda_hybrid.h``,
+``hybrid.py``): plan_requests; Cache4 with cache4_append, cache4_read and
+cache4_attention; recurrence_prefill, recurrence_step and, for training,
+recurrence_prefill_for_backward, recurrence_backward and recurrence_autograd.
 """
 from __future__ import annotations
 
@@ -736,3 +741,7 @@ def to_device(inp, device="cuda"):
              log_alpha=torch.from_numpy(inp.log_alpha).to(device), beta=torch.from_numpy(inp.beta).to(device))
     d["state0"] = None if inp.state0 is None else torch.from_numpy(inp.state0).to(device)
     return d
+
+
+# the operators beside KDA in a hybrid stack (include/kda_hybrid.h)
+from .hybrid import *  # noqa: E402,F401,F403

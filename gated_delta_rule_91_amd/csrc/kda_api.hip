@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_checks.hpp"
 #include "kda_internal.hpp"
 
 using namespace kda;
@@ -43,13 +44,8 @@ kda_status scratch_address(void** addr) {
     return KDA_OK;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// ptr must be non-null and 16-byte aligned when the array is non-empty
-bool ok_ptr(const void* p, bool nonempty) { return !nonempty || (p != nullptr && aligned16(p)); }
 // beta is only read one fp32 at a time: natural alignment suffices
-bool ok_beta(const void* p, bool nonempty) { return !nonempty || (p != nullptr && ((uintptr_t)p & 3u) == 0); }
-bool ok_opt_ptr(const void* p) { return p == nullptr || aligned16(p); }
+bool ok_beta(const void* p, bool nonempty) { return ok_elem(p, nonempty, 4); }
 
 kda_status check_floor(float f, int chunk) {
     // the floor keeps exp(chunk * |floor|) -- the largest decay factor folded
@@ -75,13 +71,6 @@ kda_status check_problem(const kda_problem* p) {
 }
 
 int64_t n_chunks(const kda_problem* p) { return (p->seqlen + p->chunk - 1) / p->chunk; }
-
-kda_status device_ready() {
-    int dev = 0;
-    return hipGetDevice(&dev) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
-}
-
-kda_status hip_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 // Packed variable-length batches: chunk offsets first, then each chunk's
 // sequence index, then the cards.

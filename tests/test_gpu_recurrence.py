@@ -1,0 +1,244 @@
+"""The gated linear recurrence on an MI355X against a plain 64-bit form.
+
+Tolerance, from the roundings that the kernel may make.  A step rounds twice
+(2 u, u = 2^-24), expm1 is off by 4 u of itself, and each rounding fades as the
+state does: a channel that remembers N tokens (1 / (1 - a), at most T) sums
+(2 N + 8) of them, and joining tiles adds a few a tile, below one a token.  So
+states are within (3 N + 16) u max |h|, and in reverse dh within (3 N + 16) u
+max |dh|; products add the errors of their factors; a gate is off by 8 u; an
+output rounds once, u of its type."""
+import math
+
+import pytest
+
+import _hybrid_ref as ref
+
+torch = pytest.importorskip("torch")
+import gated_delta_rule_91_amd as kda
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+UO = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+U = 2.0 ** -24
+FLOOR = -0.5
+
+
+def made(B, T, D, io, n=None, gate=True, seed=0, slowest=-7.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed + B * 7 + T * 3 + D)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    slow = torch.rand(D, generator=gen, device="cuda") * (slowest - 1) + 1     # up to e: beyond the floor
+    la = -torch.exp(slow + 0.3 * r(B, T, D))
+    x, g, d_out = (r(B, T, D).to(DT[io]) for _ in range(3))
+    n = B if n is None else n
+    return dict(x=x, la=la, g=g if gate else None, s0=r(n, D), d_out=d_out, d_state=r(n, D))
+
+
+def bounds(i, want, io):
+    """Per channel tolerances of h and dh, from the documented rule."""
+    T = i["x"].shape[1]
+    least = -torch.clamp(torch.nan_to_num(i["la"].double(), nan=-math.inf), min=FLOOR).cpu()
+    mem = torch.clamp(1 / torch.clamp(1 - torch.exp(-least.amin((0, 1))), min=1e-9), max=T) if T else torch.zeros(least.shape[-1])
+    return (3 * mem + 16) * U
+
+
+def within(got, want, tol, label):
+    got, want = got.cpu().double(), want
+    keep = ~torch.isnan(want)
+    worst = ((got - want).abs() / (tol + 1e-30))[keep]
+    assert worst.numel() == 0 or float(worst.max()) <= 1, (label, float(worst.max()))
+
+
+def check(i, io, cu=None, backward=True):
+    cut = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    cpu = {k: None if v is None else v.cpu() for k, v in i.items()}
+    want = ref.recurrence(cpu["x"], cpu["la"], FLOOR, cpu["g"], cpu["s0"], cu, cpu["d_out"], cpu["d_state"])
+    k = bounds(i, want, io)
+    top = lambda x: torch.nan_to_num(x).abs().flatten(0, -2).amax(0) if x.numel() else torch.zeros(x.shape[-1], dtype=torch.float64)
+    s0 = torch.zeros(1, i["x"].shape[2], dtype=torch.float64) if cpu["s0"] is None else cpu["s0"].double()
+    th = k * torch.maximum(top(want["h"]), top(s0))
+    out = torch.full_like(i["x"], 55.0)
+    got, state = kda.recurrence_prefill(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], cu_seqlens=cut, out=out)
+    torch.cuda.synchronize()
+    left = torch.isnan(want["out"])
+    assert (out.cpu()[left] == 55.0).all()                # tokens of no sequence
+    within(out, want["out"], th + 8 * U * want["out"].abs() + UO[io] * want["out"].abs(), "out")
+    within(state, want["state"], th, "state")
+    if not backward:
+        return
+    out2, state2, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], cu_seqlens=cut)
+    torch.cuda.synchronize()
+    assert torch.equal(out2.cpu()[~left], out.cpu()[~left]) and torch.equal(state2, state)
+    ds = torch.zeros_like(s0) if cpu["d_state"] is None else cpu["d_state"].double()
+    td = k * torch.maximum(top(want["dx"]), top(ds))
+    a = torch.exp(torch.clamp(torch.nan_to_num(cpu["la"].double(), nan=-math.inf), min=FLOOR))
+    before = torch.maximum(top(want["h"]), top(s0))
+    for _ in range(2):                                    # the workspace serves a second call
+        r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, g=i["g"], state_in=i["s0"], cu_seqlens=cut,
+                                    d_out=i["d_out"], d_state=i["d_state"])
+        torch.cuda.synchronize()
+        within(r["dx"], want["dx"], td + UO[io] * want["dx"].abs(), "dx")
+        tl = a * (td * before + th * torch.maximum(top(want["dx"]), top(ds))) + 16 * U * want["dlog_alpha"].abs()
+        within(r["dlog_alpha"], want["dlog_alpha"], tl, "dlog_alpha")
+        within(r["dstate0"], want["dstate0"], td, "dstate0")
+        if i["g"] is not None:
+            d = torch.zeros_like(want["h"]) if cpu["d_out"] is None else cpu["d_out"].double()
+            # sigmoid and 1 - sigmoid are off by 4 u of 1 each
+            within(r["dg"], want["dg"], d.abs() * (th + 16 * U * want["h"].abs()) + UO[io] * want["dg"].abs(), "dg")
+        else:
+            assert r["dg"] is None
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("B,T,D", [(1, 1, 1), (2, 63, 5), (3, 64, 64), (1, 65, 129), (2, 255, 66), (1, 256, 128), (1, 257, 130),
+                                   (2, 1000, 34), (1, 2500, 257), (5, 7, 300)])
+def test_uniform(B, T, D, gate, io):
+    check(made(B, T, D, io, gate=gate), io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("cu,T,D", [([0, 5], 5, 3), ([0, 1, 2, 3], 3, 64), ([0, 64, 128], 128, 130), ([0, 0, 70, 70, 70, 300, 300], 300, 66),
+                                    ([0, 255, 256, 257, 513, 1400], 1400, 33), ([3, 10, 200], 260, 128),
+                                    ([0, 1300], 1300, 200), ([0, 0], 40, 8), ([2, 600, 600, 1025], 1030, 65)])
+def test_packed(cu, T, D, io):
+    check(made(1, T, D, io, n=len(cu) - 1), io, cu=cu)
+
+
+def test_packed_many_short_sequences():
+    gen = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 9, (400,), generator=gen).tolist()
+    cu = [0]
+    for m in lens:
+        cu.append(cu[-1] + m)
+    check(made(1, cu[-1], 70, "f32", n=400), "f32", cu=cu)
+
+
+def test_packed_equals_alone():
+    """A sequence gives the same in a batch as alone, to the tolerance of both (their tiles lie otherwise)."""
+    cu = [0, 300, 1100]
+    i = made(1, 1100, 64, "f32", n=2)
+    check(i, "f32", cu=cu)
+    for s in range(2):
+        j = {k: v[:, cu[s]:cu[s + 1]].contiguous() if v.dim() == 3 else v[s:s + 1].contiguous() for k, v in i.items()}
+        check(j, "f32")
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 4000, 64), (2, 700, 31)])
+def test_slow_channels(B, T, D):
+    """Channels that remember thousands of tokens."""
+    check(made(B, T, D, "f32", slowest=-10.0), "f32")
+
+
+def test_optional_arguments():
+    for name in ("s0", "d_out", "d_state"):
+        i = made(2, 300, 40, "f32")
+        i[name] = None
+        check(i, "f32")
+    i = made(2, 300, 40, "f32")
+    out, state = kda.recurrence_prefill(i["x"], i["la"], FLOOR, want_state=False)
+    assert state is None
+    _, _, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR)
+    assert kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, d_out=i["d_out"], want_dstate=False)["dstate0"] is None
+
+
+def test_no_tokens():
+    z = lambda *s: torch.zeros(*s, device="cuda")
+    s0 = torch.randn(3, 20, device="cuda")
+    for x, cu in ((z(3, 0, 20), None), (z(1, 0, 20), torch.zeros(4, dtype=torch.int32, device="cuda"))):
+        out, state, ws = kda.recurrence_prefill_for_backward(x, x, FLOOR, state_in=s0, cu_seqlens=cu)
+        r = kda.recurrence_backward(x, x, FLOOR, ws, state_in=s0, cu_seqlens=cu, d_state=2 * s0)
+        torch.cuda.synchronize()
+        assert torch.equal(state, s0) and torch.equal(r["dstate0"], 2 * s0)
+    out, state = kda.recurrence_prefill(z(0, 5, 20), z(0, 5, 20), FLOOR)
+    assert out.shape == (0, 5, 20) and state.shape == (0, 20)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, state = kda.recurrence_prefill(z(1, 5, 20), z(1, 5, 20), FLOOR, cu_seqlens=none, out=torch.full((1, 5, 20), 9.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert (out == 9).all() and state.shape == (0, 20)
+
+
+def test_floor_nan_and_infinities():
+    i = made(1, 600, 16, "f32")
+    i["la"][0, 10, 0] = math.nan                          # acts as the floor
+    i["la"][0, 300, 1] = -math.inf
+    i["la"][0, :, 2] = FLOOR                              # the floor binds: no gradient
+    check(i, "f32")
+    x, la = i["x"].clone(), i["la"]
+    x[0, 100, 3] = math.nan                               # stays in its channel, from its token on
+    x[0, 270, 4] = math.inf
+    out, state = kda.recurrence_prefill(x, la, FLOOR, state_in=i["s0"])
+    torch.cuda.synchronize()
+    bad = ~torch.isfinite(out.cpu()[0])
+    want = torch.zeros_like(bad)
+    want[100:, 3] = True
+    want[270:, 4] = True
+    assert torch.equal(bad, want)
+    # no floor: a decay to nothing forgets
+    la = la.clone()
+    la[0, 50] = -math.inf
+    out, state = kda.recurrence_prefill(i["x"], la, -math.inf)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0, 50], i["x"][0, 50])
+
+
+def test_state_in_place():
+    for B, T in ((3, 40), (2, 900)):
+        i = made(B, T, 50, "f32")
+        out, state = kda.recurrence_prefill(i["x"], i["la"], FLOOR, state_in=i["s0"])
+        s = i["s0"].clone()
+        out2, same = kda.recurrence_prefill(i["x"], i["la"], FLOOR, state_in=s, state_out=s)
+        torch.cuda.synchronize()
+        assert same is s and torch.equal(s, state) and torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D", [(1, 1), (3, 77), (7, 128), (300, 96)])
+def test_step(N, D, io):
+    i = made(N, 1, D, io)
+    want = ref.recurrence(i["x"].cpu(), i["la"].cpu(), FLOOR, i["g"].cpu(), i["s0"].cpu())
+    state = i["s0"].clone()
+    out = kda.recurrence_step(i["x"][:, 0].contiguous(), i["la"][:, 0].contiguous(), state, FLOOR, g=i["g"][:, 0].contiguous())
+    torch.cuda.synchronize()
+    size = want["h"][:, 0].abs() + i["s0"].cpu().double().abs() + i["x"].cpu().double()[:, 0].abs()
+    within(state, want["state"], 8 * U * size, "state")
+    within(out, want["out"][:, 0], 16 * U * size + UO[io] * want["out"][:, 0].abs(), "out")
+
+
+def test_gradients_against_differences():
+    """Central differences of the 64-bit form, for a few entries of every input."""
+    i = made(1, 300, 6, "f32", n=2)
+    cu = [0, 120, 300]
+    leaves = {k: i[k].clone().requires_grad_(True) for k in ("x", "la", "g", "s0")}
+    out, state = kda.recurrence_autograd(leaves["x"], leaves["la"], FLOOR, g=leaves["g"], state_in=leaves["s0"],
+                                         cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    ((out * i["d_out"]).sum() + (state * i["d_state"]).sum()).backward()
+    torch.cuda.synchronize()
+    cpu = {k: v.cpu().double() for k, v in i.items()}
+
+    def loss(**kw):
+        a = {**cpu, **kw}
+        r = ref.recurrence(a["x"], a["la"], FLOOR, a["g"], a["s0"], cu)
+        return float((r["out"] * cpu["d_out"]).sum() + (r["state"] * cpu["d_state"]).sum())
+
+    eps = 1e-5
+    for k, leaf in leaves.items():
+        for at in ((0, 0, 1), (0, 119, 2), (0, 120, 3), (0, 257, 4)) if leaf.dim() == 3 else ((0, 2), (1, 5)):
+            if k == "la" and abs(float(cpu[k][at]) - FLOOR) < 1e-3:
+                continue
+            up, down = cpu[k].clone(), cpu[k].clone()
+            up[at] += eps
+            down[at] -= eps
+            diff = (loss(**{k: up}) - loss(**{k: down})) / (2 * eps)
+            # differences of second order: eps^2 times third derivatives, and 1e-11 of the loss's rounding over eps
+            assert abs(float(leaf.grad[at]) - diff) <= 1e-4 * max(1.0, abs(diff)), (k, at)
+
+
+def test_autograd_of_outputs_that_are_not_used():
+    i = made(2, 100, 10, "bf16")
+    x = i["x"].clone().requires_grad_(True)
+    out, state = kda.recurrence_autograd(x, i["la"], FLOOR)
+    state.sum().backward()
+    _, _, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR)
+    r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, d_state=torch.ones(2, 10, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, r["dx"])
