@@ -8,11 +8,33 @@
 //   dx_t = dh_t,  dlog_alpha_t = dh_t e^lambda_t h_(t-1)    (0 where the floor binds)
 //   dg_t = d_out_t h_t sigmoid'(g_t),  d_state_in = e^lambda_0 dh_0
 //
+// Both directions are bound by HBM (10 bytes an element forward, 20 in the
+// training pass's backward, with a gate in bf16), so each reads its inputs
+// once: a workgroup holds a tile of kTile tokens x 64 VEC channels in
+// registers while the state that enters it is found.
+//  * A wave runs its stretch of the tile from nothing: (A, H), the product of
+//    its decays and the state it ends with.  A stretch is the map
+//    h -> A h + H; maps are joined through LDS.
+//  * Every tile publishes its map, then its inclusive state h_out = A h_in + H
+//    once h_in is known.  h_in is the last tile's h_out, or follows from an
+//    earlier tile's h_out and the maps between, taken in the order of time:
+//    the same operations whichever tile was ready, so results do not depend
+//    on timing.  A look-back window of kWindow tiles lets the states run ahead
+//    that many tiles per exchange between workgroups instead of one.
+//  * The waves then run again from their true states and write the outputs.
+// A sequence's first token starts its state anew, which makes the maps of its
+// tile constant (no h_in): that is all that packed batches add, and uniform
+// rows are sequences of their own.  The backward is the same in the other
+// direction, with the states that enter the tiles kept by the forward call.
+//
+// Tiles are taken in the order of time off a counter, so a tile only ever
+// waits for tiles that running workgroups have taken before it.
+//
 // A channel that remembers n tokens multiplies about n factors next to 1, so
-// where |lambda| <= 1/4 a step is taken as h + (expm1(lambda) h + x): rounding
-// e^lambda itself would cost half a step of fp32 per token, always the same
-// way for a constant lambda.  Faster decays take e^lambda h + x, which leaves
-// nothing of a large h that is forgotten.
+// where |lambda| <= 1/16 a step is taken as h + (expm1(lambda) h + x):
+// rounding e^lambda itself would cost half a step of fp32 per token, always
+// the same way for a constant lambda.  Faster decays take e^lambda h + x, which
+// leaves nothing of a large h that is forgotten.
 #include "kda_common.hpp"
 #include "kda_hybrid_internal.hpp"
 
@@ -20,102 +42,516 @@ namespace kda {
 
 namespace {
 
-constexpr int kTile = 64;     // tokens between kept states
+constexpr int kTile = 128;        // tokens a workgroup holds
+constexpr int kWindow = 8;        // tiles that a look-back reads at once
+// Polls after which a wait gives up with NaN: a tenth of a second, where a tile takes
+// microseconds.  Only a workspace that another call is using can get there.
+constexpr int kMaxPolls = 1 << 17;
+
+// The look-back words of one channel of a tile: the state in the low half,
+// above it 0 (nothing yet), kFinal (the state is the tile's last one), or the
+// product of the decays with its sign bit set (the tile's map).
+constexpr uint32_t kFinal = 0xffffffffu;
+
+template <typename E, int N> struct VecOf { typedef E type __attribute__((ext_vector_type(N))); };
+template <typename E> struct VecOf<E, 1> { typedef E type; };
+template <int N, typename V> __device__ __forceinline__ float lane_of(V v, int i) {
+    if constexpr (N == 1) return to_f32(v);
+    else return to_f32(v[i]);
+}
+template <typename E, int N>
+__device__ __forceinline__ void put(E* p, const float (&x)[N]) {
+    if constexpr (N == 1) {
+        *p = from_f32<E>(x[0]);
+    } else {
+        typename VecOf<E, N>::type v;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = from_f32<E>(x[i]);
+        *reinterpret_cast<typename VecOf<E, N>::type*>(p) = v;
+    }
+}
 
 // One token's decay, of lambda = max(log_alpha, floor): `c` is expm1(lambda)
-// where `slow` and e^lambda elsewhere.  expm1 is the Taylor series to the 8th
-// power (the rest is below 2^-31 of the value), e^lambda the hardware exp2.
+// where `slow` and e^lambda elsewhere.  expm1 is the Taylor series to the 5th
+// power (the rest is below 2^-29 of the value), e^lambda the hardware exp2.
 struct Decay {
     float c;
     bool slow;
     __device__ __forceinline__ explicit Decay(float x) {
-        float p = 1.f / 40320.f;
-        p = fmaf(p, x, 1.f / 5040.f);
-        p = fmaf(p, x, 1.f / 720.f);
-        p = fmaf(p, x, 1.f / 120.f);
+        float p = 1.f / 120.f;
         p = fmaf(p, x, 1.f / 24.f);
         p = fmaf(p, x, 1.f / 6.f);
         p = fmaf(p, x, 0.5f);
         p = fmaf(p * x, x, x);
-        slow = fabsf(x) <= 0.25f;
+        slow = fabsf(x) <= 0.0625f;
         c = slow ? p : __builtin_amdgcn_exp2f(1.4426950408889634f * x);
     }
+    __device__ __forceinline__ Decay(float c_, bool slow_) : c(c_), slow(slow_) {}
     // e^lambda h, and e^lambda h + x
     __device__ __forceinline__ float times(float h) const { return fmaf(c, h, slow ? h : 0.f); }
     __device__ __forceinline__ float step(float h, float x) const { return fmaf(c, h, x) + (slow ? h : 0.f); }
 };
 
-struct Span {
-    int64_t row, first, end;   // tokens [first, end) of batch row `row`; states at index blockIdx.y
+__device__ __forceinline__ float product_of(float sum) { return __builtin_amdgcn_exp2f(1.4426950408889634f * sum); }
+
+// The sequence of a token, walked along the tokens of one wave (all of it the
+// same in every lane).
+struct Walk {
+    const int32_t* cu;      // null: one sequence, the whole row
+    int n, T;
+    int s, first, end;      // sequence s holds tokens [first, end)
+    __device__ __forceinline__ void bounds() {
+        int64_t b, e;
+        seq_bounds(cu, s, T, b, e);
+        first = (int)b; end = (int)e;
+    }
+    // at token t or the next one that has a sequence
+    __device__ __forceinline__ Walk(const RecurrenceArgs& a, int row, int t)
+        : cu(a.cu_seqlens), n((int)a.n_seq), T((int)a.T), s(row), first(0), end((int)a.T) {
+        if (!cu) return;
+        int lo = 0, hi = n;               // the last sequence that begins at or before t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        s = lo;
+        bounds();
+    }
+    __device__ __forceinline__ void go_to(int s_) {
+        if (s == s_) return;
+        s = s_;
+        bounds();
+    }
+    // Whether a sequence holds token t, for t going up, and going down.
+    __device__ __forceinline__ bool up(int t) {
+        if (cu) while (t >= end && s + 1 < n) { ++s; bounds(); }
+        return t >= first && t < end;
+    }
+    __device__ __forceinline__ bool down(int t) {
+        if (cu) while (t < first && s > 0) { --s; bounds(); }
+        return t >= first && t < end;
+    }
 };
-__device__ __forceinline__ Span span_of(const RecurrenceArgs& a) {
-    Span s;
-    if (a.cu_seqlens) {
-        s.row = 0;
-        seq_bounds(a.cu_seqlens, blockIdx.y, a.T, s.first, s.end);
-    } else {
-        s.row = blockIdx.y; s.first = 0; s.end = a.T;
-    }
-    return s;
+
+struct TileGrid {
+    int64_t tiles;          // per row
+    int64_t lanes;          // rows x channel blocks: tiles of one time
+    int blocks;             // channel blocks of a row
+    __host__ __device__ int64_t total() const { return tiles * lanes; }
+};
+
+__device__ __forceinline__ uint64_t word(uint32_t high, float h) { return (uint64_t)high << 32 | __float_as_uint(h); }
+
+// One channel's part of a tile's map, as published.
+__device__ __forceinline__ uint64_t map_word(float A, float H) {
+    return word(A != A ? 0xffc00000u : __float_as_uint(A) | 0x80000000u, H);
 }
 
-__device__ __forceinline__ int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
-
-template <typename E>
-__global__ __launch_bounds__(64) void kda_recurrence_kernel(RecurrenceArgs a) {
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (c >= a.D) return;
-    const Span sp = span_of(a);
-    float h = a.state_in ? a.state_in[(int64_t)blockIdx.y * a.D + c] : 0.f;
-    float* keep = reinterpret_cast<float*>(a.ws);
-    for (int64_t t = sp.first; t < sp.end; ++t) {
-        const int64_t i = (sp.row * a.T + t) * a.D + c;
-        if (a.keep && t % kTile == 0) keep[(sp.row * tiles_of(a.T) + t / kTile) * a.D + c] = h;
-        h = Decay(fmaxf(a.log_alpha[i], a.floor_)).step(h, to_f32(reinterpret_cast<const E*>(a.x)[i]));
-        const float s = a.g ? sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i])) : 1.f;
-        reinterpret_cast<E*>(a.out)[i] = from_f32<E>(h * s);
-    }
-    if (a.state_out) a.state_out[(int64_t)blockIdx.y * a.D + c] = h;
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t w) {
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <typename E>
-__global__ __launch_bounds__(64) void kda_recurrence_backward_kernel(RecurrenceArgs a) {
-    __shared__ float before[kTile][64];
-    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (c >= a.D) return;
-    const Span sp = span_of(a);
-    const float* keep = reinterpret_cast<const float*>(a.ws);
-    float carry = a.d_state ? a.d_state[(int64_t)blockIdx.y * a.D + c] : 0.f;
-    for (int64_t end = sp.end; end > sp.first;) {
-        const int64_t tile = (end - 1) / kTile;
-        const int64_t lo = tile * kTile > sp.first ? tile * kTile : sp.first;
-        float h = lo == sp.first ? (a.state_in ? a.state_in[(int64_t)blockIdx.y * a.D + c] : 0.f)
-                                 : keep[(sp.row * tiles_of(a.T) + tile) * a.D + c];
-        for (int64_t t = lo; t < end; ++t) {
-            const int64_t i = (sp.row * a.T + t) * a.D + c;
-            before[t - lo][threadIdx.x] = h;
-            h = Decay(fmaxf(a.log_alpha[i], a.floor_)).step(h, to_f32(reinterpret_cast<const E*>(a.x)[i]));
-        }
-        for (int64_t t = end - 1; t >= lo; --t) {
-            const int64_t i = (sp.row * a.T + t) * a.D + c;
-            const float la = a.log_alpha[i];
-            const Decay decay(fmaxf(la, a.floor_));
-            const float d = a.d_out ? to_f32(reinterpret_cast<const E*>(a.d_out)[i]) : 0.f;
-            const float hb = before[t - lo][threadIdx.x];
-            float s = 1.f;
-            if (a.g) {
-                s = sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
-                const float ht = decay.step(hb, to_f32(reinterpret_cast<const E*>(a.x)[i]));
-                reinterpret_cast<E*>(a.dg)[i] = from_f32<E>(d * ht * s * (1.f - s));
+// The state that leaves tile i - 1 in the order of the scan, per channel:
+// words + k * stride is channel 0's word of tile i - 1 - k, k < i.
+template <int VEC>
+__device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, int64_t i, float (&h)[VEC]) {
+    const int64_t most = i < kWindow ? i : kWindow;
+    bool have[VEC];
+    for (int polls = 0; polls < kMaxPolls; ++polls) {
+        uint64_t w[kWindow][VEC];
+#pragma unroll
+        for (int k = 0; k < kWindow; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                w[k][v] = k < most ? __hip_atomic_load(const_cast<uint64_t*>(words) + k * stride + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+        bool all = true;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            have[v] = false;
+#pragma unroll
+            for (int k = kWindow - 1; k >= 0; --k) {       // from the earliest tile on
+                const uint32_t high = (uint32_t)(w[k][v] >> 32);
+                const float H = __uint_as_float((uint32_t)w[k][v]);
+                const bool final = high == kFinal;
+                h[v] = final ? H : fmaf(__uint_as_float(high & 0x7fffffffu), h[v], H);
+                have[v] = final || (have[v] && high != 0);
             }
-            const float dh = fmaf(d, s, carry);
-            carry = decay.times(dh);
-            reinterpret_cast<E*>(a.dx)[i] = from_f32<E>(dh);
-            a.dlog_alpha[i] = la > a.floor_ ? carry * hb : 0.f;
+            all = all && have[v];
         }
-        end = lo;
+        if (__all(all)) return;
+        __builtin_amdgcn_s_sleep(1);
     }
-    if (a.d_state_in) a.d_state_in[(int64_t)blockIdx.y * a.D + c] = carry;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        if (!have[v]) h[v] = __uint_as_float(0x7fc00000u);
+}
+
+// Where a workgroup works: a tile taken off the counter where tiles wait for
+// each other, else its own index.  False: nothing left.
+__device__ __forceinline__ bool take_tile(const TileGrid& g, int32_t* counter, int32_t* lds, int64_t& id) {
+    id = blockIdx.x;
+    if (g.tiles > 1) {
+        if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        id = __builtin_amdgcn_readfirstlane(*lds);
+    }
+    return id >= 0 && id < g.total();
+}
+
+template <typename E, int VEC, int WAVES, bool GATE>
+__global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
+                                                                    uint64_t* words, float* keep) {
+    constexpr int TPW = kTile / WAVES;
+    static_assert(TPW * VEC <= 32, "one flag a value");
+    typedef typename VecOf<E, VEC>::type EV;
+    typedef typename VecOf<float, VEC>::type FV;
+    __shared__ float sA[WAVES][64 * VEC], sH[WAVES][64 * VEC], sIn[64 * VEC];
+    __shared__ int32_t sCut[WAVES], sId;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t id;
+    if (!take_tile(grid, counter, &sId, id)) return;
+    const int64_t i = id / grid.lanes, row = (id % grid.lanes) / grid.blocks;
+    const int64_t c0 = (id % grid.blocks) * (64 * VEC) + lane * VEC;
+    const bool in = c0 < a.D;                     // D is a multiple of VEC
+    const int64_t c = in ? c0 : a.D - VEC;
+    const int t0 = (int)(i * kTile) + wave * TPW;
+
+    EV x[TPW], g[TPW];
+    float d[TPW][VEC];
+    const int64_t base = row * a.T;
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int64_t t = t0 + j < (int)a.T ? t0 + j : (int)a.T - 1, at = (base + t) * a.D + c;
+        x[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.x) + at);
+        const FV l = *reinterpret_cast<const FV*>(a.log_alpha + at);
+        if constexpr (GATE) g[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.g) + at);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) d[j][v] = lane_of<VEC>(l, v);
+    }
+
+    // this wave's map
+    float h[VEC], sum[VEC];
+    uint32_t slow = 0;
+    bool cut = false;
+    Walk walk(a, (int)row, t0);
+    const int s0 = walk.s;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { h[v] = 0.f; sum[v] = 0.f; }
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.up(t)) {
+            const bool start = t == walk.first;
+            if (start) {
+                cut = true;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float l = fmaxf(d[j][v], a.floor_);
+                const Decay k(l);
+                sum[v] += l;
+                slow |= (uint32_t)k.slow << (j * VEC + v);
+                h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
+                // state_in is read once: state_out may be the same array
+                d[j][v] = start ? h[v] : k.c;
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        sA[wave][lane * VEC + v] = product_of(sum[v]);
+        sH[wave][lane * VEC + v] = h[v];
+    }
+    if (lane == 0) sCut[wave] = cut;
+    __syncthreads();
+
+    if (wave == 0) {
+        // the tile's map, and the state that enters it
+        float A[VEC], H[VEC], hin[VEC];
+        bool constant = false;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; H[v] = 0.f; hin[v] = 0.f; }
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const bool cw = sCut[w] != 0;
+            constant = constant || cw;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float Aw = sA[w][lane * VEC + v], Hw = sH[w][lane * VEC + v];
+                H[v] = cw ? Hw : fmaf(Aw, H[v], Hw);
+                A[v] *= Aw;
+            }
+        }
+        if (grid.tiles > 1) {
+            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
+            if (in && i + 1 < grid.tiles) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, H[v]) : map_word(A[v], H[v]));
+            }
+            if (i > 0) look_back<VEC>(mine - a.D, -a.D, i, hin);
+            if (in && !constant && i + 1 < grid.tiles) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], hin[v], H[v])));
+            }
+            if (in && a.keep) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) keep[(row * grid.tiles + i) * a.D + c + v] = hin[v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sIn[lane * VEC + v] = hin[v];
+    }
+    __syncthreads();
+
+    // again from the true state
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = sIn[lane * VEC + v];
+    for (int w = 0; w < wave; ++w) {
+        const bool cw = sCut[w] != 0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float Hw = sH[w][lane * VEC + v];
+            h[v] = cw ? Hw : fmaf(sA[w][lane * VEC + v], h[v], Hw);
+        }
+    }
+    walk.go_to(s0);
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.up(t)) {
+            const bool start = t == walk.first;
+            float y[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                h[v] = start ? d[j][v] : Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
+                y[v] = h[v];
+                if constexpr (GATE) y[v] *= sigmoidf_(lane_of<VEC>(g[j], v));
+            }
+            if (in) put<E, VEC>(reinterpret_cast<E*>(a.out) + (base + t) * a.D + c, y);
+            if (in && a.state_out && t == walk.end - 1) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) a.state_out[(int64_t)walk.s * a.D + c + v] = h[v];
+            }
+        }
+    }
+}
+
+template <typename E, int VEC, int WAVES, bool GATE>
+__global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
+                                                                             uint64_t* words, const float* keep) {
+    constexpr int TPW = kTile / WAVES;
+    static_assert(TPW * VEC <= 32, "one flag a value");
+    typedef typename VecOf<E, VEC>::type EV;
+    typedef typename VecOf<float, VEC>::type FV;
+    __shared__ float sA[WAVES][64 * VEC], sH[WAVES][64 * VEC], sC[WAVES][64 * VEC], sIn[64 * VEC];
+    __shared__ int32_t sFirst[WAVES], sLast[WAVES], sId;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t id;
+    if (!take_tile(grid, counter, &sId, id)) return;
+    const int64_t i = grid.tiles - 1 - id / grid.lanes, row = (id % grid.lanes) / grid.blocks;
+    const int64_t c0 = (id % grid.blocks) * (64 * VEC) + lane * VEC;
+    const bool in = c0 < a.D;
+    const int64_t c = in ? c0 : a.D - VEC;
+    const int t0 = (int)(i * kTile) + wave * TPW;
+
+    EV x[TPW], g[TPW], o[TPW];
+    float d[TPW][VEC];
+    const int64_t base = row * a.T;
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int64_t t = t0 + j < (int)a.T ? t0 + j : (int)a.T - 1, at = (base + t) * a.D + c;
+        x[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.x) + at);
+        const FV l = *reinterpret_cast<const FV*>(a.log_alpha + at);
+        if constexpr (GATE) g[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.g) + at);
+        o[j] = EV(0);
+        if (a.d_out) o[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.d_out) + at);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) d[j][v] = lane_of<VEC>(l, v);
+    }
+
+    // this wave's maps, of the state forward and of its gradient in reverse
+    float h[VEC], e[VEC], sum[VEC];
+    uint32_t slow = 0, free_ = 0;                 // free_: the floor does not bind
+    bool first = false, last = false;
+    Walk walk(a, (int)row, t0);
+    const int s0 = walk.s;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { h[v] = 0.f; e[v] = 0.f; sum[v] = 0.f; }
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.up(t)) {
+            if (t == walk.first) {
+                first = true;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float l = fmaxf(d[j][v], a.floor_);
+                free_ |= (uint32_t)(d[j][v] > a.floor_) << (j * VEC + v);
+                const Decay k(l);
+                sum[v] += l;
+                d[j][v] = k.c;
+                slow |= (uint32_t)k.slow << (j * VEC + v);
+                h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
+            }
+        }
+    }
+    const int s1 = walk.s;
+#pragma unroll
+    for (int j = TPW - 1; j >= 0; --j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.down(t)) {
+            if (t == walk.end - 1) {
+                last = true;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float s = GATE ? sigmoidf_(lane_of<VEC>(g[j], v)) : 1.f;
+                e[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).times(fmaf(lane_of<VEC>(o[j], v), s, e[v]));
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        sA[wave][lane * VEC + v] = product_of(sum[v]);
+        sH[wave][lane * VEC + v] = h[v];
+        sC[wave][lane * VEC + v] = e[v];
+    }
+    if (lane == 0) { sFirst[wave] = first; sLast[wave] = last; }
+    __syncthreads();
+
+    if (wave == 0) {
+        // the tile's map of the gradient, and the gradient that enters it from behind
+        float A[VEC], C[VEC], ein[VEC];
+        bool constant = false;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; C[v] = 0.f; ein[v] = 0.f; }
+#pragma unroll
+        for (int w = WAVES - 1; w >= 0; --w) {
+            const bool cw = sLast[w] != 0;
+            constant = constant || cw;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float Aw = sA[w][lane * VEC + v], Cw = sC[w][lane * VEC + v];
+                C[v] = cw ? Cw : fmaf(Aw, C[v], Cw);
+                A[v] *= Aw;
+            }
+        }
+        if (grid.tiles > 1) {
+            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
+            const int64_t behind = grid.tiles - 1 - i;
+            if (in && i > 0) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, C[v]) : map_word(A[v], C[v]));
+            }
+            if (behind > 0) look_back<VEC>(mine + a.D, a.D, behind, ein);
+            if (in && !constant && i > 0) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], ein[v], C[v])));
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sIn[lane * VEC + v] = ein[v];
+    }
+    __syncthreads();
+
+    // the states before each token, from the kept one that enters the tile
+    float before[TPW][VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = i > 0 ? keep[(row * grid.tiles + i) * a.D + c + v] : 0.f;
+    for (int w = 0; w < wave; ++w) {
+        const bool cw = sFirst[w] != 0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float Hw = sH[w][lane * VEC + v];
+            h[v] = cw ? Hw : fmaf(sA[w][lane * VEC + v], h[v], Hw);
+        }
+    }
+    walk.go_to(s0);
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.up(t)) {
+            if (t == walk.first) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                before[j][v] = h[v];
+                h[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
+            }
+        }
+    }
+
+    // the gradients, from the one that enters the wave's stretch from behind
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) e[v] = sIn[lane * VEC + v];
+    for (int w = WAVES - 1; w > wave; --w) {
+        const bool cw = sLast[w] != 0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float Cw = sC[w][lane * VEC + v];
+            e[v] = cw ? Cw : fmaf(sA[w][lane * VEC + v], e[v], Cw);
+        }
+    }
+    walk.go_to(s1);
+#pragma unroll
+    for (int j = TPW - 1; j >= 0; --j) {
+        const int t = t0 + j;
+        if (t < (int)a.T && walk.down(t)) {
+            if (t == walk.end - 1) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
+            }
+            float dx[VEC], dl[VEC], dg[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const Decay k(d[j][v], slow >> (j * VEC + v) & 1u);
+                const float dy = lane_of<VEC>(o[j], v);
+                float s = 1.f;
+                if constexpr (GATE) {
+                    s = sigmoidf_(lane_of<VEC>(g[j], v));
+                    dg[v] = dy * k.step(before[j][v], lane_of<VEC>(x[j], v)) * s * (1.f - s);
+                }
+                dx[v] = fmaf(dy, s, e[v]);
+                e[v] = k.times(dx[v]);
+                dl[v] = free_ >> (j * VEC + v) & 1u ? e[v] * before[j][v] : 0.f;
+            }
+            if (in) {
+                const int64_t at = (base + t) * a.D + c;
+                put<E, VEC>(reinterpret_cast<E*>(a.dx) + at, dx);
+                put<float, VEC>(a.dlog_alpha + at, dl);
+                if constexpr (GATE) put<E, VEC>(reinterpret_cast<E*>(a.dg) + at, dg);
+                if (a.d_state_in && t == walk.first) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) a.d_state_in[(int64_t)walk.s * a.D + c + v] = e[v];
+                }
+            }
+        }
+    }
+}
+
+// Before a scan: no tile taken, nothing published; and the sequences without
+// a token, which no tile sees, pass their state through (to may be from).
+__global__ __launch_bounds__(kThreads) void kda_recurrence_begin_kernel(uint64_t* clear, int64_t n_clear, const int32_t* cu,
+                                                                        int64_t n_seq, int64_t T, int64_t D,
+                                                                        const float* from, float* to) {
+    const int64_t step = (int64_t)gridDim.x * kThreads, at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    for (int64_t k = at; k < n_clear; k += step) clear[k] = 0;
+    if (!to) return;
+    for (int64_t s = blockIdx.x; s < n_seq; s += gridDim.x) {
+        int64_t b = 0, e = T;
+        if (cu) seq_bounds(cu, s, T, b, e);
+        if (e > b) continue;
+        for (int64_t c = threadIdx.x; c < D; c += kThreads) to[s * D + c] = from ? from[s * D + c] : 0.f;
+    }
 }
 
 template <typename E>
@@ -128,24 +564,70 @@ __global__ __launch_bounds__(kThreads) void kda_recurrence_step_kernel(Recurrenc
     reinterpret_cast<E*>(a.out)[i] = from_f32<E>(h * s);
 }
 
+int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+
+// The workspace: the counter (its own 256 bytes), the look-back words, then
+// for training the state that enters every tile.  One tile a row needs none.
+size_t words_bytes(int64_t B, int64_t T, int64_t D) {
+    return tiles_of(T) > 1 ? ((size_t)(B * tiles_of(T)) * (size_t)D * 8 + 255) / 256 * 256 : 0;
+}
+constexpr size_t kCounterBytes = 256;
+
+constexpr int kForwardWaves = 8, kBackwardWaves = 16;
+
+template <typename E, int VEC, bool GATE>
+hipError_t launch_scan_v(const RecurrenceArgs& a, bool backward, hipStream_t s) {
+    TileGrid g;
+    g.tiles = tiles_of(a.T);
+    g.blocks = (int)((a.D + 64 * VEC - 1) / (64 * VEC));
+    g.lanes = a.B * g.blocks;
+    int32_t* counter = reinterpret_cast<int32_t*>(a.ws);
+    uint64_t* words = reinterpret_cast<uint64_t*>(a.ws + kCounterBytes);
+    float* keep = reinterpret_cast<float*>(a.ws + kCounterBytes + words_bytes(a.B, a.T, a.D));
+    if (backward)
+        hipLaunchKernelGGL((kda_recurrence_backward_kernel<E, VEC, kBackwardWaves, GATE>), dim3((unsigned)g.total()),
+                           dim3(kBackwardWaves * 64), 0, s, a, g, counter, words, keep);
+    else
+        hipLaunchKernelGGL((kda_recurrence_kernel<E, VEC, kForwardWaves, GATE>), dim3((unsigned)g.total()),
+                           dim3(kForwardWaves * 64), 0, s, a, g, counter, words, keep);
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_scan_t(const RecurrenceArgs& a, bool backward, hipStream_t s) {
+    const float* from = backward ? a.d_state : a.state_in;
+    float* to = backward ? a.d_state_in : a.state_out;
+    const bool empties = to && (a.cu_seqlens || a.T == 0);
+    const int64_t n_clear = a.T > kTile ? (int64_t)((kCounterBytes + words_bytes(a.B, a.T, a.D)) / 8) : 0;
+    if (n_clear > 0 || empties) {
+        int64_t blocks = (n_clear + 8 * kThreads - 1) / (8 * kThreads);
+        if (empties && a.n_seq > blocks) blocks = a.n_seq;
+        blocks = blocks > 2048 ? 2048 : blocks;
+        hipLaunchKernelGGL(kda_recurrence_begin_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                           reinterpret_cast<uint64_t*>(a.ws), n_clear, a.cu_seqlens, a.n_seq, a.T, a.D, from,
+                           empties ? to : nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.B == 0 || a.T == 0) return hipSuccess;
+    // two channels a lane where rows stay aligned to them
+    if (a.D % 2 == 0) return a.g ? launch_scan_v<E, 2, true>(a, backward, s) : launch_scan_v<E, 2, false>(a, backward, s);
+    return a.g ? launch_scan_v<E, 1, true>(a, backward, s) : launch_scan_v<E, 1, false>(a, backward, s);
+}
+
 }  // namespace
 
 size_t recurrence_workspace_bytes(int64_t B, int64_t T, int64_t D, bool backward) {
-    return backward ? (size_t)(B * ((T + kTile - 1) / kTile)) * (size_t)D * sizeof(float) : 0;
+    if (B == 0 || T <= kTile) return 0;
+    return kCounterBytes + words_bytes(B, T, D) + (backward ? (size_t)(B * tiles_of(T)) * (size_t)D * sizeof(float) : 0);
 }
 
 hipError_t launch_recurrence(bool bf16, const RecurrenceArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)(a.cu_seqlens ? a.n_seq : a.B));
-    if (bf16) hipLaunchKernelGGL(kda_recurrence_kernel<__bf16>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(kda_recurrence_kernel<float>, grid, dim3(64), 0, s, a);
-    return hipGetLastError();
+    return bf16 ? launch_scan_t<__bf16>(a, false, s) : launch_scan_t<float>(a, false, s);
 }
 
 hipError_t launch_recurrence_backward(bool bf16, const RecurrenceArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.D + 63) / 64), (unsigned)(a.cu_seqlens ? a.n_seq : a.B));
-    if (bf16) hipLaunchKernelGGL(kda_recurrence_backward_kernel<__bf16>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(kda_recurrence_backward_kernel<float>, grid, dim3(64), 0, s, a);
-    return hipGetLastError();
+    return bf16 ? launch_scan_t<__bf16>(a, true, s) : launch_scan_t<float>(a, true, s);
 }
 
 hipError_t launch_recurrence_step(bool bf16, const RecurrenceStepArgs& a, hipStream_t s) {

@@ -161,8 +161,8 @@ kda_status kda_recurrence_prefill_for_backward(const kda_recurrence_problem* p, 
  * too: not the array that state_out went to).  Where log_alpha <=
  * log_alpha_min, or is NaN, dlog_alpha is 0.  d_out, d_state may be NULL
  * (zero); dg is written where g is given and may be NULL otherwise;
- * d_state_in may be NULL.  Outputs are overwritten; tokens of no sequence are
- * not written.  The workspace can serve further backward calls, one at a time. */
+ * d_state_in may be NULL.  Outputs are overwritten and may not overlap each
+ * other or the inputs; tokens of no sequence are not written.  The workspace can serve further backward calls, one at a time. */
 kda_status kda_recurrence_backward(const kda_recurrence_problem* p, const void* x, const float* log_alpha,
                                    const void* g, const float* state_in, const int32_t* cu_seqlens,
                                    const void* d_out, const float* d_state, void* dx, float* dlog_alpha, void* dg,
