@@ -1,8 +1,34 @@
 // kda_cache4_attention.hip -- causal grouped-query attention over the paged
-// 4-bit cache, one wave per (query, head).
+// 4-bit cache.
 //
 //   out = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),  s_t = scale q . K_t,
 //   m = max s_t, kept as a running maximum and sum in fp32.
+//
+// The cache's values go from memory into MFMA operands without LDS.  A wave
+// takes 32 tokens of one key/value head at a time, against 16 R rows; a row is
+// a (query, head of the group) pair, so the heads that share keys share their
+// loads.  With lane = 16 g + n:
+//  * S^T = K Q^T.  A operand: token n of 16, its channels [D/4 g, D/4 g + D/4)
+//    as one 16-byte (D = 128) load, D/32 steps of 8 channels; one scale byte
+//    covers them.  B operand: the row n with the same channels.
+//  * The result holds row n's scores of the tokens 4 g + v (and 16 + 4 g + v of
+//    the second half): as they lie these are the B operand of O^T = V^T P^T, no
+//    exchange between lanes.  Maximum and sum of a row are in-lane, then two
+//    exchanges over g.
+//  * V^T as A operand needs 8 tokens of one channel a lane.  A lane loads, for
+//    its 8 tokens, the word with the channels D/16 n + j: conversion gives
+//    channel pairs of one token, a byte permute pairs the tokens, and j runs
+//    over the MFMAs.  O^T then holds D/4 consecutive channels of row n.
+// 4-bit values times their power of two are exact in bf16.  bf16 queries are
+// exact too and the probabilities round once to bf16; fp32 queries and
+// probabilities are taken in three bf16 parts, which together hold 24 bits.
+//
+// Few rows (decode): the four waves of a workgroup take turns at the 32-token
+// tiles and join their results through LDS, and a sequence is split into
+// pieces over workgroups, joined by a second kernel.  Many rows: each wave has
+// rows of its own.
+#include <type_traits>
+
 #include "kda_common.hpp"
 #include "kda_hybrid_internal.hpp"
 
@@ -10,86 +36,631 @@ namespace kda {
 
 namespace {
 
-__device__ __forceinline__ float value_of(uint32_t code, uint32_t scale) {
-    const uint32_t m = code & 7u;
-    const float unit = __uint_as_float(scale == 255 ? 0x7fc00000u : scale == 0 ? 0x00400000u : scale << 23);
-    const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-    return (code & 8u ? -mag : mag) * unit;
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+// The running maximum moves only when a score passes it by this much (in
+// powers of two): probabilities then stay below 2^8 and the rescaling of the
+// sums is rare.
+constexpr float kSlack = 8.f;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// How the work is laid out (host and kernels).
+struct Layout {
+    int rows;        // rows of a workgroup
+    int64_t slots;   // upper bound of row blocks over all sequences
+    int per_seq;     // without offsets: row blocks of each sequence
+    int nsplit;      // pieces of a sequence
+    int piece;       // tokens of a piece, at least (a multiple of 128)
+};
+
+struct Block {
+    int64_t s;       // sequence
+    int64_t row0;    // its first query's row of q
+    int queries;
+    int total;       // tokens that count (at most what the table holds)
+    int first;       // position of the first query, may be negative
+    int begin;       // first (query, head) row of this block
+    bool any;
+};
+
+__device__ __forceinline__ int cap_tokens(const Cache4AttentionArgs& a) { return a.max_pages << a.c.page_shift; }
+
+// What sequence s is.
+__device__ __forceinline__ void sequence_of(const Cache4AttentionArgs& a, int64_t s, Block& b) {
+    int64_t r0 = s, r1 = s + 1;
+    if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.tokens, r0, r1);
+    const int64_t total = a.total_lens[s] > 0 ? a.total_lens[s] : 0;
+    b.s = s;
+    b.row0 = r0;
+    b.queries = (int)(r1 - r0);
+    const int64_t first = total - b.queries;
+    b.first = (int)first;
+    const int cap = cap_tokens(a);
+    b.total = (int)(total < cap ? total : cap);
 }
 
-// Row index along q that sequence s's queries begin and end at.
-__device__ __forceinline__ void rows_of(const Cache4AttentionArgs& a, int64_t s, int64_t& b, int64_t& e) {
-    if (!a.cu_seqlens) { b = s; e = s + 1; return; }
-    seq_bounds(a.cu_seqlens, s, a.tokens, b, e);
+// Row blocks of sequence s with offsets begin at slot floor(cu[s] G / rows) + s,
+// which leaves each its ceil(m G / rows) slots and can be searched.
+__device__ __forceinline__ int64_t first_slot(const Cache4AttentionArgs& a, const Layout& l, int64_t s) {
+    int64_t c = a.cu_seqlens[s];
+    c = c < 0 ? 0 : (c > a.tokens ? a.tokens : c);
+    return c * a.group / l.rows + s;
 }
 
-template <typename E, int D>
-__global__ __launch_bounds__(64) void kda_cache4_attention_kernel(Cache4AttentionArgs a) {
-    constexpr int PER = D / 64;
-    const int lane = threadIdx.x, head = blockIdx.y, kvh = head / a.group;
-    const int64_t row = blockIdx.x;
-    int64_t s = 0, b, e;
+__device__ __forceinline__ Block block_of(const Cache4AttentionArgs& a, const Layout& l, int64_t slot) {
+    Block b;
+    int64_t at;
     if (a.cu_seqlens) {
-        int64_t lo = 0, hi = a.n_seq;          // the last sequence that begins at or before the row
+        int64_t lo = 0, hi = a.n_seq;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (first_slot(a, l, mid) <= slot) lo = mid; else hi = mid;
+        }
+        sequence_of(a, lo, b);
+        at = slot - first_slot(a, l, lo);
+    } else {
+        const int64_t s = slot / l.per_seq;
+        if (s >= a.n_seq) {         // more slots than row blocks
+            b = Block{};
+            return b;
+        }
+        sequence_of(a, s, b);
+        at = slot % l.per_seq;
+    }
+    const int64_t begin = at * l.rows;
+    b.any = begin >= 0 && begin < (int64_t)b.queries * a.group;
+    b.begin = b.any ? (int)begin : 0;
+    return b;
+}
+
+// Tokens that row r of a sequence sees.
+__device__ __forceinline__ int end_of(const Cache4AttentionArgs& a, const Block& b, int r) {
+    if (r >= b.queries * a.group) return 0;
+    const int64_t end = (int64_t)b.first + r / a.group + 1;
+    return (int)(end < 0 ? 0 : (end > b.total ? b.total : end));
+}
+
+__device__ __forceinline__ int piece_of(const Layout& l, int total) {
+    const int even = (int)((((int64_t)total + l.nsplit - 1) / l.nsplit + 127) / 128 * 128);
+    return even > l.piece ? even : l.piece;
+}
+
+// Index of (row of q, head) of row r.
+__device__ __forceinline__ int64_t place_of(const Cache4AttentionArgs& a, const Block& b, int kvh, int r) {
+    return (b.row0 + r / a.group) * a.heads + kvh * a.group + r % a.group;
+}
+
+__device__ __forceinline__ float scale_bits(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 8 channels of a word, times their scale.
+__device__ __forceinline__ bf16x8 eight_of(uint32_t w, float scale) {
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+    return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+__device__ __forceinline__ uint32_t bits_of(bf16x2 x) { return __builtin_bit_cast(uint32_t, x); }
+
+// Channels (2 I, 2 I + 1) of 8 tokens as two operands: lo and hi.
+template <int I>
+__device__ __forceinline__ void two_channels(const uint32_t (&w)[8], const float (&s)[8], bf16x8& lo, bf16x8& hi) {
+    uint32_t p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[e], s[e], I));
+    u32x4 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        a[e] = __builtin_amdgcn_perm(p[2 * e + 1], p[2 * e], 0x05040100u);
+        b[e] = __builtin_amdgcn_perm(p[2 * e + 1], p[2 * e], 0x07060302u);
+    }
+    lo = __builtin_bit_cast(bf16x8, a);
+    hi = __builtin_bit_cast(bf16x8, b);
+}
+
+// x in PARTS bf16 parts whose sum holds 8 PARTS bits of it.
+template <int PARTS>
+__device__ __forceinline__ void parts_of(float x, __bf16 (&p)[PARTS]) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        p[i] = (__bf16)x;
+        x -= (float)p[i];
+    }
+}
+
+// One 32-token tile as loaded: keys, values and scales of both 16-token halves.
+template <int D>
+struct Tile {
+    uint32_t k[2][D / 32];
+    uint32_t ks[2];
+    uint32_t v[2][4];
+    uint32_t vs[2][D / 32];     // scales of 4 tokens, D/32 bytes each
+    bool ok[2];                 // the half's page exists
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, const int32_t* table, int kvh, int t0, int total,
+                                          int lane, Tile<D>& x) {
+    const int g = lane >> 4, n = lane & 15;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int t = t0 + 16 * u;
+        int64_t page = t < total ? table[t >> a.c.page_shift] : -1;
+        x.ok[u] = page >= 0 && page < a.c.pages;
+        if (x.ok[u]) {
+            const int64_t row = ((page * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
+            const uint8_t* kp = a.c.k + row * (D / 2) + n * (D / 2) + g * (D / 8);
+            if constexpr (D == 128) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(kp);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x.k[u][j] = w[j];
+            } else {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(kp);
+                x.k[u][0] = w[0]; x.k[u][1] = w[1];
+            }
+            x.ks[u] = a.c.k_scale[row * (D / 32) + n * (D / 32) + g * (D / 32) / 4];
+            const uint8_t* vp = a.c.v + row * (D / 2) + 4 * g * (D / 2) + (D == 128 ? 4 * n : 4 * (n >> 1));
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x.v[u][v] = *reinterpret_cast<const uint32_t*>(vp + v * (D / 2));
+            const uint8_t* sp = a.c.v_scale + row * (D / 32) + 4 * g * (D / 32);
+            if constexpr (D == 128) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(sp);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x.vs[u][j] = w[j];
+            } else {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(sp);
+                x.vs[u][0] = w[0]; x.vs[u][1] = w[1];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) { x.k[u][j] = 0; x.vs[u][j] = 0x7f7f7f7fu; }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x.v[u][v] = 0;
+            x.ks[u] = 127;
+        }
+    }
+}
+
+// The words and scales of this lane's channel group for its 8 tokens; those at
+// or past `end` are zeros, whatever memory holds there.
+template <int D>
+__device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int lane, uint32_t (&w)[8], float (&s)[8]) {
+    const int g = lane >> 4, n = lane & 15;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const bool in = t0 + 16 * u + 4 * g + v < end;
+            uint32_t b, c;
+            if constexpr (D == 128) {
+                b = x.vs[u][v] >> (8 * (n >> 2)) & 255u;
+                c = x.v[u][v];
+            } else {
+                b = x.vs[u][v >> 1] >> (16 * (v & 1) + 8 * (n >> 3)) & 255u;
+                c = x.v[u][v] >> (16 * (n & 1));
+            }
+            w[4 * u + v] = in ? c : 0u;
+            s[4 * u + v] = scale_bits(in ? b : 127u);
+        }
+}
+
+template <typename E, int D, int R, bool SPLITW>
+__global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, float* part_o,
+                                                                           float* part_ml) {
+    constexpr int PARTS = sizeof(E) == 2 ? 1 : 3;
+    constexpr int KS = D / 32;          // MFMA steps over the channels
+    constexpr int VJ = D / 16;          // MFMAs of a value tile
+    constexpr int PER = D / 4;          // channels of a lane's result
+    constexpr int ROWS = 16 * R;        // rows of a wave
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, n = lane & 15;
+
+    // key/value heads alternate fastest, so workgroups that share keys and
+    // values lie on one XCD where there are 8 heads
+    const int64_t id = blockIdx.x;
+    const int kvh = (int)(id % a.c.heads);
+    const int split = (int)(id / a.c.heads % l.nsplit);
+    const Block b = block_of(a, l, id / a.c.heads / l.nsplit);
+    if (!b.any) return;
+    const int piece = piece_of(l, b.total);
+    const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
+    const int n_rows = b.queries * a.group;
+    const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
+    const int lo = split * (int64_t)piece < b.total ? split * piece : b.total;
+    const int hi = last < row0 ? lo : min(end_of(a, b, last), (int)min((int64_t)lo + piece, (int64_t)b.total));
+    // every wave of a workgroup that shares rows sees the same range
+    if (SPLITW && l.nsplit > 1 && (hi <= lo || (int64_t)split * piece >= b.total)) return;
+    const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
+
+    // queries: row n of each 16, channels [PER g, PER g + PER)
+    bf16x8 q[R][KS][PARTS];
+    int end[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = row0 + 16 * r + n;
+        end[r] = end_of(a, b, row);
+        const E* p = reinterpret_cast<const E*>(a.q) + place_of(a, b, kvh, row < n_rows ? row : 0) * D + PER * g;
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (PARTS == 1) {
+                    q[r][j][0][e] = p[8 * j + e];
+                } else {
+                    __bf16 s[PARTS];
+                    parts_of<PARTS>(p[8 * j + e], s);
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) q[r][j][i][e] = s[i];
+                }
+            }
+    }
+
+    f32x4 o[R][VJ];
+    float m[R], sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const float to_log2 = a.scale * kLog2e;
+    const int32_t* table = a.block_table + b.s * a.max_pages;
+
+    constexpr int STEP = SPLITW ? 32 * kWaves : 32;
+    Tile<D> next;
+    int t0 = lo + (SPLITW ? 32 * wave : 0);
+    if (t0 < hi) load_tile<D>(a, table, kvh, t0, hi, lane, next);
+    for (; t0 < hi; t0 += STEP) {
+        const Tile<D> x = next;
+        if (t0 + STEP < hi) load_tile<D>(a, table, kvh, t0 + STEP, hi, lane, next);
+        const bool whole = x.ok[0] && x.ok[1] && t0 + 32 <= all_see && t0 + 32 <= hi;
+
+        bf16x8 k[2][KS];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) k[u][j] = eight_of(x.k[u][j], scale_bits(x.ks[u]));
+        bf16x8 p[R][PARTS];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float y[8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][j], q[r][j][i], acc, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[4 * u + v] = acc[v] * to_log2;
+            }
+            if (!whole) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int t = t0 + 16 * u + 4 * g + v;
+                        if (!x.ok[u] || t >= end[r] || t >= hi) y[4 * u + v] = -INFINITY;
+                    }
+            }
+            float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (__any(top > m[r] + kSlack)) {
+                const float mn = fmaxf(m[r], top);
+                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
+                sum[r] *= f;
+#pragma unroll
+                for (int j = 0; j < VJ; ++j) o[r][j] *= f;
+                m[r] = mn;
+            }
+            const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = __builtin_amdgcn_exp2f(y[e] - base);
+                sum[r] += y[e];
+                if constexpr (PARTS == 1) {
+                    p[r][0][e] = (__bf16)y[e];
+                } else {
+                    __bf16 s[PARTS];
+                    parts_of<PARTS>(y[e], s);
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) p[r][i][e] = s[i];
+                }
+            }
+        }
+
+        uint32_t w[8];
+        float s[8];
+        auto accumulate = [&](const bf16x8 (&pp)[R][PARTS]) {
+            auto pair = [&](auto I) {
+                bf16x8 c[2];
+                two_channels<decltype(I)::value>(w, s, c[0], c[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i)
+                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pp[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+            };
+            pair(std::integral_constant<int, 0>{});
+            pair(std::integral_constant<int, 1>{});
+            if constexpr (VJ == 8) {
+                pair(std::integral_constant<int, 2>{});
+                pair(std::integral_constant<int, 3>{});
+            }
+        };
+        values_of<D>(x, t0, hi, lane, w, s);
+        bool odd = false;       // a value that is no number, where some rows do not see it
+        if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
+        }
+        if (!__any(odd)) {
+            accumulate(p);
+        } else {
+            // one end at a time, with the tokens behind it cleared: 0 times NaN would reach rows that do not see it
+            for (int e = max(t0, 0); e < t0 + 32; ++e) {
+                const int stop = e + 1;
+                bf16x8 pe[R][PARTS];
+                bool some = false;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int mine = min(max(end[r], 0), min(hi, t0 + 32));
+                    const bool use = mine == stop;
+                    some = some || use;
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) pe[r][i][c] = use ? p[r][i][c] : (__bf16)0.f;
+                }
+                if (!__any(some)) continue;
+                values_of<D>(x, t0, stop, lane, w, s);
+                accumulate(pe);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        sum[r] += __shfl_xor(sum[r], 16);
+        sum[r] += __shfl_xor(sum[r], 32);
+    }
+
+    // what a row's result becomes: a part of a split sequence, or the output
+    auto put = [&](int row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
+        const int64_t at = place_of(a, b, kvh, row);
+        if (l.nsplit > 1) {
+            const int64_t i = (int64_t)split * a.tokens * a.heads + at;
+            float* po = part_o + i * D + c0;
+            *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
+            *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
+            if (c0 == 0) { part_ml[2 * i] = mx; part_ml[2 * i + 1] = sm; }
+            return;
+        }
+        const float f = sm == 0.f ? 0.f : 1.f / sm;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = y[e] * f;
+        if (a.g) {
+            const E* gp = reinterpret_cast<const E*>(a.g) + at * D + c0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] *= sigmoidf_(to_f32(gp[e]));
+        }
+        E* op = reinterpret_cast<E*>(a.out) + at * D + c0;
+        st4(op, f32x4{z[0], z[1], z[2], z[3]});
+        st4(op + 4, f32x4{z[4], z[5], z[6], z[7]});
+    };
+
+    if constexpr (!SPLITW) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = row0 + 16 * r + n;
+            if (row >= n_rows || (l.nsplit > 1 && end[r] <= lo)) continue;
+            // element (j, v) of the result is channel PER g + VJ v + j
+#pragma unroll
+            for (int c = 0; c < PER; c += 8) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = o[r][(c + e) % VJ][(c + e) / VJ];
+                put(row, PER * g + c, y, m[r], sum[r]);
+            }
+        }
+    } else {
+        // join the waves' results, in their order
+        constexpr int LD = D + 4;
+        __shared__ float so[ROWS][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
+        if (g == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) { sm[wave][16 * r + n] = m[r]; ss[wave][16 * r + n] = sum[r]; }
+        }
+        __syncthreads();
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][16 * r + n]);
+            f[r] = m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - mx);
+        }
+        for (int w = 0; w < kWaves; ++w) {
+            if (w == wave) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+#pragma unroll
+                        for (int j = 0; j < VJ; j += 4) {
+                            f32x4* at = reinterpret_cast<f32x4*>(&so[16 * r + n][PER * g + VJ * v + j]);
+                            f32x4 y = {o[r][j][v] * f[r], o[r][j + 1][v] * f[r], o[r][j + 2][v] * f[r], o[r][j + 3][v] * f[r]};
+                            *at = w == 0 ? y : *at + y;
+                        }
+            }
+            __syncthreads();
+        }
+        for (int i = threadIdx.x; i < ROWS * (D / 8); i += kWaves * 64) {
+            const int r = i / (D / 8), c0 = i % (D / 8) * 8, row = row0 + r;
+            if (row >= n_rows || (l.nsplit > 1 && end_of(a, b, row) <= lo)) continue;
+            float mx = -INFINITY, sum_r = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                if (sm[w][r] != -INFINITY) sum_r += ss[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - mx);
+            put(row, c0, &so[r][c0], mx, sum_r);
+        }
+    }
+}
+
+// Joins the pieces of one (row, head): weights 2^(m_i - max m), in the order of
+// the pieces.  A quarter of them each wave, whose sums are joined through LDS.
+template <typename E, int D>
+__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, const float* part_o,
+                                                                         const float* part_ml) {
+    constexpr int PER = D / 64;
+    extern __shared__ float weight[];                  // [nsplit]
+    __shared__ float red[kWaves], acc[kWaves][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t at = blockIdx.x, row = at / a.heads;
+    int64_t s = row;
+    if (a.cu_seqlens) {
+        int64_t lo = 0, hi = a.n_seq;
         while (hi - lo > 1) {
             const int64_t mid = (lo + hi) >> 1;
             if (a.cu_seqlens[mid] <= row) lo = mid; else hi = mid;
         }
         s = lo;
-    } else {
-        s = row;
     }
-    rows_of(a, s, b, e);
-    if (row < b || row >= e) return;
-    const int64_t total = a.total_lens[s];
+    Block b;
+    sequence_of(a, s, b);
+    if (row < b.row0 || row >= b.row0 + b.queries) return;
+    const int end = end_of(a, b, (int)(row - b.row0) * a.group);
+    const int piece = piece_of(l, b.total);
+    const int count = (int)min((int64_t)l.nsplit, ((int64_t)end + piece - 1) / piece);
+    const int64_t stride = a.tokens * a.heads;
+
+    float mx = -INFINITY;
+    for (int i = threadIdx.x; i < count; i += kWaves * 64) mx = fmaxf(mx, part_ml[2 * (i * stride + at)]);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+    if (lane == 0) red[wave] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    __syncthreads();
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < count; i += kWaves * 64) {
+        const float mi = part_ml[2 * (i * stride + at)];
+        const float w = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mx);
+        weight[i] = w;
+        sum += w * part_ml[2 * (i * stride + at) + 1];
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+    if (lane == 0) red[wave] = sum;
+    __syncthreads();
+    sum = red[0] + red[1] + red[2] + red[3];
+    float o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int i = wave; i < count; i += kWaves) {
+        const float w = weight[i];
+        const float* p = part_o + (i * stride + at) * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] += w == 0.f ? 0.f : w * p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[wave][lane * PER + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x < D) {
+        const int c = threadIdx.x;
+        float y = acc[0][c] + acc[1][c] + acc[2][c] + acc[3][c];
+        y = sum == 0.f ? 0.f : y / sum;
+        if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[at * D + c]));
+        reinterpret_cast<E*>(a.out)[at * D + c] = from_f32<E>(y);
+    }
+}
+
+constexpr int kSplitMaxRows = 32;      // rows that the waves of a workgroup share
+
+// bf16 rows of a wave in the many-rows form; fp32 takes three times the
+// registers for its queries
+constexpr int rows_r(bool bf16) { return bf16 ? 2 : 1; }
+
+struct Plan {
+    Layout l;
+    bool splitw;
+    int r;
+};
+
+Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
+    Plan p = {};
+    const int64_t rows = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
+    p.splitw = rows <= kSplitMaxRows;
+    p.r = p.splitw ? (rows <= 16 ? 1 : 2) : rows_r(bf16);
+    p.l.rows = p.splitw ? 16 * p.r : 16 * p.r * kWaves;
+    p.l.per_seq = (a.group + p.l.rows - 1) / p.l.rows;
+    // with or without offsets: enough slots for both
+    p.l.slots = a.tokens * a.group / p.l.rows + a.n_seq;
+    if (a.n_seq * p.l.per_seq > p.l.slots) p.l.slots = a.n_seq * p.l.per_seq;
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
-    int64_t end = total - (e - b) + (row - b) + 1;      // tokens that the query sees
-    end = end < cap ? end : cap;
-    float q[PER], o[PER], m = -INFINITY, l = 0.f;
-    const int64_t at = (row * a.heads + head) * D;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) { q[i] = to_f32(reinterpret_cast<const E*>(a.q)[at + lane * PER + i]); o[i] = 0.f; }
-    for (int64_t t = 0; t < end; ++t) {
-        const int64_t page = a.block_table[s * a.max_pages + (t >> a.c.page_shift)];
-        if (page < 0 || page >= a.c.pages) continue;
-        const int64_t r = ((page * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
-        float dot = 0.f, v[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int ch = lane * PER + i;
-            const int64_t byte = r * (D / 2) + ch / 2, sc = r * (D / 32) + ch / 32;
-            dot += q[i] * value_of(a.c.k[byte] >> (4 * (ch & 1)), a.c.k_scale[sc]);
-            v[i] = value_of(a.c.v[byte] >> (4 * (ch & 1)), a.c.v_scale[sc]);
-        }
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) dot += __shfl_xor(dot, off);
-        const float x = dot * a.scale;
-        const float mn = x <= m ? m : x;                // a NaN score stays
-        const float f = m == -INFINITY ? 0.f : __expf(m - mn), p = mn == -INFINITY ? 0.f : __expf(x - mn);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) o[i] = o[i] * f + p * v[i];
-        m = mn;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        float y = l == 0.f ? 0.f : o[i] / l;
-        if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[at + lane * PER + i]));
-        reinterpret_cast<E*>(a.out)[at + lane * PER + i] = from_f32<E>(y);
-    }
+    const int64_t len = a.max_len < cap ? a.max_len : cap;
+    const int64_t base = p.l.slots * a.c.heads;
+    // Few rows: pieces of at most 1024 tokens, so that ragged sequences even
+    // out, and down to 128 until about 1024 workgroups run.  Many rows: split
+    // only what leaves the card empty, since parts cost as much as outputs.
+    int64_t piece = p.splitw ? 1024 : (len > 0 ? len : 1);
+    const int64_t target = p.splitw ? 1024 : 512;
+    if (base * ((len + piece - 1) / piece) < target) piece = len * base / target;
+    piece = (piece + 127) / 128 * 128;
+    if (piece < 128) piece = 128;
+    int64_t n = (len + piece - 1) / piece;
+    if (n > INT32_MAX / base) n = INT32_MAX / base;
+    p.l.nsplit = (int)(n < 1 ? 1 : (n > 1024 ? 1024 : n));
+    p.l.piece = (int)(piece > (1 << 30) ? (1 << 30) : piece);
+    return p;
+}
+
+template <typename E, int D, int R, bool SPLITW>
+hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, float* part_o, float* part_ml, hipStream_t s) {
+    const int64_t blocks = p.l.slots * a.c.heads * p.l.nsplit;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, s, a, p.l,
+                       part_o, part_ml);
+    return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
+    constexpr bool bf16 = sizeof(E) == 2;
+    const Plan p = plan_of(bf16, a);
+    const int64_t places = (int64_t)p.l.nsplit * a.tokens * a.heads;
+    float* part_o = reinterpret_cast<float*>(ws);
+    float* part_ml = part_o + places * D;
+    hipError_t e;
+    if (!p.splitw) e = launch_attention_r<E, D, rows_r(bf16), false>(a, p, part_o, part_ml, s);
+    else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, part_o, part_ml, s);
+    else e = launch_attention_r<E, D, 2, true>(a, p, part_o, part_ml, s);
+    if (e != hipSuccess || p.l.nsplit == 1) return e;
+    hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D>), dim3((unsigned)(a.tokens * a.heads)), dim3(kWaves * 64),
+                       p.l.nsplit * sizeof(float), s, a, p.l, part_o, part_ml);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t cache4_attention_workspace_bytes(int, const Cache4AttentionArgs&) { return 0; }
+size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
+    const Plan p = plan_of(bf16, a);
+    if (p.l.nsplit == 1) return 0;
+    return (size_t)p.l.nsplit * (size_t)(a.tokens * a.heads) * (size_t)(d + 2) * sizeof(float);
+}
 
-hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char*, hipStream_t s) {
-    const dim3 grid((unsigned)a.tokens, (unsigned)a.heads);
-    if (bf16 && d == 128) hipLaunchKernelGGL((kda_cache4_attention_kernel<__bf16, 128>), grid, dim3(64), 0, s, a);
-    else if (bf16) hipLaunchKernelGGL((kda_cache4_attention_kernel<__bf16, 64>), grid, dim3(64), 0, s, a);
-    else if (d == 128) hipLaunchKernelGGL((kda_cache4_attention_kernel<float, 128>), grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL((kda_cache4_attention_kernel<float, 64>), grid, dim3(64), 0, s, a);
-    return hipGetLastError();
+hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
+    if (bf16) return d == 128 ? launch_attention_t<__bf16, 128>(a, ws, s) : launch_attention_t<__bf16, 64>(a, ws, s);
+    return d == 128 ? launch_attention_t<float, 128>(a, ws, s) : launch_attention_t<float, 64>(a, ws, s);
 }
 
 }  // namespace kda

@@ -186,7 +186,7 @@ kda_status kda_cache4_read(const kda_cache4* c, int64_t tokens, kda_dtype io_dty
 
 size_t kda_cache4_attention_workspace_size(const kda_cache4* c, const kda_cache4_attention_problem* p) {
     if (check_attention(c, p) != KDA_OK || no_rows(p)) return 0;
-    return cache4_attention_workspace_bytes(c->d, attention_args(c, p));
+    return cache4_attention_workspace_bytes(p->io_dtype == KDA_BF16, c->d, attention_args(c, p));
 }
 
 kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_problem* p, const void* q,

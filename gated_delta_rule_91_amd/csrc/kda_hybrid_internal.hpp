@@ -96,7 +96,7 @@ struct RecurrenceStepArgs {
 hipError_t launch_plan(const PlanArgs& a, hipStream_t s);
 hipError_t launch_cache4_append(bool bf16, int d, const Cache4RowsArgs& a, hipStream_t s);
 hipError_t launch_cache4_read(bool bf16, int d, const Cache4RowsArgs& a, hipStream_t s);
-size_t cache4_attention_workspace_bytes(int d, const Cache4AttentionArgs& a);
+size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a);
 hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s);
 // backward: the workspace of the training pair; else of the prefill alone
 size_t recurrence_workspace_bytes(int64_t B, int64_t T, int64_t D, bool backward);
