@@ -161,6 +161,15 @@ __device__ __forceinline__ void two_channels(const uint32_t (&w)[8], const float
     hi = __builtin_bit_cast(bf16x8, b);
 }
 
+// The largest over the four lanes with the same n.
+__device__ __forceinline__ float over_g(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+    const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
 // x in PARTS bf16 parts whose sum holds 8 PARTS bits of it.
 template <int PARTS>
 __device__ __forceinline__ void parts_of(float x, __bf16 (&p)[PARTS]) {
@@ -181,14 +190,33 @@ struct Tile {
     bool ok[2];                 // the half's page exists
 };
 
+// The block table of a sequence, 64 entries at a time in the lanes of a wave,
+// so that a tile's pages cost no memory access.
+struct Pages {
+    const int32_t* table;
+    int most, shift, base, mine;
+    __device__ __forceinline__ Pages(const Cache4AttentionArgs& a, int64_t s, int t)
+        : table(a.block_table + s * a.max_pages), most(a.max_pages), shift(a.c.page_shift) { fill(t >> shift); }
+    __device__ __forceinline__ void fill(int first) {
+        base = first;
+        const int i = first + (int)(threadIdx.x & 63);
+        mine = i < most ? table[i] : -1;
+    }
+    __device__ __forceinline__ int of(int t) {
+        const int i = t >> shift;
+        if (i - base > 63) fill(i);
+        return __builtin_amdgcn_readlane(mine, i - base);
+    }
+};
+
 template <int D>
-__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, const int32_t* table, int kvh, int t0, int total,
+__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int total,
                                           int lane, Tile<D>& x) {
     const int g = lane >> 4, n = lane & 15;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int t = t0 + 16 * u;
-        int64_t page = t < total ? table[t >> a.c.page_shift] : -1;
+        const int64_t page = t < total ? pages.of(t) : -1;
         x.ok[u] = page >= 0 && page < a.c.pages;
         if (x.ok[u]) {
             const int64_t row = ((page * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
@@ -233,7 +261,7 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
     for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const bool in = t0 + 16 * u + 4 * g + v < end;
+            const bool in = t0 + 32 <= end || t0 + 16 * u + 4 * g + v < end;
             uint32_t b, c;
             if constexpr (D == 128) {
                 b = x.vs[u][v] >> (8 * (n >> 2)) & 255u;
@@ -248,7 +276,7 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
 }
 
 template <typename E, int D, int R, bool SPLITW>
-__global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, float* part_o,
+__global__ __launch_bounds__(kWaves * 64, 2) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, float* part_o,
                                                                            float* part_ml) {
     constexpr int PARTS = sizeof(E) == 2 ? 1 : 3;
     constexpr int KS = D / 32;          // MFMA steps over the channels
@@ -271,8 +299,14 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
     const int lo = split * (int64_t)piece < b.total ? split * piece : b.total;
     const int hi = last < row0 ? lo : min(end_of(a, b, last), (int)min((int64_t)lo + piece, (int64_t)b.total));
     // every wave of a workgroup that shares rows sees the same range
-    if (SPLITW && l.nsplit > 1 && (hi <= lo || (int64_t)split * piece >= b.total)) return;
+    if (split > 0 && hi <= lo && (SPLITW || end_of(a, b, min(b.begin + l.rows, n_rows) - 1) <= lo)) return;
     const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
+
+    // scores in powers of two, with the sign of the scale in the queries, so
+    // that the largest product is the largest score; not 0, which would make
+    // NaN of a masked score's -inf
+    const float to_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
 
     // queries: row n of each 16, channels [PER g, PER g + PER)
     bf16x8 q[R][KS][PARTS];
@@ -287,10 +321,10 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if constexpr (PARTS == 1) {
-                    q[r][j][0][e] = p[8 * j + e];
+                    q[r][j][0][e] = (__bf16)(sign * to_f32(p[8 * j + e]));
                 } else {
                     __bf16 s[PARTS];
-                    parts_of<PARTS>(p[8 * j + e], s);
+                    parts_of<PARTS>(sign * p[8 * j + e], s);
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) q[r][j][i][e] = s[i];
                 }
@@ -306,16 +340,15 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
 #pragma unroll
         for (int j = 0; j < VJ; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    const float to_log2 = a.scale * kLog2e;
-    const int32_t* table = a.block_table + b.s * a.max_pages;
+    Pages pages(a, b.s, lo);
 
     constexpr int STEP = SPLITW ? 32 * kWaves : 32;
     Tile<D> next;
     int t0 = lo + (SPLITW ? 32 * wave : 0);
-    if (t0 < hi) load_tile<D>(a, table, kvh, t0, hi, lane, next);
+    if (t0 < hi) load_tile<D>(a, pages, kvh, t0, hi, lane, next);
     for (; t0 < hi; t0 += STEP) {
         const Tile<D> x = next;
-        if (t0 + STEP < hi) load_tile<D>(a, table, kvh, t0 + STEP, hi, lane, next);
+        if (t0 + STEP < hi) load_tile<D>(a, pages, kvh, t0 + STEP, hi, lane, next);
         const bool whole = x.ok[0] && x.ok[1] && t0 + 32 <= all_see && t0 + 32 <= hi;
 
         bf16x8 k[2][KS];
@@ -335,7 +368,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][j], q[r][j][i], acc, 0, 0, 0);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[4 * u + v] = acc[v] * to_log2;
+                for (int v = 0; v < 4; ++v) y[4 * u + v] = acc[v];
             }
             if (!whole) {
 #pragma unroll
@@ -347,8 +380,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
                     }
             }
             float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = over_g(top) * to_log2;
             if (__any(top > m[r] + kSlack)) {
                 const float mn = fmaxf(m[r], top);
                 const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
@@ -360,7 +392,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
             const float base = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y[e] = __builtin_amdgcn_exp2f(y[e] - base);
+                y[e] = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
                 sum[r] += y[e];
                 if constexpr (PARTS == 1) {
                     p[r][0][e] = (__bf16)y[e];
@@ -375,7 +407,28 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
 
         uint32_t w[8];
         float s[8];
-        auto accumulate = [&](const bf16x8 (&pp)[R][PARTS]) {
+        bool odd = false;       // a value that is no number, where some rows do not see it
+        if (!whole) {
+            values_of<D>(x, t0, hi, lane, w, s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
+        }
+        const bool apart = __any(odd);
+        // Where apart, one end at a time, with the tokens behind it cleared: 0
+        // times NaN would reach rows that do not see it.
+        for (int stop = apart ? t0 + 1 : hi;; ++stop) {
+            values_of<D>(x, t0, stop, lane, w, s);
+            bf16x8 pe[R][PARTS];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t use = !apart || min(end[r], hi) == stop || (stop == t0 + 32 && min(end[r], hi) > stop) ? ~0u : 0u;
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
+                    z &= use;
+                    pe[r][i] = __builtin_bit_cast(bf16x8, z);
+                }
+            }
             auto pair = [&](auto I) {
                 bf16x8 c[2];
                 two_channels<decltype(I)::value>(w, s, c[0], c[1]);
@@ -385,7 +438,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
                     for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int i = 0; i < PARTS; ++i)
-                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pp[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pe[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
             };
             pair(std::integral_constant<int, 0>{});
             pair(std::integral_constant<int, 1>{});
@@ -393,35 +446,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
                 pair(std::integral_constant<int, 2>{});
                 pair(std::integral_constant<int, 3>{});
             }
-        };
-        values_of<D>(x, t0, hi, lane, w, s);
-        bool odd = false;       // a value that is no number, where some rows do not see it
-        if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
-        }
-        if (!__any(odd)) {
-            accumulate(p);
-        } else {
-            // one end at a time, with the tokens behind it cleared: 0 times NaN would reach rows that do not see it
-            for (int e = max(t0, 0); e < t0 + 32; ++e) {
-                const int stop = e + 1;
-                bf16x8 pe[R][PARTS];
-                bool some = false;
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int mine = min(max(end[r], 0), min(hi, t0 + 32));
-                    const bool use = mine == stop;
-                    some = some || use;
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) pe[r][i][c] = use ? p[r][i][c] : (__bf16)0.f;
-                }
-                if (!__any(some)) continue;
-                values_of<D>(x, t0, stop, lane, w, s);
-                accumulate(pe);
-            }
+            if (!apart || stop == t0 + 32) break;
         }
     }
 
@@ -431,10 +456,10 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
         sum[r] += __shfl_xor(sum[r], 32);
     }
 
-    // what a row's result becomes: a part of a split sequence, or the output
-    auto put = [&](int row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
+    // what a row's result becomes: one of several parts, or the output
+    auto put = [&](int row, int end_row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
         const int64_t at = place_of(a, b, kvh, row);
-        if (l.nsplit > 1) {
+        if (end_row > piece) {
             const int64_t i = (int64_t)split * a.tokens * a.heads + at;
             float* po = part_o + i * D + c0;
             *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
@@ -460,14 +485,14 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = row0 + 16 * r + n;
-            if (row >= n_rows || (l.nsplit > 1 && end[r] <= lo)) continue;
+            if (row >= n_rows || (split > 0 && end[r] <= lo)) continue;
             // element (j, v) of the result is channel PER g + VJ v + j
 #pragma unroll
             for (int c = 0; c < PER; c += 8) {
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = o[r][(c + e) % VJ][(c + e) / VJ];
-                put(row, PER * g + c, y, m[r], sum[r]);
+                put(row, end[r], PER * g + c, y, m[r], sum[r]);
             }
         }
     } else {
@@ -504,28 +529,32 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_attention_kernel(Cache
         }
         for (int i = threadIdx.x; i < ROWS * (D / 8); i += kWaves * 64) {
             const int r = i / (D / 8), c0 = i % (D / 8) * 8, row = row0 + r;
-            if (row >= n_rows || (l.nsplit > 1 && end_of(a, b, row) <= lo)) continue;
+            const int end_row = end_of(a, b, row);
+            if (row >= n_rows || (split > 0 && end_row <= lo)) continue;
             float mx = -INFINITY, sum_r = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 if (sm[w][r] != -INFINITY) sum_r += ss[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - mx);
-            put(row, c0, &so[r][c0], mx, sum_r);
+            put(row, end_row, c0, &so[r][c0], mx, sum_r);
         }
     }
 }
 
-// Joins the pieces of one (row, head): weights 2^(m_i - max m), in the order of
-// the pieces.  A quarter of them each wave, whose sums are joined through LDS.
-template <typename E, int D>
+// Joins the pieces of a (row, head): weights 2^(m_i - max m).  WAVES waves
+// take turns at the pieces of one, and their sums are joined through LDS in
+// the order of the waves.
+template <typename E, int D, int WAVES>
 __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, const float* part_o,
                                                                          const float* part_ml) {
     constexpr int PER = D / 64;
-    extern __shared__ float weight[];                  // [nsplit]
-    __shared__ float red[kWaves], acc[kWaves][D];
+    __shared__ float acc[kWaves][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t at = blockIdx.x, row = at / a.heads;
+    const int64_t at = (int64_t)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
+    const int turn = wave % WAVES;
+    if (at >= a.tokens * a.heads) return;              // WAVES < kWaves: no barrier below
+    const int64_t row = at / a.heads;
     int64_t s = row;
     if (a.cu_seqlens) {
         int64_t lo = 0, hi = a.n_seq;
@@ -540,49 +569,56 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     if (row < b.row0 || row >= b.row0 + b.queries) return;
     const int end = end_of(a, b, (int)(row - b.row0) * a.group);
     const int piece = piece_of(l, b.total);
+    if (end <= piece) return;                          // written already
     const int count = (int)min((int64_t)l.nsplit, ((int64_t)end + piece - 1) / piece);
     const int64_t stride = a.tokens * a.heads;
 
     float mx = -INFINITY;
-    for (int i = threadIdx.x; i < count; i += kWaves * 64) mx = fmaxf(mx, part_ml[2 * (i * stride + at)]);
+    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_ml[2 * (i * stride + at)]);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-    if (lane == 0) red[wave] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    float sum = 0.f;
-    for (int i = threadIdx.x; i < count; i += kWaves * 64) {
-        const float mi = part_ml[2 * (i * stride + at)];
-        const float w = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mx);
-        weight[i] = w;
-        sum += w * part_ml[2 * (i * stride + at) + 1];
+    float sum = 0.f, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int i0 = 0; i0 < count; i0 += 64) {
+        float w = 0.f;
+        if (i0 + lane < count) {
+            const float mi = part_ml[2 * ((i0 + lane) * stride + at)];
+            w = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mx);
+            sum += w * part_ml[2 * ((i0 + lane) * stride + at) + 1];
+        }
+        const int most = min(count - i0, 64);
+#pragma unroll 8
+        for (int k = turn; k < most; k += WAVES) {
+            const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
+            const float* p = part_o + ((i0 + k) * stride + at) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] += wk * p[e];
+        }
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
-    if (lane == 0) red[wave] = sum;
-    __syncthreads();
-    sum = red[0] + red[1] + red[2] + red[3];
-    float o[PER];
+    if constexpr (WAVES > 1) {
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    for (int i = wave; i < count; i += kWaves) {
-        const float w = weight[i];
-        const float* p = part_o + (i * stride + at) * D + lane * PER;
+        for (int e = 0; e < PER; ++e) acc[wave][lane * PER + e] = o[e];
+        __syncthreads();
+        if (turn != 0) return;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] += w == 0.f ? 0.f : w * p[e];
+        for (int k = 1; k < WAVES; ++k)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] += acc[wave + k][lane * PER + e];
     }
+    float y[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[wave][lane * PER + e] = o[e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-        const int c = threadIdx.x;
-        float y = acc[0][c] + acc[1][c] + acc[2][c] + acc[3][c];
-        y = sum == 0.f ? 0.f : y / sum;
-        if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[at * D + c]));
-        reinterpret_cast<E*>(a.out)[at * D + c] = from_f32<E>(y);
+    for (int e = 0; e < PER; ++e) {
+        const int64_t i = at * D + lane * PER + e;
+        y[e] = sum == 0.f ? 0.f : o[e] / sum;
+        if (a.g) y[e] *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
+        reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y[e]);
     }
 }
+
+constexpr int kWideCombine = 16;       // pieces from which on four waves join those of a row
 
 constexpr int kSplitMaxRows = 32;      // rows that the waves of a workgroup share
 
@@ -645,8 +681,13 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
     else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, part_o, part_ml, s);
     else e = launch_attention_r<E, D, 2, true>(a, p, part_o, part_ml, s);
     if (e != hipSuccess || p.l.nsplit == 1) return e;
-    hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D>), dim3((unsigned)(a.tokens * a.heads)), dim3(kWaves * 64),
-                       p.l.nsplit * sizeof(float), s, a, p.l, part_o, part_ml);
+    const int64_t joined = a.tokens * a.heads;
+    if (p.l.nsplit > kWideCombine)
+        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), dim3((unsigned)joined), dim3(kWaves * 64), 0, s, a, p.l, part_o,
+                           part_ml);
+    else
+        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1>), dim3((unsigned)((joined + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0,
+                           s, a, p.l, part_o, part_ml);
     return hipGetLastError();
 }
 
