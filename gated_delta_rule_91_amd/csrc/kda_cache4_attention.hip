@@ -24,9 +24,12 @@
 // probabilities are taken in three bf16 parts, which together hold 24 bits.
 //
 // Few rows (decode): the four waves of a workgroup take turns at the 32-token
-// tiles and join their results through LDS, and a sequence is split into
-// pieces over workgroups, joined by a second kernel.  Many rows: each wave has
-// rows of its own.
+// tiles and join their results through LDS.  Many rows: each wave has rows of
+// its own.  Sequences are ragged and a query's tokens grow along a prompt, so
+// work is dealt out by tokens: the row blocks' tokens lie end to end in units
+// of 128, and each workgroup takes the same number of units, which may end one
+// block, hold several and begin another.  What a workgroup has of a block
+// that it does not hold whole is a part; a second kernel joins the parts.
 #include <type_traits>
 
 #include "kda_common.hpp"
@@ -46,13 +49,26 @@ constexpr float kSlack = 8.f;
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kUnit = 128;         // tokens that are dealt out at once
+constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
+
 // How the work is laid out (host and kernels).
 struct Layout {
-    int rows;        // rows of a workgroup
+    int rows;        // rows of a block
     int64_t slots;   // upper bound of row blocks over all sequences
     int per_seq;     // without offsets: row blocks of each sequence
-    int nsplit;      // pieces of a sequence
-    int piece;       // tokens of a piece, at least (a multiple of 128)
+    int groups;      // workgroups of a key/value head that units are dealt to; 0: a block each
+};
+
+// Where the second kernel finds the parts: before[slot] units lie before a
+// row block, workgroup w has the units [w * each, (w + 1) * each) and two
+// parts at most, 2 w of a block that began before and 2 w + 1 of one that
+// begins in it.  Part i of row r of a block and key/value head h is at
+// (i * heads + h) * rows + r.
+struct Parts {
+    int32_t* before;     // [slots + 1], then each
+    float* sums;         // maximum and sum
+    float* o;            // D channels
 };
 
 struct Block {
@@ -122,14 +138,43 @@ __device__ __forceinline__ int end_of(const Cache4AttentionArgs& a, const Block&
     return (int)(end < 0 ? 0 : (end > b.total ? b.total : end));
 }
 
-__device__ __forceinline__ int piece_of(const Layout& l, int total) {
-    const int even = (int)((((int64_t)total + l.nsplit - 1) / l.nsplit + 127) / 128 * 128);
-    return even > l.piece ? even : l.piece;
-}
-
 // Index of (row of q, head) of row r.
 __device__ __forceinline__ int64_t place_of(const Cache4AttentionArgs& a, const Block& b, int kvh, int r) {
     return (b.row0 + r / a.group) * a.heads + kvh * a.group + r % a.group;
+}
+
+// before[i]: units of the row blocks before i, i <= slots; returns all of them.
+// A block with rows has one unit at least, whose output may be zeros.
+__device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* before) {
+    __shared__ int32_t part[kWaves];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int sum = 0;
+    for (int base = 0; base < l.slots; base += kWaves * 64) {
+        int c = 0;
+        if (base + t < l.slots) {
+            const Block b = block_of(a, l, base + t);
+            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.queries * a.group) - 1) + kUnit - 1) / kUnit, 1);
+        }
+        int in = c;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int u = __shfl_up(in, off);
+            if (lane >= off) in += u;
+        }
+        if (lane == 63) part[wave] = in;
+        __syncthreads();
+        int ahead = sum;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) ahead += part[w];
+            sum += part[w];
+        }
+        if (base + t < l.slots) before[base + t] = ahead + in - c;
+        __syncthreads();
+    }
+    if (t == 0) before[l.slots] = sum;
+    __syncthreads();
+    return sum;
 }
 
 __device__ __forceinline__ float scale_bits(uint32_t byte) { return __uint_as_float(byte << 23); }
@@ -275,31 +320,68 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
         }
 }
 
+// Waves per SIMD that registers are kept for: what fits without spilling.
+template <typename E, int D, int R> constexpr int waves_of() {
+    if (sizeof(E) == 2) return R == 1 ? 3 : 2;
+    return R == 2 && D == 128 ? 1 : 2;
+}
+
 template <typename E, int D, int R, bool SPLITW>
-__global__ __launch_bounds__(kWaves * 64, 2) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, float* part_o,
-                                                                           float* part_ml) {
+__global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
     constexpr int PARTS = sizeof(E) == 2 ? 1 : 3;
     constexpr int KS = D / 32;          // MFMA steps over the channels
     constexpr int VJ = D / 16;          // MFMAs of a value tile
     constexpr int PER = D / 4;          // channels of a lane's result
     constexpr int ROWS = 16 * R;        // rows of a wave
+    constexpr int LD = D + 4;
+    __shared__ float so[SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
+    extern __shared__ int32_t before[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, n = lane & 15;
 
     // key/value heads alternate fastest, so workgroups that share keys and
     // values lie on one XCD where there are 8 heads
-    const int64_t id = blockIdx.x;
-    const int kvh = (int)(id % a.c.heads);
-    const int split = (int)(id / a.c.heads % l.nsplit);
-    const Block b = block_of(a, l, id / a.c.heads / l.nsplit);
-    if (!b.any) return;
-    const int piece = piece_of(l, b.total);
+    const int kvh = (int)(blockIdx.x % a.c.heads), group = (int)(blockIdx.x / a.c.heads);
+    int64_t slot = group;
+    int at = 0, stop = 1, each = 1;     // this workgroup's units
+    if (l.groups > 0) {
+        const int all = deal_out(a, l, before);
+        each = max((all + l.groups - 1) / l.groups, 1);
+        if (blockIdx.x == 0) {
+            for (int i = threadIdx.x; i <= l.slots; i += kWaves * 64) parts.before[i] = before[i];
+            if (threadIdx.x == 0) parts.before[l.slots + 1] = each;
+        }
+        at = (int)min((int64_t)group * each, (int64_t)all);
+        stop = min(at + each, all);
+        int lo = 0, hi = (int)l.slots;  // the last block that begins at or before `at`: empty ones lie before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= at) lo = mid; else hi = mid;
+        }
+        slot = __builtin_amdgcn_readfirstlane(lo);
+        at = __builtin_amdgcn_readfirstlane(at);
+        stop = __builtin_amdgcn_readfirstlane(stop);
+    }
+
+    for (; at < stop; ++slot) {
+    const Block b = block_of(a, l, slot);
+    int lo = 0, lim = b.total, whole_block = 1;
+    if (l.groups > 0) {
+        const int p0 = __builtin_amdgcn_readfirstlane(before[slot]), p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
+        if (p1 == p0) continue;         // no rows
+        const int to = min(stop, p1);
+        lo = (at - p0) * kUnit;
+        lim = min(b.total, (to - p0) * kUnit);
+        whole_block = at == p0 && to == p1;
+        at = to;
+    } else {
+        at = stop;
+        if (!b.any) continue;
+    }
+    const int part = whole_block ? -1 : 2 * group + (lo == 0 ? 1 : 0);
     const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
     const int n_rows = b.queries * a.group;
     const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
-    const int lo = split * (int64_t)piece < b.total ? split * piece : b.total;
-    const int hi = last < row0 ? lo : min(end_of(a, b, last), (int)min((int64_t)lo + piece, (int64_t)b.total));
-    // every wave of a workgroup that shares rows sees the same range
-    if (split > 0 && hi <= lo && (SPLITW || end_of(a, b, min(b.begin + l.rows, n_rows) - 1) <= lo)) return;
+    const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
     const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
 
     // scores in powers of two, with the sign of the scale in the queries, so
@@ -456,17 +538,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kda_cache4_attention_kernel(Ca
         sum[r] += __shfl_xor(sum[r], 32);
     }
 
-    // what a row's result becomes: one of several parts, or the output
-    auto put = [&](int row, int end_row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
-        const int64_t at = place_of(a, b, kvh, row);
-        if (end_row > piece) {
-            const int64_t i = (int64_t)split * a.tokens * a.heads + at;
-            float* po = part_o + i * D + c0;
+    // what a row's result becomes: a part, or the output
+    auto put = [&](int row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
+        if (part >= 0) {
+            const int64_t i = ((int64_t)part * a.c.heads + kvh) * l.rows + (row - b.begin);
+            float* po = parts.o + i * D + c0;
             *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
             *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
-            if (c0 == 0) { part_ml[2 * i] = mx; part_ml[2 * i + 1] = sm; }
+            if (c0 == 0) { parts.sums[2 * i] = mx; parts.sums[2 * i + 1] = sm; }
             return;
         }
+        const int64_t at = place_of(a, b, kvh, row);
         const float f = sm == 0.f ? 0.f : 1.f / sm;
         float z[8];
 #pragma unroll
@@ -485,20 +567,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kda_cache4_attention_kernel(Ca
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = row0 + 16 * r + n;
-            if (row >= n_rows || (split > 0 && end[r] <= lo)) continue;
+            if (row >= n_rows) continue;
             // element (j, v) of the result is channel PER g + VJ v + j
 #pragma unroll
             for (int c = 0; c < PER; c += 8) {
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = o[r][(c + e) % VJ][(c + e) / VJ];
-                put(row, end[r], PER * g + c, y, m[r], sum[r]);
+                put(row, PER * g + c, y, m[r], sum[r]);
             }
         }
     } else {
         // join the waves' results, in their order
-        constexpr int LD = D + 4;
-        __shared__ float so[ROWS][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
         if (g == 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r) { sm[wave][16 * r + n] = m[r]; ss[wave][16 * r + n] = sum[r]; }
@@ -529,25 +609,25 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kda_cache4_attention_kernel(Ca
         }
         for (int i = threadIdx.x; i < ROWS * (D / 8); i += kWaves * 64) {
             const int r = i / (D / 8), c0 = i % (D / 8) * 8, row = row0 + r;
-            const int end_row = end_of(a, b, row);
-            if (row >= n_rows || (split > 0 && end_row <= lo)) continue;
+            if (row >= n_rows) continue;
             float mx = -INFINITY, sum_r = 0.f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 if (sm[w][r] != -INFINITY) sum_r += ss[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - mx);
-            put(row, end_row, c0, &so[r][c0], mx, sum_r);
+            put(row, c0, &so[r][c0], mx, sum_r);
         }
+        __syncthreads();                // before the next block's results
+    }
     }
 }
 
-// Joins the pieces of a (row, head): weights 2^(m_i - max m).  WAVES waves
-// take turns at the pieces of one, and their sums are joined through LDS in
-// the order of the waves.
+// Joins the parts of a (row, head): weights 2^(m_i - max m).  WAVES waves take
+// turns at the parts of one, and their sums are joined through LDS in the
+// order of the waves.
 template <typename E, int D, int WAVES>
-__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, const float* part_o,
-                                                                         const float* part_ml) {
+__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
     constexpr int PER = D / 64;
     __shared__ float acc[kWaves][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -555,6 +635,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     const int turn = wave % WAVES;
     if (at >= a.tokens * a.heads) return;              // WAVES < kWaves: no barrier below
     const int64_t row = at / a.heads;
+    const int head = (int)(at % a.heads), kvh = head / a.group;
     int64_t s = row;
     if (a.cu_seqlens) {
         int64_t lo = 0, hi = a.n_seq;
@@ -567,14 +648,18 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     Block b;
     sequence_of(a, s, b);
     if (row < b.row0 || row >= b.row0 + b.queries) return;
-    const int end = end_of(a, b, (int)(row - b.row0) * a.group);
-    const int piece = piece_of(l, b.total);
-    if (end <= piece) return;                          // written already
-    const int count = (int)min((int64_t)l.nsplit, ((int64_t)end + piece - 1) / piece);
-    const int64_t stride = a.tokens * a.heads;
+    const int r = (int)(row - b.row0) * a.group + head % a.group;
+    const int64_t slot = (a.cu_seqlens ? first_slot(a, l, s) : s * l.per_seq) + r / l.rows;
+    if (slot < 0 || slot >= l.slots) return;           // offsets out of order
+    const int each = parts.before[l.slots + 1], p0 = parts.before[slot], p1 = parts.before[slot + 1];
+    const int w0 = p0 / each, count = (p1 - 1) / each - w0 + 1;
+    if (p1 <= p0 || count < 2) return;                 // written already
+    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r % l.rows;
+    const int64_t rest = ((int64_t)(2 * w0) * a.c.heads + kvh) * l.rows + r % l.rows, stride = 2 * (int64_t)a.c.heads * l.rows;
+    auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
 
     float mx = -INFINITY;
-    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, part_ml[2 * (i * stride + at)]);
+    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, parts.sums[2 * place(i)]);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
     float sum = 0.f, o[PER];
@@ -583,15 +668,15 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     for (int i0 = 0; i0 < count; i0 += 64) {
         float w = 0.f;
         if (i0 + lane < count) {
-            const float mi = part_ml[2 * ((i0 + lane) * stride + at)];
+            const float mi = parts.sums[2 * place(i0 + lane)];
             w = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mx);
-            sum += w * part_ml[2 * ((i0 + lane) * stride + at) + 1];
+            sum += w * parts.sums[2 * place(i0 + lane) + 1];
         }
         const int most = min(count - i0, 64);
 #pragma unroll 8
         for (int k = turn; k < most; k += WAVES) {
             const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
-            const float* p = part_o + ((i0 + k) * stride + at) * D + lane * PER;
+            const float* p = parts.o + place(i0 + k) * D + lane * PER;
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] += wk * p[e];
         }
@@ -608,19 +693,19 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
 #pragma unroll
             for (int e = 0; e < PER; ++e) o[e] += acc[wave + k][lane * PER + e];
     }
-    float y[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         const int64_t i = at * D + lane * PER + e;
-        y[e] = sum == 0.f ? 0.f : o[e] / sum;
-        if (a.g) y[e] *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
-        reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y[e]);
+        float y = sum == 0.f ? 0.f : o[e] / sum;
+        if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
+        reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y);
     }
 }
 
-constexpr int kWideCombine = 16;       // pieces from which on four waves join those of a row
-
 constexpr int kSplitMaxRows = 32;      // rows that the waves of a workgroup share
+// (row, head) pairs below which four waves join the parts of each: few pairs
+// have many parts, many have few
+constexpr int64_t kWideCombine = 2048;
 
 // bf16 rows of a wave in the many-rows form; fp32 takes three times the
 // registers for its queries
@@ -642,30 +727,30 @@ Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
     // with or without offsets: enough slots for both
     p.l.slots = a.tokens * a.group / p.l.rows + a.n_seq;
     if (a.n_seq * p.l.per_seq > p.l.slots) p.l.slots = a.n_seq * p.l.per_seq;
+    // as many workgroups as run at once, but none for less than a unit of
+    // every block's longest
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
     const int64_t len = a.max_len < cap ? a.max_len : cap;
-    const int64_t base = p.l.slots * a.c.heads;
-    // Few rows: pieces of at most 1024 tokens, so that ragged sequences even
-    // out, and down to 128 until about 1024 workgroups run.  Many rows: split
-    // only what leaves the card empty, since parts cost as much as outputs.
-    int64_t piece = p.splitw ? 1024 : (len > 0 ? len : 1);
-    const int64_t target = p.splitw ? 1024 : 512;
-    if (base * ((len + piece - 1) / piece) < target) piece = len * base / target;
-    piece = (piece + 127) / 128 * 128;
-    if (piece < 128) piece = 128;
-    int64_t n = (len + piece - 1) / piece;
-    if (n > INT32_MAX / base) n = INT32_MAX / base;
-    p.l.nsplit = (int)(n < 1 ? 1 : (n > 1024 ? 1024 : n));
-    p.l.piece = (int)(piece > (1 << 30) ? (1 << 30) : piece);
+    const int64_t units = p.l.slots * ((len + kUnit - 1) / kUnit);
+    int64_t groups = ((p.splitw ? 768 : 512) + a.c.heads - 1) / a.c.heads;
+    groups = groups < units ? groups : units;
+    const bool dealt = p.l.slots <= kMaxDealt && p.l.slots * (cap / kUnit + 1) <= INT32_MAX;
+    p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
     return p;
 }
 
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+size_t before_bytes(const Plan& p) { return round256((size_t)(p.l.slots + 2) * sizeof(int32_t)); }
+size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
+    return 2 * (size_t)p.l.groups * (size_t)a.c.heads * (size_t)p.l.rows;
+}
+
 template <typename E, int D, int R, bool SPLITW>
-hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, float* part_o, float* part_ml, hipStream_t s) {
-    const int64_t blocks = p.l.slots * a.c.heads * p.l.nsplit;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), 0, s, a, p.l,
-                       part_o, part_ml);
+hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, const Parts& parts, hipStream_t s) {
+    const int64_t blocks = (p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
+    const unsigned lds = p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * sizeof(int32_t) : 0;
+    hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), lds, s, a, p.l,
+                       parts);
     return hipGetLastError();
 }
 
@@ -673,21 +758,23 @@ template <typename E, int D>
 hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
     constexpr bool bf16 = sizeof(E) == 2;
     const Plan p = plan_of(bf16, a);
-    const int64_t places = (int64_t)p.l.nsplit * a.tokens * a.heads;
-    float* part_o = reinterpret_cast<float*>(ws);
-    float* part_ml = part_o + places * D;
+    Parts parts = {};
+    if (p.l.groups > 0) {
+        parts.before = reinterpret_cast<int32_t*>(ws);
+        parts.o = reinterpret_cast<float*>(ws + before_bytes(p));
+        parts.sums = parts.o + part_places(a, p) * D;
+    }
     hipError_t e;
-    if (!p.splitw) e = launch_attention_r<E, D, rows_r(bf16), false>(a, p, part_o, part_ml, s);
-    else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, part_o, part_ml, s);
-    else e = launch_attention_r<E, D, 2, true>(a, p, part_o, part_ml, s);
-    if (e != hipSuccess || p.l.nsplit == 1) return e;
+    if (!p.splitw) e = launch_attention_r<E, D, rows_r(bf16), false>(a, p, parts, s);
+    else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, parts, s);
+    else e = launch_attention_r<E, D, 2, true>(a, p, parts, s);
+    if (e != hipSuccess || p.l.groups < 2) return e;
     const int64_t joined = a.tokens * a.heads;
-    if (p.l.nsplit > kWideCombine)
-        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), dim3((unsigned)joined), dim3(kWaves * 64), 0, s, a, p.l, part_o,
-                           part_ml);
+    if (joined < kWideCombine)
+        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), dim3((unsigned)joined), dim3(kWaves * 64), 0, s, a, p.l, parts);
     else
         hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1>), dim3((unsigned)((joined + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0,
-                           s, a, p.l, part_o, part_ml);
+                           s, a, p.l, parts);
     return hipGetLastError();
 }
 
@@ -695,8 +782,8 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
 
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
     const Plan p = plan_of(bf16, a);
-    if (p.l.nsplit == 1) return 0;
-    return (size_t)p.l.nsplit * (size_t)(a.tokens * a.heads) * (size_t)(d + 2) * sizeof(float);
+    if (p.l.groups == 0) return 0;
+    return before_bytes(p) + part_places(a, p) * (size_t)(d + 2) * sizeof(float);
 }
 
 hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
