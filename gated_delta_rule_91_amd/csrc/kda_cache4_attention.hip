@@ -55,7 +55,7 @@ constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; m
 // How the work is laid out (host and kernels).
 struct Layout {
     int rows;        // rows of a block
-    int64_t slots;   // upper bound of row blocks over all sequences
+    int slots;       // upper bound of row blocks over all sequences
     int per_seq;     // without offsets: row blocks of each sequence
     int groups;      // workgroups of a key/value head that units are dealt to; 0: a block each
 };
@@ -72,75 +72,78 @@ struct Parts {
 };
 
 struct Block {
-    int64_t s;       // sequence
-    int64_t row0;    // its first query's row of q
-    int queries;
+    int s;           // sequence
+    int row0;        // its first query's row of q
+    int n_rows;      // (query, head of the group) pairs of the sequence
     int total;       // tokens that count (at most what the table holds)
     int first;       // position of the first query, may be negative
-    int begin;       // first (query, head) row of this block
+    int begin;       // first pair of this block
     bool any;
 };
 
-__device__ __forceinline__ int cap_tokens(const Cache4AttentionArgs& a) { return a.max_pages << a.c.page_shift; }
-
 // What sequence s is.
-__device__ __forceinline__ void sequence_of(const Cache4AttentionArgs& a, int64_t s, Block& b) {
+__device__ __forceinline__ void sequence_of(const Cache4AttentionArgs& a, int s, Block& b) {
     int64_t r0 = s, r1 = s + 1;
     if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.tokens, r0, r1);
-    const int64_t total = a.total_lens[s] > 0 ? a.total_lens[s] : 0;
+    const int total = max(a.total_lens[s], 0), queries = (int)(r1 - r0);
     b.s = s;
-    b.row0 = r0;
-    b.queries = (int)(r1 - r0);
-    const int64_t first = total - b.queries;
-    b.first = (int)first;
-    const int cap = cap_tokens(a);
-    b.total = (int)(total < cap ? total : cap);
+    b.row0 = (int)r0;
+    b.n_rows = queries * a.group;
+    b.first = total - queries;
+    b.total = min(total, a.max_pages << a.c.page_shift);
+}
+
+// The sequence that holds row `row` of q, with offsets: the last one that
+// begins at or before it.
+__device__ __forceinline__ int sequence_at(const Cache4AttentionArgs& a, int row) {
+    int lo = 0, hi = (int)a.n_seq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_seqlens[mid] <= row) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
 // Row blocks of sequence s with offsets begin at slot floor(cu[s] G / rows) + s,
 // which leaves each its ceil(m G / rows) slots and can be searched.
-__device__ __forceinline__ int64_t first_slot(const Cache4AttentionArgs& a, const Layout& l, int64_t s) {
-    int64_t c = a.cu_seqlens[s];
-    c = c < 0 ? 0 : (c > a.tokens ? a.tokens : c);
-    return c * a.group / l.rows + s;
+__device__ __forceinline__ int first_slot(const Cache4AttentionArgs& a, const Layout& l, int s) {
+    const int c = min(max(a.cu_seqlens[s], 0), (int)a.tokens);
+    return (int)((uint32_t)c * (uint32_t)a.group / (uint32_t)l.rows) + s;
 }
 
-__device__ __forceinline__ Block block_of(const Cache4AttentionArgs& a, const Layout& l, int64_t slot) {
-    Block b;
-    int64_t at;
+__device__ __forceinline__ Block block_of(const Cache4AttentionArgs& a, const Layout& l, int slot) {
+    Block b = {};
+    int at = 0;
     if (a.cu_seqlens) {
-        int64_t lo = 0, hi = a.n_seq;
+        int lo = 0, hi = (int)a.n_seq;
         while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
+            const int mid = (lo + hi) >> 1;
             if (first_slot(a, l, mid) <= slot) lo = mid; else hi = mid;
         }
         sequence_of(a, lo, b);
         at = slot - first_slot(a, l, lo);
     } else {
-        const int64_t s = slot / l.per_seq;
-        if (s >= a.n_seq) {         // more slots than row blocks
-            b = Block{};
-            return b;
-        }
+        const int s = l.per_seq == 1 ? slot : (int)((uint32_t)slot / (uint32_t)l.per_seq);
+        if (s >= a.n_seq) return b;         // more slots than row blocks
         sequence_of(a, s, b);
-        at = slot % l.per_seq;
+        at = slot - s * l.per_seq;
     }
-    const int64_t begin = at * l.rows;
-    b.any = begin >= 0 && begin < (int64_t)b.queries * a.group;
-    b.begin = b.any ? (int)begin : 0;
+    b.any = at >= 0 && (int64_t)at * l.rows < b.n_rows;
+    b.begin = b.any ? at * l.rows : 0;
     return b;
 }
 
 // Tokens that row r of a sequence sees.
 __device__ __forceinline__ int end_of(const Cache4AttentionArgs& a, const Block& b, int r) {
-    if (r >= b.queries * a.group) return 0;
-    const int64_t end = (int64_t)b.first + r / a.group + 1;
-    return (int)(end < 0 ? 0 : (end > b.total ? b.total : end));
+    if (r >= b.n_rows) return 0;
+    const int i = (int)((uint32_t)r / (uint32_t)a.group);
+    return min(max(b.first + i + 1, 0), b.total);
 }
 
 // Index of (row of q, head) of row r.
-__device__ __forceinline__ int64_t place_of(const Cache4AttentionArgs& a, const Block& b, int kvh, int r) {
-    return (b.row0 + r / a.group) * a.heads + kvh * a.group + r % a.group;
+__device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, const Block& b, int kvh, int r) {
+    const int i = (int)((uint32_t)r / (uint32_t)a.group);
+    return (b.row0 + i) * a.heads + kvh * a.group + (r - i * a.group);
 }
 
 // before[i]: units of the row blocks before i, i <= slots; returns all of them.
@@ -153,7 +156,7 @@ __device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* 
         int c = 0;
         if (base + t < l.slots) {
             const Block b = block_of(a, l, base + t);
-            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.queries * a.group) - 1) + kUnit - 1) / kUnit, 1);
+            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) + kUnit - 1) / kUnit, 1);
         }
         int in = c;
 #pragma unroll
@@ -254,69 +257,75 @@ struct Pages {
     }
 };
 
+// A half whose page does not exist reads page 0 (there is one: a cache without
+// pages counts no tokens) and is masked.
 template <int D>
-__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int total,
-                                          int lane, Tile<D>& x) {
-    const int g = lane >> 4, n = lane & 15;
+__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Tile<D>& x) {
+    const uint32_t g = lane >> 4, n = lane & 15;
+    const uint32_t ko = n * (D / 2) + g * (D / 8), kso = n * (D / 32) + g * (D / 32) / 4;
+    const uint32_t vo = 4 * g * (D / 2) + (D == 128 ? 4 * n : 4 * (n >> 1)), vso = 4 * g * (D / 32);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int t = t0 + 16 * u;
-        const int64_t page = t < total ? pages.of(t) : -1;
+        const int page = pages.of(t);
         x.ok[u] = page >= 0 && page < a.c.pages;
-        if (x.ok[u]) {
-            const int64_t row = ((page * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
-            const uint8_t* kp = a.c.k + row * (D / 2) + n * (D / 2) + g * (D / 8);
-            if constexpr (D == 128) {
-                const u32x4 w = *reinterpret_cast<const u32x4*>(kp);
+        const int64_t row = (((int64_t)(x.ok[u] ? page : 0) * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
+        const uint8_t *kp = a.c.k + row * (D / 2), *vp = a.c.v + row * (D / 2), *sp = a.c.v_scale + row * (D / 32);
+        if constexpr (D == 128) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(kp + ko), z = *reinterpret_cast<const u32x4*>(sp + vso);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x.k[u][j] = w[j];
-            } else {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(kp);
-                x.k[u][0] = w[0]; x.k[u][1] = w[1];
-            }
-            x.ks[u] = a.c.k_scale[row * (D / 32) + n * (D / 32) + g * (D / 32) / 4];
-            const uint8_t* vp = a.c.v + row * (D / 2) + 4 * g * (D / 2) + (D == 128 ? 4 * n : 4 * (n >> 1));
-#pragma unroll
-            for (int v = 0; v < 4; ++v) x.v[u][v] = *reinterpret_cast<const uint32_t*>(vp + v * (D / 2));
-            const uint8_t* sp = a.c.v_scale + row * (D / 32) + 4 * g * (D / 32);
-            if constexpr (D == 128) {
-                const u32x4 w = *reinterpret_cast<const u32x4*>(sp);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x.vs[u][j] = w[j];
-            } else {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(sp);
-                x.vs[u][0] = w[0]; x.vs[u][1] = w[1];
-            }
+            for (int j = 0; j < 4; ++j) { x.k[u][j] = w[j]; x.vs[u][j] = z[j]; }
         } else {
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) { x.k[u][j] = 0; x.vs[u][j] = 0x7f7f7f7fu; }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) x.v[u][v] = 0;
-            x.ks[u] = 127;
+            const u32x2 w = *reinterpret_cast<const u32x2*>(kp + ko), z = *reinterpret_cast<const u32x2*>(sp + vso);
+            x.k[u][0] = w[0]; x.k[u][1] = w[1];
+            x.vs[u][0] = z[0]; x.vs[u][1] = z[1];
         }
+        x.ks[u] = (a.c.k_scale + row * (D / 32))[kso];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x.v[u][v] = *reinterpret_cast<const uint32_t*>(vp + vo + v * (D / 2));
     }
 }
 
-// The words and scales of this lane's channel group for its 8 tokens; those at
-// or past `end` are zeros, whatever memory holds there.
+// Keeps the compiler from moving what both kinds of tiles compute alike ahead
+// of the branch between them, where all of it would lie in registers at once.
 template <int D>
+__device__ __forceinline__ void opaque(Tile<D>& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        asm volatile("" : "+v"(x.ks[u]));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) asm volatile("" : "+v"(x.k[u][j]), "+v"(x.vs[u][j]));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) asm volatile("" : "+v"(x.v[u][v]));
+    }
+}
+
+// The words and scales of this lane's channel group for its 8 tokens.  ALL:
+// all of them count; else those at or past `end`, or without a page, are
+// zeros, whatever memory holds there.
+template <int D, bool ALL>
 __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int lane, uint32_t (&w)[8], float (&s)[8]) {
     const int g = lane >> 4, n = lane & 15;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const bool in = t0 + 32 <= end || t0 + 16 * u + 4 * g + v < end;
             uint32_t b, c;
             if constexpr (D == 128) {
-                b = x.vs[u][v] >> (8 * (n >> 2)) & 255u;
+                b = x.vs[u][v] >> (8 * (n >> 2));
                 c = x.v[u][v];
             } else {
-                b = x.vs[u][v >> 1] >> (16 * (v & 1) + 8 * (n >> 3)) & 255u;
+                b = x.vs[u][v >> 1] >> (16 * (v & 1) + 8 * (n >> 3));
                 c = x.v[u][v] >> (16 * (n & 1));
             }
-            w[4 * u + v] = in ? c : 0u;
-            s[4 * u + v] = scale_bits(in ? b : 127u);
+            b &= 255u;
+            if constexpr (!ALL) {
+                const bool in = x.ok[u] && t0 + 16 * u + 4 * g + v < end;
+                b = in ? b : 127u;
+                c = in ? c : 0u;
+            }
+            w[4 * u + v] = c;
+            s[4 * u + v] = scale_bits(b);
         }
 }
 
@@ -334,14 +343,14 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     constexpr int PER = D / 4;          // channels of a lane's result
     constexpr int ROWS = 16 * R;        // rows of a wave
     constexpr int LD = D + 4;
-    __shared__ float so[SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
+    __shared__ float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
     extern __shared__ int32_t before[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, n = lane & 15;
 
     // key/value heads alternate fastest, so workgroups that share keys and
     // values lie on one XCD where there are 8 heads
     const int kvh = (int)(blockIdx.x % a.c.heads), group = (int)(blockIdx.x / a.c.heads);
-    int64_t slot = group;
+    int slot = group;
     int at = 0, stop = 1, each = 1;     // this workgroup's units
     if (l.groups > 0) {
         const int all = deal_out(a, l, before);
@@ -352,7 +361,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
         }
         at = (int)min((int64_t)group * each, (int64_t)all);
         stop = min(at + each, all);
-        int lo = 0, hi = (int)l.slots;  // the last block that begins at or before `at`: empty ones lie before it
+        int lo = 0, hi = l.slots;  // the last block that begins at or before `at`: empty ones lie before it
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (before[mid] <= at) lo = mid; else hi = mid;
@@ -379,7 +388,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     }
     const int part = whole_block ? -1 : 2 * group + (lo == 0 ? 1 : 0);
     const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
-    const int n_rows = b.queries * a.group;
+    const int n_rows = b.n_rows;
     const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
     const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
     const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
@@ -397,7 +406,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     for (int r = 0; r < R; ++r) {
         const int row = row0 + 16 * r + n;
         end[r] = end_of(a, b, row);
-        const E* p = reinterpret_cast<const E*>(a.q) + place_of(a, b, kvh, row < n_rows ? row : 0) * D + PER * g;
+        const E* p = reinterpret_cast<const E*>(a.q) + (int64_t)place_of(a, b, kvh, row < n_rows ? row : 0) * D + PER * g;
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -424,20 +433,10 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     }
     Pages pages(a, b.s, lo);
 
-    constexpr int STEP = SPLITW ? 32 * kWaves : 32;
-    Tile<D> next;
-    int t0 = lo + (SPLITW ? 32 * wave : 0);
-    if (t0 < hi) load_tile<D>(a, pages, kvh, t0, hi, lane, next);
-    for (; t0 < hi; t0 += STEP) {
-        const Tile<D> x = next;
-        if (t0 + STEP < hi) load_tile<D>(a, pages, kvh, t0 + STEP, hi, lane, next);
-        const bool whole = x.ok[0] && x.ok[1] && t0 + 32 <= all_see && t0 + 32 <= hi;
-
-        bf16x8 k[2][KS];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < KS; ++j) k[u][j] = eight_of(x.k[u][j], scale_bits(x.ks[u]));
+    // 32 tokens; ALL: every row sees all of them
+    auto run = [&](auto all, Tile<D> x, int t0) {
+        constexpr bool ALL = decltype(all)::value;
+        if constexpr (!ALL) opaque(x);
         bf16x8 p[R][PARTS];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -446,20 +445,19 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             for (int u = 0; u < 2; ++u) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < KS; ++j)
+                for (int j = 0; j < KS; ++j) {
+                    const bf16x8 k = eight_of(x.k[u][j], scale_bits(x.ks[u]));
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][j], q[r][j][i], acc, 0, 0, 0);
+                    for (int i = 0; i < PARTS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc, 0, 0, 0);
+                }
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[4 * u + v] = acc[v];
-            }
-            if (!whole) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
+                for (int v = 0; v < 4; ++v) {
+                    y[4 * u + v] = acc[v];
+                    if constexpr (!ALL) {
                         const int t = t0 + 16 * u + 4 * g + v;
                         if (!x.ok[u] || t >= end[r] || t >= hi) y[4 * u + v] = -INFINITY;
                     }
+                }
             }
             float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
             top = over_g(top) * to_log2;
@@ -489,28 +487,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 
         uint32_t w[8];
         float s[8];
-        bool odd = false;       // a value that is no number, where some rows do not see it
-        if (!whole) {
-            values_of<D>(x, t0, hi, lane, w, s);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
-        }
-        const bool apart = __any(odd);
-        // Where apart, one end at a time, with the tokens behind it cleared: 0
-        // times NaN would reach rows that do not see it.
-        for (int stop = apart ? t0 + 1 : hi;; ++stop) {
-            values_of<D>(x, t0, stop, lane, w, s);
-            bf16x8 pe[R][PARTS];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t use = !apart || min(end[r], hi) == stop || (stop == t0 + 32 && min(end[r], hi) > stop) ? ~0u : 0u;
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) {
-                    u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
-                    z &= use;
-                    pe[r][i] = __builtin_bit_cast(bf16x8, z);
-                }
-            }
+        auto accumulate = [&](const bf16x8 (&pp)[R][PARTS]) {
             auto pair = [&](auto I) {
                 bf16x8 c[2];
                 two_channels<decltype(I)::value>(w, s, c[0], c[1]);
@@ -520,7 +497,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
                     for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int i = 0; i < PARTS; ++i)
-                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pe[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pp[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
             };
             pair(std::integral_constant<int, 0>{});
             pair(std::integral_constant<int, 1>{});
@@ -528,8 +505,56 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
                 pair(std::integral_constant<int, 2>{});
                 pair(std::integral_constant<int, 3>{});
             }
-            if (!apart || stop == t0 + 32) break;
+        };
+        if constexpr (ALL) {
+            values_of<D, true>(x, t0, hi, lane, w, s);
+            accumulate(p);
+        } else {
+            values_of<D, false>(x, t0, hi, lane, w, s);
+            bool odd = false;       // a value that is no number, which some rows do not see
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
+            const bool apart = __any(odd);
+            // Where apart, one end at a time, with the tokens behind it
+            // cleared: 0 times NaN would reach rows that do not see it.
+            for (int stop = apart ? t0 + 1 : hi;; ++stop) {
+                if (apart) values_of<D, false>(x, t0, min(stop, hi), lane, w, s);
+                bf16x8 pe[R][PARTS];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t use = !apart || min(min(end[r], hi), t0 + 32) == stop ? ~0u : 0u;
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
+                        z &= use;
+                        pe[r][i] = __builtin_bit_cast(bf16x8, z);
+                    }
+                }
+                accumulate(pe);
+                if (!apart || stop == t0 + 32) break;
+            }
         }
+    };
+    // the next tile is on its way while one is worked on
+    constexpr int STEP = SPLITW ? 32 * kWaves : 32;
+    const int plain = min(all_see, hi) - 32;       // last tile that every row sees
+    int t0 = lo + (SPLITW ? 32 * wave : 0);
+    if (t0 < hi) {
+        Tile<D> next;
+        load_tile<D>(a, pages, kvh, t0, lane, next);
+        do {
+            while (t0 <= plain && next.ok[0] && next.ok[1]) {
+                const Tile<D> x = next;
+                t0 += STEP;
+                if (t0 < hi) load_tile<D>(a, pages, kvh, t0, lane, next);
+                run(std::true_type{}, x, t0 - STEP);
+            }
+            if (t0 >= hi) break;
+            const Tile<D> x = next;
+            t0 += STEP;
+            if (t0 < hi) load_tile<D>(a, pages, kvh, t0, lane, next);
+            run(std::false_type{}, x, t0 - STEP);
+        } while (t0 < hi);
     }
 
 #pragma unroll
@@ -583,40 +608,30 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 #pragma unroll
             for (int r = 0; r < R; ++r) { sm[wave][16 * r + n] = m[r]; ss[wave][16 * r + n] = sum[r]; }
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int j = 0; j < VJ; j += 4)
+                    *reinterpret_cast<f32x4*>(&so[wave][16 * r + n][PER * g + VJ * v + j]) =
+                        f32x4{o[r][j][v], o[r][j + 1][v], o[r][j + 2][v], o[r][j + 3][v]};
         __syncthreads();
-        float f[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][16 * r + n]);
-            f[r] = m[r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[r] - mx);
-        }
-        for (int w = 0; w < kWaves; ++w) {
-            if (w == wave) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-#pragma unroll
-                        for (int j = 0; j < VJ; j += 4) {
-                            f32x4* at = reinterpret_cast<f32x4*>(&so[16 * r + n][PER * g + VJ * v + j]);
-                            f32x4 y = {o[r][j][v] * f[r], o[r][j + 1][v] * f[r], o[r][j + 2][v] * f[r], o[r][j + 3][v] * f[r]};
-                            *at = w == 0 ? y : *at + y;
-                        }
-            }
-            __syncthreads();
-        }
-        for (int i = threadIdx.x; i < ROWS * (D / 8); i += kWaves * 64) {
-            const int r = i / (D / 8), c0 = i % (D / 8) * 8, row = row0 + r;
-            if (row >= n_rows) continue;
-            float mx = -INFINITY, sum_r = 0.f;
+        const int here = min(ROWS, n_rows - row0);
+        for (int i = threadIdx.x; i < here * (D / 8); i += kWaves * 64) {
+            const int r = i / (D / 8), c0 = i % (D / 8) * 8;
+            float mx = -INFINITY, sum_r = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                if (sm[w][r] != -INFINITY) sum_r += ss[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - mx);
-            put(row, c0, &so[r][c0], mx, sum_r);
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = sm[w][r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w][r] - mx);
+                sum_r += f * ss[w][r];
+                const f32x4 lo4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0]), hi4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0 + 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { y[e] += f * lo4[e]; y[4 + e] += f * hi4[e]; }
+            }
+            put(row0 + r, c0, y, mx, sum_r);
         }
         __syncthreads();                // before the next block's results
     }
@@ -631,31 +646,23 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     constexpr int PER = D / 64;
     __shared__ float acc[kWaves][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t at = (int64_t)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
+    const int at = (int)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
     const int turn = wave % WAVES;
-    if (at >= a.tokens * a.heads) return;              // WAVES < kWaves: no barrier below
-    const int64_t row = at / a.heads;
-    const int head = (int)(at % a.heads), kvh = head / a.group;
-    int64_t s = row;
-    if (a.cu_seqlens) {
-        int64_t lo = 0, hi = a.n_seq;
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (a.cu_seqlens[mid] <= row) lo = mid; else hi = mid;
-        }
-        s = lo;
-    }
+    if (at >= (int)a.tokens * a.heads) return;         // WAVES < kWaves: no barrier below
+    const int row = (int)((uint32_t)at / (uint32_t)a.heads), head = at - row * a.heads;
+    const int kvh = (int)((uint32_t)head / (uint32_t)a.group);
     Block b;
-    sequence_of(a, s, b);
-    if (row < b.row0 || row >= b.row0 + b.queries) return;
-    const int r = (int)(row - b.row0) * a.group + head % a.group;
-    const int64_t slot = (a.cu_seqlens ? first_slot(a, l, s) : s * l.per_seq) + r / l.rows;
-    if (slot < 0 || slot >= l.slots) return;           // offsets out of order
+    sequence_of(a, a.cu_seqlens ? sequence_at(a, row) : row, b);
+    const int r = (row - b.row0) * a.group + head - kvh * a.group;
+    if (r < 0 || r >= b.n_rows) return;                // a row of no sequence
+    const int block = (int)((uint32_t)r / (uint32_t)l.rows);
+    const int slot = (a.cu_seqlens ? first_slot(a, l, b.s) : b.s * l.per_seq) + block;
+    if (slot >= l.slots) return;                       // offsets out of order
     const int each = parts.before[l.slots + 1], p0 = parts.before[slot], p1 = parts.before[slot + 1];
     const int w0 = p0 / each, count = (p1 - 1) / each - w0 + 1;
     if (p1 <= p0 || count < 2) return;                 // written already
-    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r % l.rows;
-    const int64_t rest = ((int64_t)(2 * w0) * a.c.heads + kvh) * l.rows + r % l.rows, stride = 2 * (int64_t)a.c.heads * l.rows;
+    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + (r - block * l.rows);
+    const int64_t stride = 2 * (int64_t)a.c.heads * l.rows, rest = first - stride / 2;
     auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
 
     float mx = -INFINITY;
@@ -695,7 +702,7 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        const int64_t i = at * D + lane * PER + e;
+        const int64_t i = (int64_t)at * D + lane * PER + e;
         float y = sum == 0.f ? 0.f : o[e] / sum;
         if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
         reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y);
@@ -725,16 +732,16 @@ Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
     p.l.rows = p.splitw ? 16 * p.r : 16 * p.r * kWaves;
     p.l.per_seq = (a.group + p.l.rows - 1) / p.l.rows;
     // with or without offsets: enough slots for both
-    p.l.slots = a.tokens * a.group / p.l.rows + a.n_seq;
-    if (a.n_seq * p.l.per_seq > p.l.slots) p.l.slots = a.n_seq * p.l.per_seq;
+    const int64_t packed = a.tokens * a.group / p.l.rows + a.n_seq, plain = a.n_seq * p.l.per_seq;
+    p.l.slots = (int)(packed > plain ? packed : plain);
     // as many workgroups as run at once, but none for less than a unit of
     // every block's longest
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
     const int64_t len = a.max_len < cap ? a.max_len : cap;
-    const int64_t units = p.l.slots * ((len + kUnit - 1) / kUnit);
-    int64_t groups = ((p.splitw ? 768 : 512) + a.c.heads - 1) / a.c.heads;
+    const int64_t units = (int64_t)p.l.slots * ((len + kUnit - 1) / kUnit);
+    int64_t groups = ((p.splitw && p.r == 1 && bf16 ? 768 : 512) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
-    const bool dealt = p.l.slots <= kMaxDealt && p.l.slots * (cap / kUnit + 1) <= INT32_MAX;
+    const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1) <= INT32_MAX;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
     return p;
 }
@@ -747,7 +754,7 @@ size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
 
 template <typename E, int D, int R, bool SPLITW>
 hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, const Parts& parts, hipStream_t s) {
-    const int64_t blocks = (p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
+    const int64_t blocks = (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
     const unsigned lds = p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * sizeof(int32_t) : 0;
     hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), lds, s, a, p.l,
                        parts);

@@ -78,7 +78,8 @@ Cache4AttentionArgs attention_args(const kda_cache4* c, const kda_cache4_attenti
     Cache4AttentionArgs a = {};
     a.c = cache_args(c);
     a.n_seq = p->n_seq; a.tokens = p->tokens; a.heads = p->heads; a.group = p->heads / c->heads;
-    a.max_pages = p->max_pages; a.max_q = p->max_q; a.max_len = p->max_len; a.scale = p->scale;
+    a.max_pages = c->pages > 0 ? p->max_pages : 0;   // a cache without pages counts no tokens
+     a.max_q = p->max_q; a.max_len = p->max_len; a.scale = p->scale;
     return a;
 }
 
