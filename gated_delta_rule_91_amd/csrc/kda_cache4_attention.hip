@@ -50,6 +50,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;         // tokens that are dealt out at once
+// Units that a block counts for beside its own: beginning one costs about as
+// much as this many.
+constexpr int kBlockCost = 3;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
 
 // How the work is laid out (host and kernels).
@@ -60,15 +63,20 @@ struct Layout {
     int groups;      // workgroups of a key/value head that units are dealt to; 0: a block each
 };
 
-// Where the second kernel finds the parts: before[slot] units lie before a
-// row block, workgroup w has the units [w * each, (w + 1) * each) and two
-// parts at most, 2 w of a block that began before and 2 w + 1 of one that
-// begins in it.  Part i of row r of a block and key/value head h is at
-// (i * heads + h) * rows + r.
+// Workgroup w has two parts at most, 2 w of a block that began before it and
+// 2 w + 1 of one that begins in it and goes on.  Part i of row r of a block and
+// key/value head h is at (i * heads + h) * rows + r.  The second kernel finds
+// by cut[w] the block that begins in w and goes on.
+struct Cut {
+    int s;           // its sequence, -1: there is none
+    int begin;       // its first (query, head) row
+    int last;        // last workgroup that has a part of it
+    int pad;
+};
 struct Parts {
-    int32_t* before;     // [slots + 1], then each
-    float* sums;         // maximum and sum
-    float* o;            // D channels
+    Cut* cut;        // [groups]
+    float* sums;     // maximum and sum
+    float* o;        // D channels
 };
 
 struct Block {
@@ -146,8 +154,9 @@ __device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, const Bloc
     return (b.row0 + i) * a.heads + kvh * a.group + (r - i * a.group);
 }
 
-// before[i]: units of the row blocks before i, i <= slots; returns all of them.
-// A block with rows has one unit at least, whose output may be zeros.
+// before[i]: units that the row blocks before i count for, i <= slots; returns
+// those of all.  A block with rows has one of its own at least, though its
+// output may be zeros.
 __device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* before) {
     __shared__ int32_t part[kWaves];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -156,7 +165,7 @@ __device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* 
         int c = 0;
         if (base + t < l.slots) {
             const Block b = block_of(a, l, base + t);
-            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) + kUnit - 1) / kUnit, 1);
+            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) + kUnit - 1) / kUnit, 1) + kBlockCost;
         }
         int in = c;
 #pragma unroll
@@ -355,10 +364,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     if (l.groups > 0) {
         const int all = deal_out(a, l, before);
         each = max((all + l.groups - 1) / l.groups, 1);
-        if (blockIdx.x == 0) {
-            for (int i = threadIdx.x; i <= l.slots; i += kWaves * 64) parts.before[i] = before[i];
-            if (threadIdx.x == 0) parts.before[l.slots + 1] = each;
-        }
+        if (kvh == 0 && threadIdx.x == 0) parts.cut[group].s = -1;
         at = (int)min((int64_t)group * each, (int64_t)all);
         stop = min(at + each, all);
         int lo = 0, hi = l.slots;  // the last block that begins at or before `at`: empty ones lie before it
@@ -373,20 +379,25 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 
     for (; at < stop; ++slot) {
     const Block b = block_of(a, l, slot);
-    int lo = 0, lim = b.total, whole_block = 1;
+    int lo = 0, lim = b.total, part = -1;
     if (l.groups > 0) {
-        const int p0 = __builtin_amdgcn_readfirstlane(before[slot]), p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
-        if (p1 == p0) continue;         // no rows
-        const int to = min(stop, p1);
-        lo = (at - p0) * kUnit;
+        // the block's own units are [p0, p1)
+        const int p0 = __builtin_amdgcn_readfirstlane(before[slot]) + kBlockCost, p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
+        const int from = max(at, p0), to = min(stop, p1);
+        at = max(at, min(stop, p1));
+        if (to <= from) continue;       // no rows, or the next workgroup has them all
+        lo = (from - p0) * kUnit;
         lim = min(b.total, (to - p0) * kUnit);
-        whole_block = at == p0 && to == p1;
-        at = to;
+        if (from > p0) {
+            part = 2 * group;
+        } else if (to < p1) {
+            part = 2 * group + 1;
+            if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.s, b.begin, (p1 - 1) / each, 0};
+        }
     } else {
         at = stop;
         if (!b.any) continue;
     }
-    const int part = whole_block ? -1 : 2 * group + (lo == 0 ? 1 : 0);
     const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
     const int n_rows = b.n_rows;
     const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
@@ -638,31 +649,26 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     }
 }
 
-// Joins the parts of a (row, head): weights 2^(m_i - max m).  WAVES waves take
-// turns at the parts of one, and their sums are joined through LDS in the
-// order of the waves.
+// Joins the parts of the block that begins in a workgroup of the first kernel
+// and goes on, row by row: weights 2^(m_i - max m).  WAVES waves take turns at
+// the parts of a row, and their sums are joined through LDS in the order of
+// the waves.
 template <typename E, int D, int WAVES>
-__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
+__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts, int chunks) {
     constexpr int PER = D / 64;
     __shared__ float acc[kWaves][D];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int at = (int)blockIdx.x * (kWaves / WAVES) + wave / WAVES;
-    const int turn = wave % WAVES;
-    if (at >= (int)a.tokens * a.heads) return;         // WAVES < kWaves: no barrier below
-    const int row = (int)((uint32_t)at / (uint32_t)a.heads), head = at - row * a.heads;
-    const int kvh = (int)((uint32_t)head / (uint32_t)a.group);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % WAVES;
+    // chunks of rows, key/value heads, workgroups of the first kernel
+    const int chunk = (int)(blockIdx.x % chunks), kvh = (int)(blockIdx.x / chunks % a.c.heads), w0 = (int)(blockIdx.x / chunks / a.c.heads);
+    const Cut cut = parts.cut[w0];
+    if (cut.s < 0) return;
     Block b;
-    sequence_of(a, a.cu_seqlens ? sequence_at(a, row) : row, b);
-    const int r = (row - b.row0) * a.group + head - kvh * a.group;
-    if (r < 0 || r >= b.n_rows) return;                // a row of no sequence
-    const int block = (int)((uint32_t)r / (uint32_t)l.rows);
-    const int slot = (a.cu_seqlens ? first_slot(a, l, b.s) : b.s * l.per_seq) + block;
-    if (slot >= l.slots) return;                       // offsets out of order
-    const int each = parts.before[l.slots + 1], p0 = parts.before[slot], p1 = parts.before[slot + 1];
-    const int w0 = p0 / each, count = (p1 - 1) / each - w0 + 1;
-    if (p1 <= p0 || count < 2) return;                 // written already
-    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + (r - block * l.rows);
-    const int64_t stride = 2 * (int64_t)a.c.heads * l.rows, rest = first - stride / 2;
+    sequence_of(a, cut.s, b);
+    const int count = cut.last - w0 + 1, rows = min(l.rows, b.n_rows - cut.begin);
+    for (int r = chunk * (kWaves / WAVES) + wave / WAVES; r < rows; r += chunks * (kWaves / WAVES)) {
+    const int64_t stride = 2 * (int64_t)a.c.heads * l.rows;
+    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r, rest = first - stride / 2;
+    const int64_t at = place_of(a, b, kvh, cut.begin + r);
     auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
 
     float mx = -INFINITY;
@@ -694,26 +700,26 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[wave][lane * PER + e] = o[e];
         __syncthreads();
-        if (turn != 0) return;
+        if (turn == 0) {
 #pragma unroll
-        for (int k = 1; k < WAVES; ++k)
+            for (int k = 1; k < WAVES; ++k)
 #pragma unroll
-            for (int e = 0; e < PER; ++e) o[e] += acc[wave + k][lane * PER + e];
+                for (int e = 0; e < PER; ++e) o[e] += acc[wave + k][lane * PER + e];
+        }
+        __syncthreads();
+        if (turn != 0) continue;
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        const int64_t i = (int64_t)at * D + lane * PER + e;
+        const int64_t i = at * D + lane * PER + e;
         float y = sum == 0.f ? 0.f : o[e] / sum;
         if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
         reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y);
     }
+    }
 }
 
 constexpr int kSplitMaxRows = 32;      // rows that the waves of a workgroup share
-// (row, head) pairs below which four waves join the parts of each: few pairs
-// have many parts, many have few
-constexpr int64_t kWideCombine = 2048;
-
 // bf16 rows of a wave in the many-rows form; fp32 takes three times the
 // registers for its queries
 constexpr int rows_r(bool bf16) { return bf16 ? 2 : 1; }
@@ -738,16 +744,16 @@ Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
     // every block's longest
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
     const int64_t len = a.max_len < cap ? a.max_len : cap;
-    const int64_t units = (int64_t)p.l.slots * ((len + kUnit - 1) / kUnit);
+    const int64_t units = (int64_t)p.l.slots * ((len + kUnit - 1) / kUnit + kBlockCost);
     int64_t groups = ((p.splitw && p.r == 1 && bf16 ? 768 : 512) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
-    const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1) <= INT32_MAX;
+    const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= INT32_MAX;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
     return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t before_bytes(const Plan& p) { return round256((size_t)(p.l.slots + 2) * sizeof(int32_t)); }
+size_t cut_bytes(const Plan& p) { return round256((size_t)p.l.groups * sizeof(Cut)); }
 size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
     return 2 * (size_t)p.l.groups * (size_t)a.c.heads * (size_t)p.l.rows;
 }
@@ -767,8 +773,8 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
     const Plan p = plan_of(bf16, a);
     Parts parts = {};
     if (p.l.groups > 0) {
-        parts.before = reinterpret_cast<int32_t*>(ws);
-        parts.o = reinterpret_cast<float*>(ws + before_bytes(p));
+        parts.cut = reinterpret_cast<Cut*>(ws);
+        parts.o = reinterpret_cast<float*>(ws + cut_bytes(p));
         parts.sums = parts.o + part_places(a, p) * D;
     }
     hipError_t e;
@@ -776,12 +782,14 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
     else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, parts, s);
     else e = launch_attention_r<E, D, 2, true>(a, p, parts, s);
     if (e != hipSuccess || p.l.groups < 2) return e;
-    const int64_t joined = a.tokens * a.heads;
-    if (joined < kWideCombine)
-        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), dim3((unsigned)joined), dim3(kWaves * 64), 0, s, a, p.l, parts);
-    else
-        hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1>), dim3((unsigned)((joined + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0,
-                           s, a, p.l, parts);
+    // Where a block has many parts, four waves share those of a row.
+    const int64_t most = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
+    const int rows = (int)(most < p.l.rows ? most : p.l.rows);
+    const bool wide = p.l.slots * 4 <= p.l.groups;
+    const int chunks = wide ? rows : (rows + kWaves - 1) / kWaves;
+    const dim3 grid((unsigned)((p.l.groups - 1) * a.c.heads * chunks));
+    if (wide) hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
+    else hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
     return hipGetLastError();
 }
 
@@ -790,7 +798,7 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
     const Plan p = plan_of(bf16, a);
     if (p.l.groups == 0) return 0;
-    return before_bytes(p) + part_places(a, p) * (size_t)(d + 2) * sizeof(float);
+    return cut_bytes(p) + part_places(a, p) * (size_t)(d + 2) * sizeof(float);
 }
 
 hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
