@@ -10,7 +10,7 @@
 //
 // Both directions are bound by HBM (10 bytes an element forward, 20 in the
 // training pass's backward, with a gate in bf16), so each reads its inputs
-// once: a workgroup holds a tile of kTile tokens x 64 VEC channels in
+// once: a workgroup holds a tile of 128 or 64 tokens x 128 channels in
 // registers while the state that enters it is found.
 //  * A wave runs its stretch of the tile from nothing: (A, H), the product of
 //    its decays and the state it ends with.  A stretch is the map
@@ -42,7 +42,8 @@ namespace kda {
 
 namespace {
 
-constexpr int kTile = 128;        // tokens a workgroup holds
+// Tokens that a workgroup holds, and that its waves share.
+constexpr int kTile = 128, kBackTile = 64;
 constexpr int kWindow = 8;        // tiles that a look-back reads at once
 // Polls after which a wait gives up with NaN: a tenth of a second, where a tile takes
 // microseconds.  Only a workspace that another call is using can get there.
@@ -59,16 +60,24 @@ template <int N, typename V> __device__ __forceinline__ float lane_of(V v, int i
     if constexpr (N == 1) return to_f32(v);
     else return to_f32(v[i]);
 }
+// N elements as one access, at any multiple of the element's size: rows of an
+// odd width do not keep pairs aligned.
+template <typename E, int N>
+__device__ __forceinline__ typename VecOf<E, N>::type get(const E* p) {
+    typename VecOf<E, N>::type v;
+    __builtin_memcpy(&v, p, N * sizeof(E));
+    return v;
+}
 template <typename E, int N>
 __device__ __forceinline__ void put(E* p, const float (&x)[N]) {
+    typename VecOf<E, N>::type v;
     if constexpr (N == 1) {
-        *p = from_f32<E>(x[0]);
+        v = from_f32<E>(x[0]);
     } else {
-        typename VecOf<E, N>::type v;
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = from_f32<E>(x[i]);
-        *reinterpret_cast<typename VecOf<E, N>::type*>(p) = v;
     }
+    __builtin_memcpy(p, &v, N * sizeof(E));
 }
 
 // One token's decay, of lambda = max(log_alpha, floor): `c` is expm1(lambda)
@@ -122,6 +131,9 @@ struct Walk {
         s = s_;
         bounds();
     }
+    // Whether tokens [t, t + n) lie within one sequence, neither its first nor
+    // its last token among them.
+    __device__ __forceinline__ bool inside(int t, int n) const { return t > first && t + n < end; }
     // Whether a sequence holds token t, for t going up, and going down.
     __device__ __forceinline__ bool up(int t) {
         if (cu) while (t >= end && s + 1 < n) { ++s; bounds(); }
@@ -132,6 +144,20 @@ struct Walk {
         return t >= first && t < end;
     }
 };
+
+// The channels [c, c + VEC) of a lane.  Where the width is no multiple of VEC
+// the last lane takes the last VEC ones, and computes and writes the same
+// values as its neighbour for those they share.  Lanes behind it (in false)
+// work on the last channels too, without writing.
+struct Channels {
+    int64_t c;
+    bool in;
+};
+template <int VEC>
+__device__ __forceinline__ Channels channels_of(int64_t D, int64_t block, int lane) {
+    const int64_t c = (block * 64 + lane) * VEC;
+    return Channels{c + VEC <= D ? c : D - VEC, c < D};
+}
 
 struct TileGrid {
     int64_t tiles;          // per row
@@ -199,10 +225,10 @@ __device__ __forceinline__ bool take_tile(const TileGrid& g, int32_t* counter, i
 }
 
 template <typename E, int VEC, int WAVES, bool GATE>
-__global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
-                                                                    uint64_t* words, float* keep) {
+__global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
+                                                                       uint64_t* words, float* keep) {
     constexpr int TPW = kTile / WAVES;
-    static_assert(TPW * VEC <= 32, "one flag a value");
+    static_assert(TPW * VEC <= 32 && kBackTile % TPW == 0, "one flag a value; a kept state between waves");
     typedef typename VecOf<E, VEC>::type EV;
     typedef typename VecOf<float, VEC>::type FV;
     __shared__ float sA[WAVES][64 * VEC], sH[WAVES][64 * VEC], sIn[64 * VEC];
@@ -211,9 +237,8 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
     int64_t id;
     if (!take_tile(grid, counter, &sId, id)) return;
     const int64_t i = id / grid.lanes, row = (id % grid.lanes) / grid.blocks;
-    const int64_t c0 = (id % grid.blocks) * (64 * VEC) + lane * VEC;
-    const bool in = c0 < a.D;                     // D is a multiple of VEC
-    const int64_t c = in ? c0 : a.D - VEC;
+    const Channels ch = channels_of<VEC>(a.D, id % grid.blocks, lane);
+    const int64_t c = ch.c;
     const int t0 = (int)(i * kTile) + wave * TPW;
 
     EV x[TPW], g[TPW];
@@ -222,9 +247,9 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
 #pragma unroll
     for (int j = 0; j < TPW; ++j) {
         const int64_t t = t0 + j < (int)a.T ? t0 + j : (int)a.T - 1, at = (base + t) * a.D + c;
-        x[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.x) + at);
-        const FV l = *reinterpret_cast<const FV*>(a.log_alpha + at);
-        if constexpr (GATE) g[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.g) + at);
+        x[j] = get<E, VEC>(reinterpret_cast<const E*>(a.x) + at);
+        const FV l = get<float, VEC>(a.log_alpha + at);
+        if constexpr (GATE) g[j] = get<E, VEC>(reinterpret_cast<const E*>(a.g) + at);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) d[j][v] = lane_of<VEC>(l, v);
     }
@@ -235,27 +260,35 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
     bool cut = false;
     Walk walk(a, (int)row, t0);
     const int s0 = walk.s;
+    const bool plain = walk.inside(t0, TPW);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { h[v] = 0.f; sum[v] = 0.f; }
+    auto token = [&](int j, bool start) {
 #pragma unroll
-    for (int j = 0; j < TPW; ++j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.up(t)) {
-            const bool start = t == walk.first;
-            if (start) {
-                cut = true;
+        for (int v = 0; v < VEC; ++v) {
+            const float l = fmaxf(d[j][v], a.floor_);
+            const Decay k(l);
+            sum[v] += l;
+            slow |= (uint32_t)k.slow << (j * VEC + v);
+            h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
+            // state_in is read once: state_out may be the same array
+            d[j][v] = start ? h[v] : k.c;
+        }
+    };
+    if (plain) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
-            }
+        for (int j = 0; j < TPW; ++j) token(j, false);
+    } else {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float l = fmaxf(d[j][v], a.floor_);
-                const Decay k(l);
-                sum[v] += l;
-                slow |= (uint32_t)k.slow << (j * VEC + v);
-                h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
-                // state_in is read once: state_out may be the same array
-                d[j][v] = start ? h[v] : k.c;
+        for (int j = 0; j < TPW; ++j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.up(t)) {
+                if (t == walk.first) {
+                    cut = true;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
+                }
+                token(j, t == walk.first);
             }
         }
     }
@@ -286,18 +319,14 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
         }
         if (grid.tiles > 1) {
             uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
-            if (in && i + 1 < grid.tiles) {
+            if (ch.in && i + 1 < grid.tiles) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, H[v]) : map_word(A[v], H[v]));
             }
             if (i > 0) look_back<VEC>(mine - a.D, -a.D, i, hin);
-            if (in && !constant && i + 1 < grid.tiles) {
+            if (ch.in && !constant && i + 1 < grid.tiles) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], hin[v], H[v])));
-            }
-            if (in && a.keep) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) keep[(row * grid.tiles + i) * a.D + c + v] = hin[v];
             }
         }
 #pragma unroll
@@ -306,6 +335,7 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
     __syncthreads();
 
     // again from the true state
+    if (!ch.in) return;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h[v] = sIn[lane * VEC + v];
     for (int w = 0; w < wave; ++w) {
@@ -316,32 +346,44 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_kernel(RecurrenceAr
             h[v] = cw ? Hw : fmaf(sA[w][lane * VEC + v], h[v], Hw);
         }
     }
-    walk.go_to(s0);
+    if (a.keep && wave * TPW % kBackTile == 0 && t0 < (int)a.T) {
+        const int64_t back_tiles = (a.T + kBackTile - 1) / kBackTile;
 #pragma unroll
-    for (int j = 0; j < TPW; ++j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.up(t)) {
-            const bool start = t == walk.first;
-            float y[VEC];
+        for (int v = 0; v < VEC; ++v) keep[(row * back_tiles + t0 / kBackTile) * a.D + c + v] = h[v];
+    }
+    auto write = [&](int j, bool start) {
+        float y[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                h[v] = start ? d[j][v] : Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
-                y[v] = h[v];
-                if constexpr (GATE) y[v] *= sigmoidf_(lane_of<VEC>(g[j], v));
-            }
-            if (in) put<E, VEC>(reinterpret_cast<E*>(a.out) + (base + t) * a.D + c, y);
-            if (in && a.state_out && t == walk.end - 1) {
+        for (int v = 0; v < VEC; ++v) {
+            h[v] = start ? d[j][v] : Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
+            y[v] = h[v];
+            if constexpr (GATE) y[v] *= sigmoidf_(lane_of<VEC>(g[j], v));
+        }
+        put<E, VEC>(reinterpret_cast<E*>(a.out) + (base + t0 + j) * a.D + c, y);
+    };
+    if (plain) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) a.state_out[(int64_t)walk.s * a.D + c + v] = h[v];
+        for (int j = 0; j < TPW; ++j) write(j, false);
+    } else {
+        walk.go_to(s0);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.up(t)) {
+                write(j, t == walk.first);
+                if (a.state_out && t == walk.end - 1) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) a.state_out[(int64_t)walk.s * a.D + c + v] = h[v];
+                }
             }
         }
     }
 }
 
 template <typename E, int VEC, int WAVES, bool GATE>
-__global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
-                                                                             uint64_t* words, const float* keep) {
-    constexpr int TPW = kTile / WAVES;
+__global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_backward_kernel(RecurrenceArgs a, TileGrid grid, int32_t* counter,
+                                                                                uint64_t* words, const float* keep) {
+    constexpr int TPW = kBackTile / WAVES;
     static_assert(TPW * VEC <= 32, "one flag a value");
     typedef typename VecOf<E, VEC>::type EV;
     typedef typename VecOf<float, VEC>::type FV;
@@ -351,10 +393,9 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
     int64_t id;
     if (!take_tile(grid, counter, &sId, id)) return;
     const int64_t i = grid.tiles - 1 - id / grid.lanes, row = (id % grid.lanes) / grid.blocks;
-    const int64_t c0 = (id % grid.blocks) * (64 * VEC) + lane * VEC;
-    const bool in = c0 < a.D;
-    const int64_t c = in ? c0 : a.D - VEC;
-    const int t0 = (int)(i * kTile) + wave * TPW;
+    const Channels ch = channels_of<VEC>(a.D, id % grid.blocks, lane);
+    const int64_t c = ch.c;
+    const int t0 = (int)(i * kBackTile) + wave * TPW;
 
     EV x[TPW], g[TPW], o[TPW];
     float d[TPW][VEC];
@@ -362,14 +403,17 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
 #pragma unroll
     for (int j = 0; j < TPW; ++j) {
         const int64_t t = t0 + j < (int)a.T ? t0 + j : (int)a.T - 1, at = (base + t) * a.D + c;
-        x[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.x) + at);
-        const FV l = *reinterpret_cast<const FV*>(a.log_alpha + at);
-        if constexpr (GATE) g[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.g) + at);
+        x[j] = get<E, VEC>(reinterpret_cast<const E*>(a.x) + at);
+        const FV l = get<float, VEC>(a.log_alpha + at);
+        if constexpr (GATE) g[j] = get<E, VEC>(reinterpret_cast<const E*>(a.g) + at);
         o[j] = EV(0);
-        if (a.d_out) o[j] = *reinterpret_cast<const EV*>(reinterpret_cast<const E*>(a.d_out) + at);
+        if (a.d_out) o[j] = get<E, VEC>(reinterpret_cast<const E*>(a.d_out) + at);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) d[j][v] = lane_of<VEC>(l, v);
     }
+    float enter[VEC];                             // the state that enters the tile
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) enter[v] = i > 0 ? keep[(row * grid.tiles + i) * a.D + c + v] : 0.f;
 
     // this wave's maps, of the state forward and of its gradient in reverse
     float h[VEC], e[VEC], sum[VEC];
@@ -377,43 +421,59 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
     bool first = false, last = false;
     Walk walk(a, (int)row, t0);
     const int s0 = walk.s;
+    const bool plain = walk.inside(t0, TPW);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) { h[v] = 0.f; e[v] = 0.f; sum[v] = 0.f; }
+    auto up = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < TPW; ++j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.up(t)) {
-            if (t == walk.first) {
-                first = true;
+        for (int v = 0; v < VEC; ++v) {
+            const float l = fmaxf(d[j][v], a.floor_);
+            free_ |= (uint32_t)(d[j][v] > a.floor_) << (j * VEC + v);
+            const Decay k(l);
+            sum[v] += l;
+            d[j][v] = k.c;
+            slow |= (uint32_t)k.slow << (j * VEC + v);
+            h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
+        }
+    };
+    auto down = [&](int j) {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
-            }
+        for (int v = 0; v < VEC; ++v) {
+            const float s = GATE ? sigmoidf_(lane_of<VEC>(g[j], v)) : 1.f;
+            e[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).times(fmaf(lane_of<VEC>(o[j], v), s, e[v]));
+        }
+    };
+    if (plain) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float l = fmaxf(d[j][v], a.floor_);
-                free_ |= (uint32_t)(d[j][v] > a.floor_) << (j * VEC + v);
-                const Decay k(l);
-                sum[v] += l;
-                d[j][v] = k.c;
-                slow |= (uint32_t)k.slow << (j * VEC + v);
-                h[v] = k.step(h[v], lane_of<VEC>(x[j], v));
+        for (int j = 0; j < TPW; ++j) up(j);
+#pragma unroll
+        for (int j = TPW - 1; j >= 0; --j) down(j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.up(t)) {
+                if (t == walk.first) {
+                    first = true;
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
+                }
+                up(j);
             }
         }
     }
     const int s1 = walk.s;
+    if (!plain) {
 #pragma unroll
-    for (int j = TPW - 1; j >= 0; --j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.down(t)) {
-            if (t == walk.end - 1) {
-                last = true;
+        for (int j = TPW - 1; j >= 0; --j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.down(t)) {
+                if (t == walk.end - 1) {
+                    last = true;
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float s = GATE ? sigmoidf_(lane_of<VEC>(g[j], v)) : 1.f;
-                e[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).times(fmaf(lane_of<VEC>(o[j], v), s, e[v]));
+                    for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
+                }
+                down(j);
             }
         }
     }
@@ -446,12 +506,12 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
         if (grid.tiles > 1) {
             uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
             const int64_t behind = grid.tiles - 1 - i;
-            if (in && i > 0) {
+            if (ch.in && i > 0) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, C[v]) : map_word(A[v], C[v]));
             }
             if (behind > 0) look_back<VEC>(mine + a.D, a.D, behind, ein);
-            if (in && !constant && i > 0) {
+            if (ch.in && !constant && i > 0) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], ein[v], C[v])));
             }
@@ -460,11 +520,12 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
         for (int v = 0; v < VEC; ++v) sIn[lane * VEC + v] = ein[v];
     }
     __syncthreads();
+    if (!ch.in) return;
 
-    // the states before each token, from the kept one that enters the tile
+    // the states before each token
     float before[TPW][VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = i > 0 ? keep[(row * grid.tiles + i) * a.D + c + v] : 0.f;
+    for (int v = 0; v < VEC; ++v) h[v] = enter[v];
     for (int w = 0; w < wave; ++w) {
         const bool cw = sFirst[w] != 0;
 #pragma unroll
@@ -473,23 +534,13 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
             h[v] = cw ? Hw : fmaf(sA[w][lane * VEC + v], h[v], Hw);
         }
     }
-    walk.go_to(s0);
+    auto again = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < TPW; ++j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.up(t)) {
-            if (t == walk.first) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                before[j][v] = h[v];
-                h[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
-            }
+        for (int v = 0; v < VEC; ++v) {
+            before[j][v] = h[v];
+            h[v] = Decay(d[j][v], slow >> (j * VEC + v) & 1u).step(h[v], lane_of<VEC>(x[j], v));
         }
-    }
-
+    };
     // the gradients, from the one that enters the wave's stretch from behind
 #pragma unroll
     for (int v = 0; v < VEC; ++v) e[v] = sIn[lane * VEC + v];
@@ -501,34 +552,54 @@ __global__ __launch_bounds__(WAVES * 64) void kda_recurrence_backward_kernel(Rec
             e[v] = cw ? Cw : fmaf(sA[w][lane * VEC + v], e[v], Cw);
         }
     }
-    walk.go_to(s1);
+    auto write = [&](int j) {
+        float dx[VEC], dl[VEC], dg[VEC];
 #pragma unroll
-    for (int j = TPW - 1; j >= 0; --j) {
-        const int t = t0 + j;
-        if (t < (int)a.T && walk.down(t)) {
-            if (t == walk.end - 1) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
+        for (int v = 0; v < VEC; ++v) {
+            const Decay k(d[j][v], slow >> (j * VEC + v) & 1u);
+            const float dy = lane_of<VEC>(o[j], v);
+            float s = 1.f;
+            if constexpr (GATE) {
+                s = sigmoidf_(lane_of<VEC>(g[j], v));
+                dg[v] = dy * k.step(before[j][v], lane_of<VEC>(x[j], v)) * s * (1.f - s);
             }
-            float dx[VEC], dl[VEC], dg[VEC];
+            dx[v] = fmaf(dy, s, e[v]);
+            e[v] = k.times(dx[v]);
+            dl[v] = free_ >> (j * VEC + v) & 1u ? e[v] * before[j][v] : 0.f;
+        }
+        const int64_t at = (base + t0 + j) * a.D + c;
+        put<E, VEC>(reinterpret_cast<E*>(a.dx) + at, dx);
+        put<float, VEC>(a.dlog_alpha + at, dl);
+        if constexpr (GATE) put<E, VEC>(reinterpret_cast<E*>(a.dg) + at, dg);
+    };
+    if (plain) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const Decay k(d[j][v], slow >> (j * VEC + v) & 1u);
-                const float dy = lane_of<VEC>(o[j], v);
-                float s = 1.f;
-                if constexpr (GATE) {
-                    s = sigmoidf_(lane_of<VEC>(g[j], v));
-                    dg[v] = dy * k.step(before[j][v], lane_of<VEC>(x[j], v)) * s * (1.f - s);
+        for (int j = 0; j < TPW; ++j) again(j);
+#pragma unroll
+        for (int j = TPW - 1; j >= 0; --j) write(j);
+    } else {
+        walk.go_to(s0);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.up(t)) {
+                if (t == walk.first) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) h[v] = a.state_in ? a.state_in[(int64_t)walk.s * a.D + c + v] : 0.f;
                 }
-                dx[v] = fmaf(dy, s, e[v]);
-                e[v] = k.times(dx[v]);
-                dl[v] = free_ >> (j * VEC + v) & 1u ? e[v] * before[j][v] : 0.f;
+                again(j);
             }
-            if (in) {
-                const int64_t at = (base + t) * a.D + c;
-                put<E, VEC>(reinterpret_cast<E*>(a.dx) + at, dx);
-                put<float, VEC>(a.dlog_alpha + at, dl);
-                if constexpr (GATE) put<E, VEC>(reinterpret_cast<E*>(a.dg) + at, dg);
+        }
+        walk.go_to(s1);
+#pragma unroll
+        for (int j = TPW - 1; j >= 0; --j) {
+            const int t = t0 + j;
+            if (t < (int)a.T && walk.down(t)) {
+                if (t == walk.end - 1) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) e[v] = a.d_state ? a.d_state[(int64_t)walk.s * a.D + c + v] : 0.f;
+                }
+                write(j);
                 if (a.d_state_in && t == walk.first) {
 #pragma unroll
                     for (int v = 0; v < VEC; ++v) a.d_state_in[(int64_t)walk.s * a.D + c + v] = e[v];
@@ -564,41 +635,47 @@ __global__ __launch_bounds__(kThreads) void kda_recurrence_step_kernel(Recurrenc
     reinterpret_cast<E*>(a.out)[i] = from_f32<E>(h * s);
 }
 
-int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+int64_t tiles_of(int64_t T, int tile) { return (T + tile - 1) / tile; }
 
 // The workspace: the counter (its own 256 bytes), the look-back words, then
-// for training the state that enters every tile.  One tile a row needs none.
-size_t words_bytes(int64_t B, int64_t T, int64_t D) {
-    return tiles_of(T) > 1 ? ((size_t)(B * tiles_of(T)) * (size_t)D * 8 + 255) / 256 * 256 : 0;
+// for training the state that enters every tile of the backward.  One tile a
+// row needs none.
+size_t words_bytes(int64_t B, int64_t T, int64_t D, int tile) {
+    return tiles_of(T, tile) > 1 ? ((size_t)(B * tiles_of(T, tile)) * (size_t)D * 8 + 255) / 256 * 256 : 0;
 }
 constexpr size_t kCounterBytes = 256;
 
-constexpr int kForwardWaves = 8, kBackwardWaves = 16;
+// Tokens of a wave: 16 in bf16, 8 in fp32, whose registers hold half as many.
+template <typename E> constexpr int kForwardWaves = sizeof(E) == 2 ? 8 : 16;
+constexpr int kBackwardWaves = 8;
 
 template <typename E, int VEC, bool GATE>
 hipError_t launch_scan_v(const RecurrenceArgs& a, bool backward, hipStream_t s) {
     TileGrid g;
-    g.tiles = tiles_of(a.T);
+    g.tiles = tiles_of(a.T, backward ? kBackTile : kTile);
     g.blocks = (int)((a.D + 64 * VEC - 1) / (64 * VEC));
     g.lanes = a.B * g.blocks;
     int32_t* counter = reinterpret_cast<int32_t*>(a.ws);
     uint64_t* words = reinterpret_cast<uint64_t*>(a.ws + kCounterBytes);
-    float* keep = reinterpret_cast<float*>(a.ws + kCounterBytes + words_bytes(a.B, a.T, a.D));
+    // behind the words of the backward, of which there are more
+    float* keep = reinterpret_cast<float*>(a.ws + kCounterBytes + words_bytes(a.B, a.T, a.D, kBackTile));
     if (backward)
         hipLaunchKernelGGL((kda_recurrence_backward_kernel<E, VEC, kBackwardWaves, GATE>), dim3((unsigned)g.total()),
                            dim3(kBackwardWaves * 64), 0, s, a, g, counter, words, keep);
     else
-        hipLaunchKernelGGL((kda_recurrence_kernel<E, VEC, kForwardWaves, GATE>), dim3((unsigned)g.total()),
-                           dim3(kForwardWaves * 64), 0, s, a, g, counter, words, keep);
+        hipLaunchKernelGGL((kda_recurrence_kernel<E, VEC, kForwardWaves<E>, GATE>), dim3((unsigned)g.total()),
+                           dim3(kForwardWaves<E> * 64), 0, s, a, g, counter, words, keep);
     return hipGetLastError();
 }
 
 template <typename E>
-hipError_t launch_scan_t(const RecurrenceArgs& a, bool backward, hipStream_t s) {
+hipError_t launch_scan_t(RecurrenceArgs a, bool backward, hipStream_t s) {
+    if (a.T <= kBackTile) a.keep = false;      // one tile: entered from state_in alone
+    const int tile = backward ? kBackTile : kTile;
     const float* from = backward ? a.d_state : a.state_in;
     float* to = backward ? a.d_state_in : a.state_out;
     const bool empties = to && (a.cu_seqlens || a.T == 0);
-    const int64_t n_clear = a.T > kTile ? (int64_t)((kCounterBytes + words_bytes(a.B, a.T, a.D)) / 8) : 0;
+    const int64_t n_clear = a.T > tile ? (int64_t)((kCounterBytes + words_bytes(a.B, a.T, a.D, tile)) / 8) : 0;
     if (n_clear > 0 || empties) {
         int64_t blocks = (n_clear + 8 * kThreads - 1) / (8 * kThreads);
         if (empties && a.n_seq > blocks) blocks = a.n_seq;
@@ -610,16 +687,16 @@ hipError_t launch_scan_t(const RecurrenceArgs& a, bool backward, hipStream_t s) 
         if (e != hipSuccess) return e;
     }
     if (a.B == 0 || a.T == 0) return hipSuccess;
-    // two channels a lane where rows stay aligned to them
-    if (a.D % 2 == 0) return a.g ? launch_scan_v<E, 2, true>(a, backward, s) : launch_scan_v<E, 2, false>(a, backward, s);
-    return a.g ? launch_scan_v<E, 1, true>(a, backward, s) : launch_scan_v<E, 1, false>(a, backward, s);
+    if (a.D == 1) return a.g ? launch_scan_v<E, 1, true>(a, backward, s) : launch_scan_v<E, 1, false>(a, backward, s);
+    return a.g ? launch_scan_v<E, 2, true>(a, backward, s) : launch_scan_v<E, 2, false>(a, backward, s);
 }
 
 }  // namespace
 
 size_t recurrence_workspace_bytes(int64_t B, int64_t T, int64_t D, bool backward) {
-    if (B == 0 || T <= kTile) return 0;
-    return kCounterBytes + words_bytes(B, T, D) + (backward ? (size_t)(B * tiles_of(T)) * (size_t)D * sizeof(float) : 0);
+    const int tile = backward ? kBackTile : kTile;
+    if (B == 0 || T <= tile) return 0;
+    return kCounterBytes + words_bytes(B, T, D, tile) + (backward ? (size_t)(B * tiles_of(T, tile)) * (size_t)D * sizeof(float) : 0);
 }
 
 hipError_t launch_recurrence(bool bf16, const RecurrenceArgs& a, hipStream_t s) {

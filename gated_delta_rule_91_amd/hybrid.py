@@ -9,12 +9,11 @@ the library's HIP kernels.  Everything here is re-exported by the package.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional
 
-from . import _check, _cu, _expect, _expect_workspace, _io_code, _ptr, _stream, _torch, lib
+from . import KdaError, _cu, _expect, _expect_workspace, _io_code, _stream, _torch, lib
 
 __all__ = ["HYBRID_EXPORTS", "Cache4", "plan_requests", "cache4_append", "cache4_read", "cache4_attention",
            "cache4_attention_workspace_size", "recurrence_workspace_size", "recurrence_backward_workspace_size",
@@ -72,12 +71,32 @@ def _hlib() -> ctypes.CDLL:
     return L
 
 
-def _on(device):
-    """A call's kernels run on its tensors' device, whichever is current."""
+def _in(name: str, x, shape, dtype, device):
+    """The pointer of an argument of the given shape, dtype and device."""
+    if x is None:
+        return None
+    if x.shape != shape or x.dtype != dtype or x.device != device:
+        _expect(name, x, shape, dtype, device)
+    if not x.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return x.data_ptr()
+
+
+def _run(name: str, device, stream, *args) -> None:
+    """Call `name` with the stream behind its arguments, on its tensors' device
+    whichever is current."""
     torch = _torch()
-    if not device.type == "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    f = getattr(_hlib(), name)
+    if device.index == torch.cuda.current_device():
+        # the current stream as the raw handle: a Stream object costs 2 us
+        code = f(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, _stream(stream, device))
+    if code != 0:
+        raise KdaError(name, code)
 
 
 def _scratch(nbytes: int, device, stream):
@@ -100,7 +119,9 @@ def _workspace(workspace, nbytes: int, device, stream):
             return None, None, 0
     else:
         _expect_workspace(workspace, device)
-    return workspace, _ptr(workspace), workspace.numel()
+        if not workspace.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def plan_requests(past_lens, new_lens, block_table, free_pages, page_size: int, tokens: int, stream=None):
@@ -113,27 +134,23 @@ def plan_requests(past_lens, new_lens, block_table, free_pages, page_size: int, 
     int32 [n], slot_map int64 [tokens], pages_taken int32 [1]); the caller
     drops the first pages_taken entries of free_pages."""
     torch = _torch()
-    dev = past_lens.device
-    n = past_lens.shape[0] if past_lens.dim() == 1 else -1
-    _expect("past_lens", past_lens, (max(n, 0),), torch.int32, dev)
-    _expect("new_lens", new_lens, (n,), torch.int32, dev)
-    if block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("block_table must be [n, max_pages] and free_pages 1-D")
-    _expect("block_table", block_table, (n, block_table.shape[1]), torch.int32, dev)
-    _expect("free_pages", free_pages, (free_pages.shape[0],), torch.int32, dev)
+    dev, i32 = past_lens.device, torch.int32
+    if past_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("past_lens and free_pages must be 1-D and block_table [n, max_pages]")
     if page_size not in PAGE_SIZES:
         raise ValueError(f"page_size must be one of {PAGE_SIZES}, got {page_size!r}")
     if tokens < 0:
         raise ValueError(f"tokens must not be negative, got {tokens}")
-    cu = torch.empty(n + 1, dtype=torch.int32, device=dev)
-    total = torch.empty(n, dtype=torch.int32, device=dev)
-    taken = torch.empty(1, dtype=torch.int32, device=dev)
+    n, max_pages, n_free = past_lens.shape[0], block_table.shape[1], free_pages.shape[0]
+    args = (_in("past_lens", past_lens, (n,), i32, dev), _in("new_lens", new_lens, (n,), i32, dev),
+            _in("block_table", block_table, (n, max_pages), i32, dev), n_free,
+            _in("free_pages", free_pages, (n_free,), i32, dev))
+    cu = torch.empty(n + 1, dtype=i32, device=dev)
+    total = torch.empty(n, dtype=i32, device=dev)
+    taken = torch.empty(1, dtype=i32, device=dev)
     slots = torch.empty(tokens, dtype=torch.int64, device=dev)
-    with _on(dev):
-        _check("kda_plan_requests", _hlib().kda_plan_requests(
-            n, tokens, page_size, block_table.shape[1], _ptr(past_lens), _ptr(new_lens), _ptr(block_table),
-            free_pages.shape[0], _ptr(free_pages), _ptr(cu), _ptr(total), _ptr(slots), _ptr(taken),
-            _stream(stream, dev)))
+    _run("kda_plan_requests", dev, stream, n, tokens, page_size, max_pages, *args, cu.data_ptr(), total.data_ptr(),
+         slots.data_ptr(), taken.data_ptr())
     return cu, total, slots, taken
 
 
@@ -148,14 +165,19 @@ class Cache4:
             raise ValueError(f"k must be [pages, heads, page_size, d/2] with page_size in {PAGE_SIZES} and d 64 or "
                              f"128, got {tuple(k.shape)}")
         pages, heads, page_size, half = k.shape
-        scales = (pages, heads, page_size, half // 16)
-        _expect("k", k, k.shape, torch.uint8, k.device)
-        _expect("k_scale", k_scale, scales, torch.uint8, k.device)
-        _expect("v", v, k.shape, torch.uint8, k.device)
-        _expect("v_scale", v_scale, scales, torch.uint8, k.device)
-        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        scales, dev, u8 = (pages, heads, page_size, half // 16), k.device, torch.uint8
+        self._struct = KdaCache4(pages, page_size, heads, 2 * half, _in("k", k, k.shape, u8, dev),
+                                 _in("k_scale", k_scale, scales, u8, dev), _in("v", v, k.shape, u8, dev),
+                                 _in("v_scale", v_scale, scales, u8, dev))
+        self._tensors = (k, k_scale, v, v_scale)
         self.pages, self.heads, self.page_size, self.d = pages, heads, page_size, 2 * half
-        self.device = k.device
+        self.device = dev
+
+    # the tensors of a cache stay the ones it was made with
+    k = property(lambda self: self._tensors[0])
+    k_scale = property(lambda self: self._tensors[1])
+    v = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, d: int, device="cuda") -> "Cache4":
@@ -165,16 +187,10 @@ class Cache4:
         scales = [torch.zeros((pages, heads, page_size, d // 32), dtype=torch.uint8, device=device) for _ in range(2)]
         return cls(codes[0], scales[0], codes[1], scales[1])
 
-    def _struct(self) -> KdaCache4:
-        return KdaCache4(self.pages, self.page_size, self.heads, self.d, _ptr(self.k), _ptr(self.k_scale),
-                         _ptr(self.v), _ptr(self.v_scale))
 
-
-def _expect_slots(slot_map, device) -> int:
-    torch = _torch()
+def _rows_of(slot_map) -> int:
     if slot_map.dim() != 1:
         raise ValueError("slot_map must be 1-D")
-    _expect("slot_map", slot_map, slot_map.shape, torch.int64, device)
     return slot_map.shape[0]
 
 
@@ -182,59 +198,50 @@ def cache4_append(cache: Cache4, k, v, slot_map, stream=None) -> None:
     """Round k, v [T, heads, d] (bf16 or fp32) into the cache at slot_map int64
     [T] (page * page_size + offset; slots outside the cache are dropped, and no
     two rows may name one slot)."""
-    T = _expect_slots(slot_map, cache.device)
-    io = _io_code(k.dtype)
-    _expect("k", k, (T, cache.heads, cache.d), k.dtype, cache.device)
-    _expect("v", v, (T, cache.heads, cache.d), k.dtype, cache.device)
-    with _on(cache.device):
-        _check("kda_cache4_append", _hlib().kda_cache4_append(
-            cache._struct(), T, io, _ptr(k), _ptr(v), _ptr(slot_map), _stream(stream, cache.device)))
+    T, io, dev = _rows_of(slot_map), _io_code(k.dtype), cache.device
+    shape = (T, cache.heads, cache.d)
+    args = (_in("k", k, shape, k.dtype, dev), _in("v", v, shape, k.dtype, dev),
+            _in("slot_map", slot_map, (T,), _torch().int64, dev))
+    _run("kda_cache4_append", dev, stream, cache._struct, T, io, *args)
 
 
 def cache4_read(cache: Cache4, slot_map, dtype, stream=None):
     """(k, v) [T, heads, d] of the rows at slot_map, as the values they stand
     for; zeros for slots outside the cache."""
     torch = _torch()
-    T = _expect_slots(slot_map, cache.device)
-    io = _io_code(dtype)
-    k, v = (torch.empty((T, cache.heads, cache.d), dtype=dtype, device=cache.device) for _ in range(2))
-    with _on(cache.device):
-        _check("kda_cache4_read", _hlib().kda_cache4_read(
-            cache._struct(), T, io, _ptr(slot_map), _ptr(k), _ptr(v), _stream(stream, cache.device)))
+    T, io, dev = _rows_of(slot_map), _io_code(dtype), cache.device
+    slots = _in("slot_map", slot_map, (T,), torch.int64, dev)
+    k = torch.empty((T, cache.heads, cache.d), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _run("kda_cache4_read", dev, stream, cache._struct, T, io, slots, k.data_ptr(), v.data_ptr())
     return k, v
 
 
-def _attention_problem(cache, q, block_table, n_seq, scale, max_q, max_len) -> KdaCache4AttentionProblem:
-    T, heads, _ = q.shape
-    if heads % cache.heads:
-        raise ValueError(f"{heads} query heads over {cache.heads} key/value heads")
-    scale = 1.0 / math.sqrt(cache.d) if scale is None else float(scale)
-    if max_len is None:
-        max_len = block_table.shape[1] * cache.page_size
-    return KdaCache4AttentionProblem(n_seq, T, heads, block_table.shape[1], max(int(max_q), 1), max(int(max_len), 0),
-                                     _io_code(q.dtype), scale)
-
-
-def _attention_inputs(q, cache, block_table, total_lens, cu_seqlens, scale, max_q, max_len):
-    torch = _torch()
-    dev = cache.device
+def _attention_problem(q, cache, block_table, total_lens, cu_seqlens, scale, max_q, max_len):
+    """(problem, pointers of q, block_table, total_lens and cu_seqlens) of checked inputs."""
+    i32, dev = _torch().int32, cache.device
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [T, heads, d] and block_table [n_seq, max_pages]")
-    T, heads, d = q.shape
-    n_seq = T if cu_seqlens is None else _cu(cu_seqlens, dev)
-    _expect("q", q, (T, heads, cache.d), q.dtype, dev)
-    _expect("block_table", block_table, (n_seq, block_table.shape[1]), torch.int32, dev)
-    _expect("total_lens", total_lens, (n_seq,), torch.int32, dev)
+    T, heads, _ = q.shape
+    n_seq, max_pages = T if cu_seqlens is None else _cu(cu_seqlens, dev), block_table.shape[1]
+    io = _io_code(q.dtype)
+    ptrs = (_in("q", q, (T, heads, cache.d), q.dtype, dev), _in("block_table", block_table, (n_seq, max_pages), i32, dev),
+            _in("total_lens", total_lens, (n_seq,), i32, dev), _in("cu_seqlens", cu_seqlens, (n_seq + 1,), i32, dev))
+    if heads % cache.heads:
+        raise ValueError(f"{heads} query heads over {cache.heads} key/value heads")
     if max_q is None:
-        max_q = 1 if cu_seqlens is None else max(T, 1)
-    return _attention_problem(cache, q, block_table, n_seq, scale, max_q, max_len)
+        max_q = 1 if cu_seqlens is None else T
+    if max_len is None:
+        max_len = max_pages * cache.page_size
+    return KdaCache4AttentionProblem(n_seq, T, heads, max_pages, max(int(max_q), 1), max(int(max_len), 0), io,
+                                     1.0 / math.sqrt(cache.d) if scale is None else float(scale)), ptrs
 
 
 def cache4_attention_workspace_size(q, cache: Cache4, block_table, total_lens, cu_seqlens=None, max_q=None,
                                     max_len=None) -> int:
     """Bytes of workspace that cache4_attention needs for these arguments."""
-    p = _attention_inputs(q, cache, block_table, total_lens, cu_seqlens, None, max_q, max_len)
-    return _hlib().kda_cache4_attention_workspace_size(cache._struct(), p)
+    p, _ = _attention_problem(q, cache, block_table, total_lens, cu_seqlens, None, max_q, max_len)
+    return _hlib().kda_cache4_attention_workspace_size(cache._struct, p)
 
 
 def cache4_attention(q, cache: Cache4, block_table, total_lens, cu_seqlens=None, g=None,
@@ -250,37 +257,36 @@ def cache4_attention(q, cache: Cache4, block_table, total_lens, cu_seqlens=None,
     defaults to 1/sqrt(d).  max_q and max_len, about the most queries and the
     most tokens of a sequence, steer how the work is split, and nothing else.
     Returns out [T, heads, d]."""
-    torch = _torch()
     dev = cache.device
-    p = _attention_inputs(q, cache, block_table, total_lens, cu_seqlens, scale, max_q, max_len)
-    _expect("g", g, q.shape, q.dtype, dev)
-    _expect("out", out, q.shape, q.dtype, dev)
+    p, ptrs = _attention_problem(q, cache, block_table, total_lens, cu_seqlens, scale, max_q, max_len)
+    gate = _in("g", g, q.shape, q.dtype, dev)
     if out is None:
-        out = torch.empty_like(q)
-    c = cache._struct()
-    with _on(dev):
-        ws, ws_ptr, nbytes = _workspace(workspace, _hlib().kda_cache4_attention_workspace_size(c, p), dev, stream)
-        _check("kda_cache4_attention", _hlib().kda_cache4_attention(
-            c, p, _ptr(q), _ptr(block_table), _ptr(total_lens), _ptr(cu_seqlens), _ptr(g), _ptr(out), ws_ptr, nbytes,
-            _stream(stream, dev)))
+        out = _torch().empty_like(q)
+    to = _in("out", out, q.shape, q.dtype, dev)
+    c = cache._struct
+    ws, ws_ptr, nbytes = _workspace(workspace, _hlib().kda_cache4_attention_workspace_size(c, p), dev, stream)
+    _run("kda_cache4_attention", dev, stream, c, p, *ptrs, gate, to, ws_ptr, nbytes)
     return out
 
 
-def _recurrence_problem(x, log_alpha, log_alpha_min, g, cu_seqlens):
-    """(problem, rows of the states) of checked inputs."""
+def _recurrence_problem(x, log_alpha, log_alpha_min, g, state_in, cu_seqlens):
+    """(problem, shape of the states, pointers of x, log_alpha, g, state_in and
+    cu_seqlens) of checked inputs."""
     torch = _torch()
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
-    B, T, D = x.shape
-    io = _io_code(x.dtype)
-    _expect("log_alpha", log_alpha, (B, T, D), torch.float32, x.device)
-    _expect("g", g, (B, T, D), x.dtype, x.device)
+    (B, T, D), dtype, dev = x.shape, x.dtype, x.device
+    io = _io_code(dtype)
     n_seq = -1
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("a packed batch is [1, T, D]")
-        n_seq = _cu(cu_seqlens, x.device)
-    return KdaRecurrenceProblem(B, T, D, n_seq, io, float(log_alpha_min)), B if n_seq < 0 else n_seq
+        n_seq = _cu(cu_seqlens, dev)
+    states = (B if n_seq < 0 else n_seq, D)
+    ptrs = (_in("x", x, (B, T, D), dtype, dev), _in("log_alpha", log_alpha, (B, T, D), torch.float32, dev),
+            _in("g", g, (B, T, D), dtype, dev), _in("state_in", state_in, states, torch.float32, dev),
+            _in("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, dev))
+    return KdaRecurrenceProblem(B, T, D, n_seq, io, float(log_alpha_min)), states, ptrs
 
 
 def recurrence_workspace_size(p: KdaRecurrenceProblem) -> int:
@@ -294,20 +300,15 @@ def recurrence_backward_workspace_size(p: KdaRecurrenceProblem) -> int:
 def _recurrence_forward(name, size, x, log_alpha, log_alpha_min, g, state_in, cu_seqlens, out, state_out, want_state,
                         workspace, stream):
     torch = _torch()
-    p, n = _recurrence_problem(x, log_alpha, log_alpha_min, g, cu_seqlens)
-    dev, D = x.device, x.shape[2]
-    _expect("state_in", state_in, (n, D), torch.float32, dev)
-    _expect("out", out, x.shape, x.dtype, dev)
-    _expect("state_out", state_out, (n, D), torch.float32, dev)
+    p, states, ptrs = _recurrence_problem(x, log_alpha, log_alpha_min, g, state_in, cu_seqlens)
+    dev = x.device
     if out is None:
         out = torch.empty_like(x)
     if state_out is None and want_state:
-        state_out = torch.empty((n, D), dtype=torch.float32, device=dev)
-    with _on(dev):
-        ws, ws_ptr, nbytes = _workspace(workspace, size(p), dev, stream)
-        _check(name, getattr(_hlib(), name)(
-            p, _ptr(x), _ptr(log_alpha), _ptr(g), _ptr(state_in), _ptr(cu_seqlens), _ptr(out), _ptr(state_out), ws_ptr,
-            nbytes, _stream(stream, dev)))
+        state_out = torch.empty(states, dtype=torch.float32, device=dev)
+    to = (_in("out", out, x.shape, x.dtype, dev), _in("state_out", state_out, states, torch.float32, dev))
+    ws, ws_ptr, nbytes = _workspace(workspace, size(p), dev, stream)
+    _run(name, dev, stream, p, *ptrs, *to, ws_ptr, nbytes)
     return out, state_out, ws
 
 
@@ -341,20 +342,15 @@ def recurrence_backward(x, log_alpha, log_alpha_min: float, workspace, g=None, s
     dg (dtype of x; dg None without g), dlog_alpha fp32 and dstate0 (None
     unless want_dstate)."""
     torch = _torch()
-    p, n = _recurrence_problem(x, log_alpha, log_alpha_min, g, cu_seqlens)
-    dev, D = x.device, x.shape[2]
-    _expect("state_in", state_in, (n, D), torch.float32, dev)
-    _expect("d_out", d_out, x.shape, x.dtype, dev)
-    _expect("d_state", d_state, (n, D), torch.float32, dev)
-    _expect_workspace(workspace, dev)
+    p, states, ptrs = _recurrence_problem(x, log_alpha, log_alpha_min, g, state_in, cu_seqlens)
+    dev = x.device
+    grads = (_in("d_out", d_out, x.shape, x.dtype, dev), _in("d_state", d_state, states, torch.float32, dev))
     r = dict(dx=torch.empty_like(x), dlog_alpha=torch.empty_like(log_alpha),
              dg=torch.empty_like(g) if g is not None else None,
-             dstate0=torch.empty((n, D), dtype=torch.float32, device=dev) if want_dstate else None)
-    with _on(dev):
-        _check("kda_recurrence_backward", _hlib().kda_recurrence_backward(
-            p, _ptr(x), _ptr(log_alpha), _ptr(g), _ptr(state_in), _ptr(cu_seqlens), _ptr(d_out), _ptr(d_state),
-            _ptr(r["dx"]), _ptr(r["dlog_alpha"]), _ptr(r["dg"]), _ptr(r["dstate0"]), _ptr(workspace),
-            workspace.numel(), _stream(stream, dev)))
+             dstate0=torch.empty(states, dtype=torch.float32, device=dev) if want_dstate else None)
+    to = (None if r[k] is None else r[k].data_ptr() for k in ("dx", "dlog_alpha", "dg", "dstate0"))
+    _, ws_ptr, nbytes = _workspace(workspace, 0, dev, stream)
+    _run("kda_recurrence_backward", dev, stream, p, *ptrs, *grads, *to, ws_ptr, nbytes)
     return r
 
 
@@ -402,17 +398,12 @@ def recurrence_step(x, log_alpha, state, log_alpha_min: float, g=None, out=None,
     torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [N, D]")
-    N, D = x.shape
-    dev = x.device
-    io = _io_code(x.dtype)
-    _expect("log_alpha", log_alpha, (N, D), torch.float32, dev)
-    _expect("state", state, (N, D), torch.float32, dev)
-    _expect("g", g, (N, D), x.dtype, dev)
-    _expect("out", out, (N, D), x.dtype, dev)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    io = _io_code(dtype)
+    ptrs = (_in("x", x, shape, dtype, dev), _in("log_alpha", log_alpha, shape, torch.float32, dev),
+            _in("g", g, shape, dtype, dev), _in("state", state, shape, torch.float32, dev))
     if out is None:
         out = torch.empty_like(x)
-    with _on(dev):
-        _check("kda_recurrence_step", _hlib().kda_recurrence_step(
-            N, D, io, float(log_alpha_min), _ptr(x), _ptr(log_alpha), _ptr(g), _ptr(state), _ptr(out),
-            _stream(stream, dev)))
+    _run("kda_recurrence_step", dev, stream, shape[0], shape[1], io, float(log_alpha_min), *ptrs,
+         _in("out", out, shape, dtype, dev))
     return out
