@@ -10,8 +10,9 @@
 // value by that one rounding only.  The range of e keeps every value
 // (1/2 * 2^-125 to 6 * 2^125) a normal number of bf16 and fp32.
 //
-// Both calls stream: 8 channels a thread (one 16-byte load of bf16), four
-// threads a scale, whose maximum is two lane exchanges.  Bound by HBM.
+// Both calls stream: a thread has the same 8 channels of a row's key and value
+// (one 16-byte load of bf16 each), four threads a scale, whose maximum is two
+// exchanges within the quad.  Bound by HBM.
 #include "kda_common.hpp"
 #include "kda_hybrid_internal.hpp"
 
@@ -37,82 +38,101 @@ __device__ __forceinline__ void store8(E* p, const float (&x)[8]) {
     *reinterpret_cast<Eight<E>*>(__builtin_assume_aligned(p, 16)) = v;
 }
 
-// Row index of a slot within the cache's [pages, heads, page_size] rows, or
-// -1 outside it.
-__device__ __forceinline__ int64_t row_of(const Cache4Args& c, int64_t slot, int h) {
-    if (slot < 0) return -1;
-    const int64_t page = slot >> c.page_shift;
-    if (page >= c.pages) return -1;
-    return ((page * c.heads + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
+// What a thread works on: channels [8 j, 8 j + 8) of row th (token, head), and
+// the row of the cache, of its [pages, heads, page_size] rows, or -1.
+struct Piece {
+    int th, j;
+    int64_t row;
+};
+template <int D>
+__device__ __forceinline__ bool piece_of(const Cache4RowsArgs& a, Piece& p) {
+    constexpr int TPR = D / 8;                 // threads per row
+    const int in = threadIdx.x;
+    p.th = (int)blockIdx.x * (kThreads / TPR) + in / TPR;
+    p.j = in % TPR;
+    if (p.th >= (int)a.tokens * a.c.heads) return false;      // whole rows leave together
+    const int token = (int)((uint32_t)p.th / (uint32_t)a.c.heads), h = p.th - token * a.c.heads;
+    const int64_t slot = a.slot_map[token], page = slot >> a.c.page_shift;
+    p.row = slot < 0 || page >= a.c.pages ? -1 : ((page * a.c.heads + h) << a.c.page_shift) + (slot & ((1 << a.c.page_shift) - 1));
+    return true;
 }
 
-// The code (sign and three bits) of y = x / 2^e.
-__device__ __forceinline__ uint32_t code_of(float y) {
-    const float a = fabsf(y);
-    const uint32_t m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-    return m | ((__float_as_uint(y) >> 31) << 3);
+// The largest over the lanes of a quad.
+__device__ __forceinline__ uint32_t over_quad(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xb1, 0xf, 0xf, true));    // lanes 1 0 3 2
+    return max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4e, 0xf, 0xf, true)); // lanes 2 3 0 1
+}
+
+// The word of 8 codes of x and the scale byte of its quad.
+__device__ __forceinline__ void round8(const float (&x)[8], uint32_t& word, uint8_t& scale) {
+    uint32_t m = 0;                            // magnitudes order like their bits; NaN above all
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
+    m = over_quad(m);
+    int e = (int)(m >> 23) - 127 - 2 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = min(max(e, kScaleLow), kScaleHigh);
+    // the conversion divides by the scale, rounds halves to the even code and
+    // takes magnitudes over 6 as 6
+    const float unit = __uint_as_float((uint32_t)(127 + e) << 23);
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], unit, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], unit, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], unit, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], unit, 3);
+    const bool finite = m < 0x7f800000u;
+    word = finite ? w : 0u;
+    scale = finite ? (uint8_t)(e + 127) : (uint8_t)255;
+}
+
+// What a word of 8 codes stands for, with their scale byte.
+__device__ __forceinline__ void values8(uint32_t w, uint32_t scale, float (&x)[8]) {
+    const float unit = __uint_as_float(scale << 23);    // only the exponent counts: 0 is 2^-127, 255 NaN
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, unit, 3);
+    x[0] = a[0]; x[1] = a[1]; x[2] = b[0]; x[3] = b[1]; x[4] = c[0]; x[5] = c[1]; x[6] = d[0]; x[7] = d[1];
 }
 
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void kda_cache4_append_kernel(Cache4RowsArgs a) {
-    constexpr int TPR = D / 8;                 // threads per row
-    const int64_t per = a.tokens * a.c.heads * TPR;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= per) return;                      // whole groups of four leave together: per is a multiple of 8
-    const int j = (int)(i % TPR);
-    const int64_t th = i / TPR;
-    const bool v = blockIdx.y == 1;
-    const int64_t row = row_of(a.c, a.slot_map[th / a.c.heads], (int)(th % a.c.heads));
-    float x[8];
-    load8(reinterpret_cast<const E*>(v ? a.v_in : a.k_in) + th * D + 8 * j, x);
-    uint32_t m = 0;                            // magnitudes order like their bits; NaN above all
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-    const bool finite = m < 0x7f800000u;
-    int e = (int)(m >> 23) - 127 - 2 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = min(max(e, kScaleLow), kScaleHigh);
-    const float unit = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w |= code_of(x[k] * unit) << (4 * k);
-    if (row < 0) return;
-    reinterpret_cast<uint32_t*>(v ? a.c.v : a.c.k)[row * TPR + j] = finite ? w : 0u;
-    if ((j & 3) == 0) (v ? a.c.v_scale : a.c.k_scale)[row * (D / 32) + j / 4] = finite ? (uint8_t)(e + 127) : 255;
+    Piece p;
+    if (!piece_of<D>(a, p)) return;
+    const int64_t from = (int64_t)p.th * D + 8 * p.j;
+    float k[8], v[8];
+    load8(reinterpret_cast<const E*>(a.k_in) + from, k);
+    load8(reinterpret_cast<const E*>(a.v_in) + from, v);
+    uint32_t wk, wv;
+    uint8_t sk, sv;
+    round8(k, wk, sk);
+    round8(v, wv, sv);
+    if (p.row < 0) return;
+    reinterpret_cast<uint32_t*>(a.c.k)[p.row * (D / 8) + p.j] = wk;
+    reinterpret_cast<uint32_t*>(a.c.v)[p.row * (D / 8) + p.j] = wv;
+    if ((p.j & 3) == 0) {
+        a.c.k_scale[p.row * (D / 32) + p.j / 4] = sk;
+        a.c.v_scale[p.row * (D / 32) + p.j / 4] = sv;
+    }
 }
 
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void kda_cache4_read_kernel(Cache4RowsArgs a) {
-    constexpr int TPR = D / 8;
-    const int64_t per = a.tokens * a.c.heads * TPR;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= per) return;
-    const int j = (int)(i % TPR);
-    const int64_t th = i / TPR;
-    const bool v = blockIdx.y == 1;
-    const int64_t row = row_of(a.c, a.slot_map[th / a.c.heads], (int)(th % a.c.heads));
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (row >= 0) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(v ? a.c.v : a.c.k)[row * TPR + j];
-        const uint32_t b = (v ? a.c.v_scale : a.c.k_scale)[row * (D / 32) + j / 4];
-        // 255: NaN; 0: 2^-127, a subnormal
-        const float unit = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : b << 23);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t c = w >> (4 * k), m = c & 7u;
-            // 0, 1/2, then (1 + bit / 2) 2^(x - 1): exponent x and one mantissa bit
-            const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-            x[k] = (c & 8u ? -mag : mag) * unit;
-        }
+    Piece p;
+    if (!piece_of<D>(a, p)) return;
+    float k[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (p.row >= 0) {
+        const int64_t w = p.row * (D / 8) + p.j, s = p.row * (D / 32) + p.j / 4;
+        const uint32_t wk = reinterpret_cast<const uint32_t*>(a.c.k)[w], wv = reinterpret_cast<const uint32_t*>(a.c.v)[w];
+        const uint32_t sk = a.c.k_scale[s], sv = a.c.v_scale[s];
+        values8(wk, sk, k);
+        values8(wv, sv, v);
     }
-    store8(reinterpret_cast<E*>(v ? a.v_out : a.k_out) + th * D + 8 * j, x);
+    const int64_t to = (int64_t)p.th * D + 8 * p.j;
+    store8(reinterpret_cast<E*>(a.k_out) + to, k);
+    store8(reinterpret_cast<E*>(a.v_out) + to, v);
 }
 
-// Threads of one of K and V: 16 a row of d = 128.
 dim3 rows_grid(int d, const Cache4RowsArgs& a) {
-    const int64_t threads = a.tokens * a.c.heads * (d / 8);
-    return dim3((unsigned)((threads + kThreads - 1) / kThreads), 2);
+    const int per = kThreads / (d / 8);        // rows of a workgroup
+    return dim3((unsigned)((a.tokens * a.c.heads + per - 1) / per));
 }
 
 }  // namespace

@@ -55,7 +55,7 @@ kda_status check_rows(const kda_cache4* c, int64_t tokens, kda_dtype io, const v
     kda_status st = check_cache(c);
     if (st != KDA_OK) return st;
     if (tokens < 0 || !ok_io(io)) return KDA_ERR_INVALID_ARGUMENT;
-    if (mul_sat(mul_sat(tokens, c->heads), c->d) > ((int64_t)1 << 40)) return KDA_ERR_UNSUPPORTED;
+    if (mul_sat(tokens, c->heads) > INT32_MAX) return KDA_ERR_UNSUPPORTED;   // rows are 32-bit in the kernels
     const bool any = tokens > 0;
     if (!ok_ptr(k, any) || !ok_ptr(v, any) || !ok_elem(slot_map, any, 8)) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;

@@ -118,10 +118,17 @@ struct Walk {
     __device__ __forceinline__ Walk(const RecurrenceArgs& a, int row, int t)
         : cu(a.cu_seqlens), n((int)a.n_seq), T((int)a.T), s(row), first(0), end((int)a.T) {
         if (!cu) return;
-        int lo = 0, hi = n;               // the last sequence that begins at or before t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t) lo = mid; else hi = mid;
+        // The last sequence that begins at or before t, 64 candidates at a
+        // time in the lanes: one load of latency up to 64 sequences, two up
+        // to 4096.
+        int lo = 0, many = n;
+        while (many > 1) {
+            const int stride = (many + 63) / 64, at = lo + (int)(threadIdx.x & 63) * stride;
+            const bool before = at < lo + many && cu[at] <= t;
+            const int k = __popcll(__ballot(before));
+            const int next = lo + (k > 0 ? k - 1 : 0) * stride;
+            many = min(stride, lo + many - next);
+            lo = next;
         }
         s = lo;
         bounds();
@@ -241,6 +248,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_kernel(Recurrenc
     const int64_t c = ch.c;
     const int t0 = (int)(i * kTile) + wave * TPW;
 
+    Walk walk(a, (int)row, t0);
     EV x[TPW], g[TPW];
     float d[TPW][VEC];
     const int64_t base = row * a.T;
@@ -258,7 +266,6 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_kernel(Recurrenc
     float h[VEC], sum[VEC];
     uint32_t slow = 0;
     bool cut = false;
-    Walk walk(a, (int)row, t0);
     const int s0 = walk.s;
     const bool plain = walk.inside(t0, TPW);
 #pragma unroll
@@ -397,6 +404,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_backward_kernel(
     const int64_t c = ch.c;
     const int t0 = (int)(i * kBackTile) + wave * TPW;
 
+    Walk walk(a, (int)row, t0);
     EV x[TPW], g[TPW], o[TPW];
     float d[TPW][VEC];
     const int64_t base = row * a.T;
@@ -419,7 +427,6 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_backward_kernel(
     float h[VEC], e[VEC], sum[VEC];
     uint32_t slow = 0, free_ = 0;                 // free_: the floor does not bind
     bool first = false, last = false;
-    Walk walk(a, (int)row, t0);
     const int s0 = walk.s;
     const bool plain = walk.inside(t0, TPW);
 #pragma unroll
@@ -625,14 +632,31 @@ __global__ __launch_bounds__(kThreads) void kda_recurrence_begin_kernel(uint64_t
     }
 }
 
+// N elements from i on (aligned to N of them).
+template <typename E, int N>
+__device__ __forceinline__ void step_elements(const RecurrenceStepArgs& a, int64_t i) {
+    const auto x = get<E, N>(reinterpret_cast<const E*>(a.x) + i);
+    const auto l = get<float, N>(a.log_alpha + i), h0 = get<float, N>(a.state + i);
+    auto g = x;
+    if (a.g) g = get<E, N>(reinterpret_cast<const E*>(a.g) + i);
+    float h[N], y[N];
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        h[v] = Decay(fmaxf(lane_of<N>(l, v), a.floor_)).step(lane_of<N>(h0, v), lane_of<N>(x, v));
+        y[v] = a.g ? h[v] * sigmoidf_(lane_of<N>(g, v)) : h[v];
+    }
+    put<float, N>(a.state + i, h);
+    put<E, N>(reinterpret_cast<E*>(a.out) + i, y);
+}
+
+// Bound by HBM, by latency when small: four elements a thread, the last ones
+// one by one.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void kda_recurrence_step_kernel(RecurrenceStepArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.n) return;
-    const float h = Decay(fmaxf(a.log_alpha[i], a.floor_)).step(a.state[i], to_f32(reinterpret_cast<const E*>(a.x)[i]));
-    a.state[i] = h;
-    const float s = a.g ? sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i])) : 1.f;
-    reinterpret_cast<E*>(a.out)[i] = from_f32<E>(h * s);
+    const int64_t i = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x);
+    if (i + 4 <= a.n) step_elements<E, 4>(a, i);
+    else
+        for (int64_t k = i; k < a.n; ++k) step_elements<E, 1>(a, k);
 }
 
 int64_t tiles_of(int64_t T, int tile) { return (T + tile - 1) / tile; }
@@ -708,7 +732,7 @@ hipError_t launch_recurrence_backward(bool bf16, const RecurrenceArgs& a, hipStr
 }
 
 hipError_t launch_recurrence_step(bool bf16, const RecurrenceStepArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.n + kThreads - 1) / kThreads));
+    const dim3 grid((unsigned)((a.n + 4 * kThreads - 1) / (4 * kThreads)));
     if (bf16) hipLaunchKernelGGL(kda_recurrence_step_kernel<__bf16>, grid, dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL(kda_recurrence_step_kernel<float>, grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
