@@ -39,19 +39,23 @@ __device__ __forceinline__ void store8(E* p, const float (&x)[8]) {
 }
 
 // What a thread works on: channels [8 j, 8 j + 8) of row th (token, head), and
-// the row of the cache, of its [pages, heads, page_size] rows, or -1.
+// the row of the cache, of its [pages, heads, page_size] rows, or -1.  A
+// workgroup has consecutive tokens of one head, whose slots mostly follow each
+// other: it writes whole lines of the cache (with tokens and heads the other
+// way round the append took 87 us instead of 85, the read 63 instead of 55, on 64K
+// tokens x 8 heads; two rows a thread take 89 and 60).
 struct Piece {
-    int th, j;
-    int64_t row;
+    int64_t th, row;
+    int j;
 };
 template <int D>
 __device__ __forceinline__ bool piece_of(const Cache4RowsArgs& a, Piece& p) {
     constexpr int TPR = D / 8;                 // threads per row
-    const int in = threadIdx.x;
-    p.th = (int)blockIdx.x * (kThreads / TPR) + in / TPR;
-    p.j = in % TPR;
-    if (p.th >= (int)a.tokens * a.c.heads) return false;      // whole rows leave together
-    const int token = (int)((uint32_t)p.th / (uint32_t)a.c.heads), h = p.th - token * a.c.heads;
+    const int tb = (int)((uint32_t)blockIdx.x / (uint32_t)a.c.heads), h = (int)blockIdx.x - tb * a.c.heads;
+    const int64_t token = (int64_t)tb * (kThreads / TPR) + threadIdx.x / TPR;
+    p.j = threadIdx.x % TPR;
+    if (token >= a.tokens) return false;       // whole rows leave together
+    p.th = token * a.c.heads + h;
     const int64_t slot = a.slot_map[token], page = slot >> a.c.page_shift;
     p.row = slot < 0 || page >= a.c.pages ? -1 : ((page * a.c.heads + h) << a.c.page_shift) + (slot & ((1 << a.c.page_shift) - 1));
     return true;
@@ -96,7 +100,7 @@ template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void kda_cache4_append_kernel(Cache4RowsArgs a) {
     Piece p;
     if (!piece_of<D>(a, p)) return;
-    const int64_t from = (int64_t)p.th * D + 8 * p.j;
+    const int64_t from = p.th * D + 8 * p.j;
     float k[8], v[8];
     load8(reinterpret_cast<const E*>(a.k_in) + from, k);
     load8(reinterpret_cast<const E*>(a.v_in) + from, v);
@@ -125,14 +129,14 @@ __global__ __launch_bounds__(kThreads) void kda_cache4_read_kernel(Cache4RowsArg
         values8(wk, sk, k);
         values8(wv, sv, v);
     }
-    const int64_t to = (int64_t)p.th * D + 8 * p.j;
+    const int64_t to = p.th * D + 8 * p.j;
     store8(reinterpret_cast<E*>(a.k_out) + to, k);
     store8(reinterpret_cast<E*>(a.v_out) + to, v);
 }
 
 dim3 rows_grid(int d, const Cache4RowsArgs& a) {
     const int per = kThreads / (d / 8);        // rows of a workgroup
-    return dim3((unsigned)((a.tokens * a.c.heads + per - 1) / per));
+    return dim3((unsigned)((a.tokens + per - 1) / per * a.c.heads));
 }
 
 }  // namespace
