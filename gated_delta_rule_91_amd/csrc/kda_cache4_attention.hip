@@ -189,6 +189,9 @@ __device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* 
     return sum;
 }
 
+// Whether values with this scale may be Inf or NaN.
+__device__ __forceinline__ bool is_odd(float scale) { return (__float_as_uint(scale) >> 23) >= 253u; }
+
 __device__ __forceinline__ float scale_bits(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // 8 channels of a word, times their scale.
@@ -218,13 +221,17 @@ __device__ __forceinline__ void two_channels(const uint32_t (&w)[8], const float
     hi = __builtin_bit_cast(bf16x8, b);
 }
 
+// The larger of two, NaN if one is: one instruction for three of them, where
+// fmaxf first quiets each.  A row with a NaN score is NaN whatever its maximum.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 // The largest over the four lanes with the same n.
 __device__ __forceinline__ float over_g(float x) {
     const uint32_t b = __float_as_uint(x);
     const auto p = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+    const uint32_t c = __float_as_uint(larger(__uint_as_float(p[0]), __uint_as_float(p[1])));
     const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
-    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+    return larger(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
 // x in PARTS bf16 parts whose sum holds 8 PARTS bits of it.
@@ -266,33 +273,69 @@ struct Pages {
     }
 };
 
-// A half whose page does not exist reads page 0 (there is one: a cache without
-// pages counts no tokens) and is masked.
+// The first row of 16 tokens in the cache's arrays.  Tokens whose page does
+// not exist read page 0 (there is one: a cache without pages counts no tokens)
+// and are masked.
+__device__ __forceinline__ int64_t cache_row(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t, bool& ok) {
+    const int page = pages.of(t);
+    ok = page >= 0 && page < a.c.pages;
+    return (((int64_t)(ok ? page : 0) * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
+}
+
+template <int D>
+__device__ __forceinline__ void keys_at(const Cache4AttentionArgs& a, int64_t row, int lane, uint32_t (&k)[D / 32], uint32_t& ks) {
+    const uint32_t g = lane >> 4, n = lane & 15;
+    const uint8_t* kp = a.c.k + row * (D / 2);
+    const uint32_t ko = n * (D / 2) + g * (D / 8);
+    if constexpr (D == 128) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(kp + ko);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = w[j];
+    } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(kp + ko);
+        k[0] = w[0]; k[1] = w[1];
+    }
+    ks = (a.c.k_scale + row * (D / 32))[n * (D / 32) + g * (D / 32) / 4];
+}
+
+template <int D>
+__device__ __forceinline__ void values_at(const Cache4AttentionArgs& a, int64_t row, int lane, uint32_t (&v)[4], uint32_t (&vs)[D / 32]) {
+    const uint32_t g = lane >> 4, n = lane & 15;
+    const uint8_t *vp = a.c.v + row * (D / 2), *sp = a.c.v_scale + row * (D / 32);
+    const uint32_t vo = 4 * g * (D / 2) + (D == 128 ? 4 * n : 4 * (n >> 1)), vso = 4 * g * (D / 32);
+    if constexpr (D == 128) {
+        const u32x4 z = *reinterpret_cast<const u32x4*>(sp + vso);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vs[j] = z[j];
+    } else {
+        const u32x2 z = *reinterpret_cast<const u32x2*>(sp + vso);
+        vs[0] = z[0]; vs[1] = z[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(vp + vo + i * (D / 2));
+}
+
 template <int D>
 __device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Tile<D>& x) {
-    const uint32_t g = lane >> 4, n = lane & 15;
-    const uint32_t ko = n * (D / 2) + g * (D / 8), kso = n * (D / 32) + g * (D / 32) / 4;
-    const uint32_t vo = 4 * g * (D / 2) + (D == 128 ? 4 * n : 4 * (n >> 1)), vso = 4 * g * (D / 32);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int t = t0 + 16 * u;
-        const int page = pages.of(t);
-        x.ok[u] = page >= 0 && page < a.c.pages;
-        const int64_t row = (((int64_t)(x.ok[u] ? page : 0) * a.c.heads + kvh) << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1));
-        const uint8_t *kp = a.c.k + row * (D / 2), *vp = a.c.v + row * (D / 2), *sp = a.c.v_scale + row * (D / 32);
-        if constexpr (D == 128) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(kp + ko), z = *reinterpret_cast<const u32x4*>(sp + vso);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) { x.k[u][j] = w[j]; x.vs[u][j] = z[j]; }
-        } else {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(kp + ko), z = *reinterpret_cast<const u32x2*>(sp + vso);
-            x.k[u][0] = w[0]; x.k[u][1] = w[1];
-            x.vs[u][0] = z[0]; x.vs[u][1] = z[1];
-        }
-        x.ks[u] = (a.c.k_scale + row * (D / 32))[kso];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x.v[u][v] = *reinterpret_cast<const uint32_t*>(vp + vo + v * (D / 2));
+        const int64_t row = cache_row(a, pages, kvh, t0 + 16 * u, x.ok[u]);
+        keys_at<D>(a, row, lane, x.k[u], x.ks[u]);
+        values_at<D>(a, row, lane, x.v[u], x.vs[u]);
     }
+}
+
+// The keys of 16 tokens, as a tile's first half.
+template <int D>
+__device__ __forceinline__ void load_keys(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Tile<D>& x) {
+    bool ok;
+    keys_at<D>(a, cache_row(a, pages, kvh, t0, ok), lane, x.k[0], x.ks[0]);
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Tile<D>& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) values_at<D>(a, cache_row(a, pages, kvh, t0 + 16 * u, x.ok[u]), lane, x.v[u], x.vs[u]);
 }
 
 // Keeps the compiler from moving what both kinds of tiles compute alike ahead
@@ -338,6 +381,9 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
         }
 }
 
+// Bytes of two tiles of 64 tokens as operands.
+__host__ __device__ constexpr int shared_tiles(int d) { return 2 * 64 * d * 2 * 2; }
+
 // Waves per SIMD that registers are kept for: what fits without spilling.
 template <typename E, int D, int R> constexpr int waves_of() {
     if (sizeof(E) == 2) return R == 1 ? 3 : 2;
@@ -353,7 +399,9 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     constexpr int ROWS = 16 * R;        // rows of a wave
     constexpr int LD = D + 4;
     __shared__ float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
-    extern __shared__ int32_t before[];
+    // many rows: the converted tiles, two of 64 tokens in turn; then the prefix sums
+    extern __shared__ __align__(16) char dynamic[];
+    int32_t* before = reinterpret_cast<int32_t*>(dynamic + (SPLITW ? 0 : shared_tiles(D)));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, n = lane & 15;
 
     // key/value heads alternate fastest, so workgroups that share keys and
@@ -444,14 +492,72 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     }
     Pages pages(a, b.s, lo);
 
+    // The running maxima, of N scores of a lane for each row tile.
+    auto raise = [&](const auto& y) {
+        constexpr int N = sizeof(y[0]) / sizeof(float);
+        float top[R];
+        bool more = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            top[r] = y[r][0];
+#pragma unroll
+            for (int e = 1; e < N; ++e) top[r] = larger(top[r], y[r][e]);
+            top[r] = over_g(top[r]) * to_log2;
+            more = more || top[r] > m[r] + kSlack;
+        }
+        if (__any(more)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float mn = fmaxf(m[r], top[r]);
+                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
+                sum[r] *= f;
+#pragma unroll
+                for (int j = 0; j < VJ; ++j) o[r][j] *= f;
+                m[r] = mn;
+            }
+        }
+    };
+    // 8 scores into probabilities of row tile r, whose sum is kept.
+    auto weigh = [&](int r, const float* y, bf16x8 (&p)[PARTS]) {
+        const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float z = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
+            sum[r] += z;
+            if constexpr (PARTS == 1) {
+                p[0][e] = (__bf16)z;
+            } else {
+                __bf16 s[PARTS];
+                parts_of<PARTS>(z, s);
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) p[i][e] = s[i];
+            }
+        }
+    };
+    // The probabilities of the rows whose last token of a tile is stop - 1, or
+    // of all rows.
+    auto only = [&](bf16x8 (&to)[R][PARTS], const bf16x8 (&p)[R][PARTS], int t0, int stop, bool all) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t use = all || min(min(end[r], hi), t0 + 32) == stop ? ~0u : 0u;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
+                z &= use;
+                to[r][i] = __builtin_bit_cast(bf16x8, z);
+            }
+        }
+    };
+
+    if constexpr (SPLITW) {
     // 32 tokens; ALL: every row sees all of them
     auto run = [&](auto all, Tile<D> x, int t0) {
         constexpr bool ALL = decltype(all)::value;
         if constexpr (!ALL) opaque(x);
         bf16x8 p[R][PARTS];
+        float y[R][8];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float y[8];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -463,38 +569,17 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
                 }
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    y[4 * u + v] = acc[v];
+                    y[r][4 * u + v] = acc[v];
                     if constexpr (!ALL) {
                         const int t = t0 + 16 * u + 4 * g + v;
-                        if (!x.ok[u] || t >= end[r] || t >= hi) y[4 * u + v] = -INFINITY;
+                        if (!x.ok[u] || t >= end[r] || t >= hi) y[r][4 * u + v] = -INFINITY;
                     }
                 }
             }
-            float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-            top = over_g(top) * to_log2;
-            if (__any(top > m[r] + kSlack)) {
-                const float mn = fmaxf(m[r], top);
-                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
-                sum[r] *= f;
-#pragma unroll
-                for (int j = 0; j < VJ; ++j) o[r][j] *= f;
-                m[r] = mn;
-            }
-            const float base = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
-                sum[r] += y[e];
-                if constexpr (PARTS == 1) {
-                    p[r][0][e] = (__bf16)y[e];
-                } else {
-                    __bf16 s[PARTS];
-                    parts_of<PARTS>(y[e], s);
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) p[r][i][e] = s[i];
-                }
-            }
         }
+        raise(y);
+#pragma unroll
+        for (int r = 0; r < R; ++r) weigh(r, y[r], p[r]);
 
         uint32_t w[8];
         float s[8];
@@ -524,32 +609,23 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             values_of<D, false>(x, t0, hi, lane, w, s);
             bool odd = false;       // a value that is no number, which some rows do not see
 #pragma unroll
-            for (int e = 0; e < 8; ++e) odd = odd || (__float_as_uint(s[e]) >> 23) >= 253u;
+            for (int e = 0; e < 8; ++e) odd = odd || is_odd(s[e]);
             const bool apart = __any(odd);
             // Where apart, one end at a time, with the tokens behind it
             // cleared: 0 times NaN would reach rows that do not see it.
             for (int stop = apart ? t0 + 1 : hi;; ++stop) {
                 if (apart) values_of<D, false>(x, t0, min(stop, hi), lane, w, s);
                 bf16x8 pe[R][PARTS];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const uint32_t use = !apart || min(min(end[r], hi), t0 + 32) == stop ? ~0u : 0u;
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
-                        z &= use;
-                        pe[r][i] = __builtin_bit_cast(bf16x8, z);
-                    }
-                }
+                only(pe, p, t0, stop, !apart);
                 accumulate(pe);
                 if (!apart || stop == t0 + 32) break;
             }
         }
     };
     // the next tile is on its way while one is worked on
-    constexpr int STEP = SPLITW ? 32 * kWaves : 32;
+    constexpr int STEP = 32 * kWaves;
     const int plain = min(all_see, hi) - 32;       // last tile that every row sees
-    int t0 = lo + (SPLITW ? 32 * wave : 0);
+    int t0 = lo + 32 * wave;
     if (t0 < hi) {
         Tile<D> next;
         load_tile<D>(a, pages, kvh, t0, lane, next);
@@ -566,6 +642,167 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             if (t0 < hi) load_tile<D>(a, pages, kvh, t0, lane, next);
             run(std::false_type{}, x, t0 - STEP);
         } while (t0 < hi);
+    }
+    } else {
+    // 64 tokens at a time for all waves, as operands in LDS: [k | v] operands of
+    // 64 lanes x 16 bytes.  Wave w converts the keys of its 16 tokens and half
+    // of the channels of the values of 32, while the last 64 tokens' are used.
+    constexpr int KB = 4 * KS, OPS = KB + 2 * VJ;
+    __shared__ int odd[2][2];       // whether values of 32 tokens were left out (see below)
+    bf16x8* ops = reinterpret_cast<bf16x8*>(dynamic);
+    const int half = wave >> 1;
+    const int hi_all = min(end_of(a, b, min(b.begin + l.rows, n_rows) - 1), lim), see_all = end_of(a, b, b.begin);
+    Tile<D> x;                      // the values of 32 tokens; the keys of 16 in its first half
+    int ok = 0, ok_next = 0;        // which 16 tokens have a page
+    auto fetch = [&](int T0) {
+        ok_next = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int page = pages.of(T0 + 16 * u);
+            ok_next |= (page >= 0 && page < a.c.pages && T0 + 16 * u < hi_all) << u;
+        }
+        load_keys<D>(a, pages, kvh, T0 + 16 * wave, lane, x);
+        load_values<D>(a, pages, kvh, T0 + 32 * half, lane, x);
+    };
+    auto convert = [&](int T0, int buf) {
+        bf16x8* to = ops + buf * OPS * 64 + lane;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) to[(wave * KS + j) * 64] = eight_of(x.k[0][j], scale_bits(x.ks[0]));
+        uint32_t w[8];
+        float s[8];
+        values_of<D, false>(x, T0 + 32 * half, hi_all, lane, w, s);
+        // Values that are no numbers, of tokens that some rows do not see, are
+        // left out, as 0 times NaN would reach those rows; the others get them
+        // one end at a time.
+        const bool partly = T0 + 64 > see_all;
+        bool some = false;
+        if (partly) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool no = is_odd(s[e]);
+                some = some || no;
+                if (no) { w[e] = 0; s[e] = 1.f; }
+            }
+        }
+        if ((wave & 1) == 0) {
+            const bool any = __any(some);
+            if (lane == 0) odd[buf][half] = any;
+        }
+        auto pair = [&](auto I) {
+            two_channels<decltype(I)::value>(w, s, to[(KB + half * VJ + 2 * decltype(I)::value) * 64], to[(KB + half * VJ + 2 * decltype(I)::value + 1) * 64]);
+        };
+        if constexpr (VJ == 8) {
+            if ((wave & 1) == 0) { pair(std::integral_constant<int, 0>{}); pair(std::integral_constant<int, 1>{}); }
+            else { pair(std::integral_constant<int, 2>{}); pair(std::integral_constant<int, 3>{}); }
+        } else {
+            if ((wave & 1) == 0) pair(std::integral_constant<int, 0>{});
+            else pair(std::integral_constant<int, 1>{});
+        }
+    };
+    // What the values that were left out of 32 tokens add.
+    auto add_odd = [&](const bf16x8 (&p)[R][PARTS], int t0) {
+        Tile<D> z;
+        load_values<D>(a, pages, kvh, t0, lane, z);
+#pragma unroll 1
+        for (int stop = t0 + 1; stop <= t0 + 32; ++stop) {
+            uint32_t w[8];
+            float s[8];
+            bf16x8 pe[R][PARTS];
+            values_of<D, false>(z, t0, min(stop, hi_all), lane, w, s);
+            only(pe, p, t0, stop, false);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!is_odd(s[e])) { w[e] = 0; s[e] = 1.f; }
+            auto pair = [&](auto I) {
+                bf16x8 c[2];
+                two_channels<decltype(I)::value>(w, s, c[0], c[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i)
+                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pe[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+            };
+            pair(std::integral_constant<int, 0>{});
+            pair(std::integral_constant<int, 1>{});
+            if constexpr (VJ == 8) {
+                pair(std::integral_constant<int, 2>{});
+                pair(std::integral_constant<int, 3>{});
+            }
+        }
+    };
+    // 64 tokens, of which every row sees all or not
+    auto use = [&](bool all, int T0, int buf) {
+        const bf16x8* from = ops + buf * OPS * 64 + lane;
+        float y[R][16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            f32x4 acc[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                const bf16x8 k = from[(u * KS + j) * 64];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc[r], 0, 0, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y[r][4 * u + v] = acc[r][v];
+        }
+        if (!all) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool page = ok >> u & 1;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int t = T0 + 16 * u + 4 * g + v;
+                    const bool in = page && t < hi;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
+                }
+            }
+        }
+        raise(y);
+        bf16x8 p[2][R][PARTS];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) weigh(r, y[r] + 8 * hh, p[hh][r]);
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) {
+                const bf16x8 v = from[(KB + hh * VJ + j) * 64];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) o[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[hh][r][i], o[r][j], 0, 0, 0);
+            }
+        }
+        if (!all) {
+            if (__builtin_amdgcn_readfirstlane(odd[buf][0])) add_odd(p[0], T0);
+            if (__builtin_amdgcn_readfirstlane(odd[buf][1])) add_odd(p[1], T0 + 32);
+        }
+    };
+    const int plain = min(all_see, hi) - 64;       // last tile that every row of the wave sees
+    if (lo < hi_all) {
+        fetch(lo);
+        convert(lo, 0);
+        ok = ok_next;
+        __syncthreads();
+        int buf = 0;
+        for (int T0 = lo; T0 < hi_all; T0 += 64, buf ^= 1) {
+            if (T0 + 64 < hi_all) fetch(T0 + 64);
+            if (T0 < hi) use(T0 <= plain && ok == 15, T0, buf);
+            if (T0 + 64 < hi_all) convert(T0 + 64, buf ^ 1);
+            ok = ok_next;
+            __syncthreads();
+        }
+    }
     }
 
 #pragma unroll
@@ -761,7 +998,7 @@ size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
 template <typename E, int D, int R, bool SPLITW>
 hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, const Parts& parts, hipStream_t s) {
     const int64_t blocks = (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
-    const unsigned lds = p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * sizeof(int32_t) : 0;
+    const unsigned lds = (SPLITW ? 0u : (unsigned)shared_tiles(D)) + (p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * (unsigned)sizeof(int32_t) : 0u);
     hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), lds, s, a, p.l,
                        parts);
     return hipGetLastError();
