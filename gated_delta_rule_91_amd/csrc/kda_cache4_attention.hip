@@ -735,20 +735,28 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     // 64 tokens, of which every row sees all or not
     auto use = [&](bool all, int T0, int buf) {
         const bf16x8* from = ops + buf * OPS * 64 + lane;
+        // operands are read a group ahead of their products: left alone the
+        // compiler reads each right before its product and waits
         float y[R][16];
+        bf16x8 k[2][KS];
+#pragma unroll
+        for (int j = 0; j < KS; ++j) k[0][j] = from[j * 64];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            if (u < 3) {
+#pragma unroll
+                for (int j = 0; j < KS; ++j) k[(u + 1) & 1][j] = from[((u + 1) * KS + j) * 64];
+            }
+            __builtin_amdgcn_sched_barrier(0);
             f32x4 acc[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                const bf16x8 k = from[(u * KS + j) * 64];
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc[r], 0, 0, 0);
-            }
+                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u & 1][j], q[r][j][i], acc[r], 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -769,18 +777,32 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             }
         }
         raise(y);
-        bf16x8 p[2][R][PARTS];
+        bf16x8 p[2][R][PARTS], v[2][4];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
+        for (int j = 0; j < 4; ++j) v[0][j] = from[(KB + j) * 64];
 #pragma unroll
-            for (int r = 0; r < R; ++r) weigh(r, y[r] + 8 * hh, p[hh][r]);
+        for (int r = 0; r < R; ++r) weigh(r, y[r], p[0][r]);
 #pragma unroll
-            for (int j = 0; j < VJ; ++j) {
-                const bf16x8 v = from[(KB + hh * VJ + j) * 64];
+        for (int c = 0; c < 2 * VJ / 4; ++c) {         // four operands at a time
+            if (c + 1 < 2 * VJ / 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[(c + 1) & 1][j] = from[(KB + 4 * (c + 1) + j) * 64];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const int hh = c / (VJ / 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) o[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[hh][r][i], o[r][j], 0, 0, 0);
+                    for (int i = 0; i < PARTS; ++i) {
+                        f32x4& to = o[r][4 * c % VJ + j];
+                        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c & 1][j], p[hh][r][i], to, 0, 0, 0);
+                    }
+            // the second half's exponentials go beside the first half's products
+            if (c == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) weigh(r, y[r] + 8, p[1][r]);
             }
         }
         if (!all) {
