@@ -50,9 +50,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;         // tokens that are dealt out at once
-// Units that a block counts for beside its own: beginning one costs about as
-// much as this many.
-constexpr int kBlockCost = 3;
+// Units that a block counts for beside its own, as beginning one costs: 256
+// ragged contexts take 98 us with 2, 93 with 3, 91 with 5, 102 with 8, and 120
+// with none; prompts 197, 207, 201 and 213.
+constexpr int kBlockCost = 4;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
 
 // How the work is laid out (host and kernels).
@@ -68,10 +69,10 @@ struct Layout {
 // key/value head h is at (i * heads + h) * rows + r.  The second kernel finds
 // by cut[w] the block that begins in w and goes on.
 struct Cut {
-    int s;           // its sequence, -1: there is none
-    int begin;       // its first (query, head) row
+    int row0;        // first row of q of its sequence
+    int n_rows;      // (query, head) rows of its sequence, 0: there is no such block
+    int begin;       // its first one of them
     int last;        // last workgroup that has a part of it
-    int pad;
 };
 struct Parts {
     Cut* cut;        // [groups]
@@ -149,9 +150,9 @@ __device__ __forceinline__ int end_of(const Cache4AttentionArgs& a, const Block&
 }
 
 // Index of (row of q, head) of row r.
-__device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, const Block& b, int kvh, int r) {
+__device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, int row0, int kvh, int r) {
     const int i = (int)((uint32_t)r / (uint32_t)a.group);
-    return (b.row0 + i) * a.heads + kvh * a.group + (r - i * a.group);
+    return (row0 + i) * a.heads + kvh * a.group + (r - i * a.group);
 }
 
 // before[i]: units that the row blocks before i count for, i <= slots; returns
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     if (l.groups > 0) {
         const int all = deal_out(a, l, before);
         each = max((all + l.groups - 1) / l.groups, 1);
-        if (kvh == 0 && threadIdx.x == 0) parts.cut[group].s = -1;
+        if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{0, 0, 0, group};
         at = (int)min((int64_t)group * each, (int64_t)all);
         stop = min(at + each, all);
         int lo = 0, hi = l.slots;  // the last block that begins at or before `at`: empty ones lie before it
@@ -427,6 +428,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 
     for (; at < stop; ++slot) {
     const Block b = block_of(a, l, slot);
+    const int n_rows = b.n_rows;
     int lo = 0, lim = b.total, part = -1;
     if (l.groups > 0) {
         // the block's own units are [p0, p1)
@@ -440,14 +442,13 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             part = 2 * group;
         } else if (to < p1) {
             part = 2 * group + 1;
-            if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.s, b.begin, (p1 - 1) / each, 0};
+            if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.row0, n_rows, b.begin, (p1 - 1) / each};
         }
     } else {
         at = stop;
         if (!b.any) continue;
     }
     const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
-    const int n_rows = b.n_rows;
     const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
     const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
     const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
@@ -465,7 +466,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     for (int r = 0; r < R; ++r) {
         const int row = row0 + 16 * r + n;
         end[r] = end_of(a, b, row);
-        const E* p = reinterpret_cast<const E*>(a.q) + (int64_t)place_of(a, b, kvh, row < n_rows ? row : 0) * D + PER * g;
+        const E* p = reinterpret_cast<const E*>(a.q) + (int64_t)place_of(a, b.row0, kvh, row < n_rows ? row : 0) * D + PER * g;
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -843,7 +844,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             if (c0 == 0) { parts.sums[2 * i] = mx; parts.sums[2 * i + 1] = sm; }
             return;
         }
-        const int64_t at = place_of(a, b, kvh, row);
+        const int64_t at = place_of(a, b.row0, kvh, row);
         const float f = sm == 0.f ? 0.f : 1.f / sm;
         float z[8];
 #pragma unroll
@@ -915,65 +916,76 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 template <typename E, int D, int WAVES>
 __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts, int chunks) {
     constexpr int PER = D / 64;
-    __shared__ float acc[kWaves][D];
+    __shared__ __align__(16) float acc[kWaves][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % WAVES;
     // chunks of rows, key/value heads, workgroups of the first kernel
     const int chunk = (int)(blockIdx.x % chunks), kvh = (int)(blockIdx.x / chunks % a.c.heads), w0 = (int)(blockIdx.x / chunks / a.c.heads);
     const Cut cut = parts.cut[w0];
-    if (cut.s < 0) return;
-    Block b;
-    sequence_of(a, cut.s, b);
-    const int count = cut.last - w0 + 1, rows = min(l.rows, b.n_rows - cut.begin);
+    // bounded, so that a workspace that another call writes meanwhile gives
+    // wrong values but no access outside the arrays
+    const int count = min(cut.last, l.groups - 1) - w0 + 1, rows = min(l.rows, cut.n_rows - cut.begin);
+    if (cut.n_rows <= 0 || cut.begin < 0 || count < 2) return;
     for (int r = chunk * (kWaves / WAVES) + wave / WAVES; r < rows; r += chunks * (kWaves / WAVES)) {
     const int64_t stride = 2 * (int64_t)a.c.heads * l.rows;
     const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r, rest = first - stride / 2;
-    const int64_t at = place_of(a, b, kvh, cut.begin + r);
+    const int64_t at = place_of(a, cut.row0, kvh, cut.begin + r);
+    if (at < 0 || at >= a.tokens * a.heads) return;
     auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
+    auto sums = [&](int i) { return i < count ? *reinterpret_cast<const f32x2*>(parts.sums + 2 * place(i)) : f32x2{-INFINITY, 0.f}; };
+    typedef typename std::conditional<PER == 2, f32x2, float>::type OV;
+    auto part = [&](int i) { return *reinterpret_cast<const OV*>(parts.o + place(i) * D + lane * PER); };
 
-    float mx = -INFINITY;
-    for (int i = lane; i < count; i += 64) mx = fmaxf(mx, parts.sums[2 * place(i)]);
+    // the first parts are on their way while their weights are found
+    constexpr int AHEAD = 8;
+    f32x2 ms = sums(lane);
+    OV x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) x[k] = part(min(turn + k * WAVES, count - 1));
+    E gate[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) gate[e] = a.g ? reinterpret_cast<const E*>(a.g)[at * D + lane * PER + e] : (E)0.f;
+    float mx = ms[0];
+    for (int i = lane + 64; i < count; i += 64) mx = fmaxf(mx, sums(i)[0]);
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-    float sum = 0.f, o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    float sum = 0.f;
+    OV o = OV(0.f);
     for (int i0 = 0; i0 < count; i0 += 64) {
-        float w = 0.f;
-        if (i0 + lane < count) {
-            const float mi = parts.sums[2 * place(i0 + lane)];
-            w = mi == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mi - mx);
-            sum += w * parts.sums[2 * place(i0 + lane) + 1];
-        }
+        if (i0 > 0) ms = sums(i0 + lane);
+        const float w = ms[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[0] - mx);
+        sum += w * ms[1];
+        auto weight = [&](int k) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k)); };
         const int most = min(count - i0, 64);
-#pragma unroll 8
-        for (int k = turn; k < most; k += WAVES) {
-            const float wk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k));
-            const float* p = parts.o + place(i0 + k) * D + lane * PER;
+        int k = turn;
+        if (i0 == 0) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) o[e] += wk * p[e];
+            for (int q = 0; q < AHEAD; ++q)
+                if (turn + q * WAVES < most) o += weight(turn + q * WAVES) * x[q];
+            k += AHEAD * WAVES;
         }
+#pragma unroll 8
+        for (; k < most; k += WAVES) o += weight(k) * part(i0 + k);
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
     if constexpr (WAVES > 1) {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[wave][lane * PER + e] = o[e];
+        *reinterpret_cast<OV*>(&acc[wave][lane * PER]) = o;
         __syncthreads();
         if (turn == 0) {
 #pragma unroll
-            for (int k = 1; k < WAVES; ++k)
-#pragma unroll
-                for (int e = 0; e < PER; ++e) o[e] += acc[wave + k][lane * PER + e];
+            for (int k = 1; k < WAVES; ++k) o += *reinterpret_cast<const OV*>(&acc[wave + k][lane * PER]);
         }
         __syncthreads();
         if (turn != 0) continue;
     }
+    float y[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        const int64_t i = at * D + lane * PER + e;
-        float y = sum == 0.f ? 0.f : o[e] / sum;
-        if (a.g) y *= sigmoidf_(to_f32(reinterpret_cast<const E*>(a.g)[i]));
-        reinterpret_cast<E*>(a.out)[i] = from_f32<E>(y);
+        if constexpr (PER == 2) y[e] = o[e];
+        else y[e] = o;
+        y[e] = sum == 0.f ? 0.f : y[e] / sum;
+        if (a.g) y[e] *= sigmoidf_(to_f32(gate[e]));
+        reinterpret_cast<E*>(a.out)[at * D + lane * PER + e] = from_f32<E>(y[e]);
     }
     }
 }
