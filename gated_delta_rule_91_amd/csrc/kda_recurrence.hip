@@ -101,7 +101,12 @@ struct Decay {
     __device__ __forceinline__ float step(float h, float x) const { return fmaf(c, h, x) + (slow ? h : 0.f); }
 };
 
-__device__ __forceinline__ float product_of(float sum) { return __builtin_amdgcn_exp2f(1.4426950408889634f * sum); }
+// e^sum; next to 1 rounded from 1 + expm1, since the hardware exp2 falls short
+// of it there, which a long chain of stretches adds up.
+__device__ __forceinline__ float product_of(float sum) {
+    const Decay d(sum);
+    return d.slow ? 1.f + d.c : d.c;
+}
 
 // The sequence of a token, walked along the tokens of one wave (all of it the
 // same in every lane).
