@@ -269,7 +269,7 @@ struct Pages {
     }
     __device__ __forceinline__ int of(int t) {
         const int i = t >> shift;
-        if (i - base > 63) fill(i);
+        if ((uint32_t)(i - base) > 63u) fill(i);
         return __builtin_amdgcn_readlane(mine, i - base);
     }
 };
@@ -535,19 +535,16 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             }
         }
     };
-    // The probabilities of the rows whose last token of a tile is stop - 1, or
-    // of all rows.
-    auto only = [&](bf16x8 (&to)[R][PARTS], const bf16x8 (&p)[R][PARTS], int t0, int stop, bool all) {
+    // Whether stop - 1 is the last token that this lane's row of row tile r sees
+    // of the 32 from t0 on.
+    auto ends_at = [&](int r, int t0, int stop) { return min(min(end[r], hi), t0 + 32) == stop; };
+    // to + values x probabilities, where the row counts.
+    auto product = [&](f32x4& to, bf16x8 value, const bf16x8 (&p)[PARTS], bool counts) {
+        f32x4 sum = to;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const uint32_t use = all || min(min(end[r], hi), t0 + 32) == stop ? ~0u : 0u;
+        for (int i = 0; i < PARTS; ++i) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value, p[i], sum, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                u32x4 z = __builtin_bit_cast(u32x4, p[r][i]);
-                z &= use;
-                to[r][i] = __builtin_bit_cast(bf16x8, z);
-            }
-        }
+        for (int v = 0; v < 4; ++v) to[v] = counts ? sum[v] : to[v];
     };
 
     if constexpr (SPLITW) {
@@ -584,17 +581,14 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 
         uint32_t w[8];
         float s[8];
-        auto accumulate = [&](const bf16x8 (&pp)[R][PARTS]) {
+        auto accumulate = [&](auto counts) {
             auto pair = [&](auto I) {
                 bf16x8 c[2];
                 two_channels<decltype(I)::value>(w, s, c[0], c[1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int i = 0; i < PARTS; ++i)
-                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pp[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+                    for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], counts(r));
             };
             pair(std::integral_constant<int, 0>{});
             pair(std::integral_constant<int, 1>{});
@@ -605,21 +599,19 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
         };
         if constexpr (ALL) {
             values_of<D, true>(x, t0, hi, lane, w, s);
-            accumulate(p);
+            accumulate([](int) { return true; });
         } else {
             values_of<D, false>(x, t0, hi, lane, w, s);
             bool odd = false;       // a value that is no number, which some rows do not see
 #pragma unroll
             for (int e = 0; e < 8; ++e) odd = odd || is_odd(s[e]);
             const bool apart = __any(odd);
-            // Where apart, one end at a time, with the tokens behind it
-            // cleared: 0 times NaN would reach rows that do not see it.
-            for (int stop = apart ? t0 + 1 : hi;; ++stop) {
+            // Where apart, the rows of one end at a time, with the tokens behind
+            // it cleared: 0 times NaN would reach rows that do not see it.
+            for (int stop = apart ? t0 + 1 : t0 + 32;; ++stop) {
                 if (apart) values_of<D, false>(x, t0, min(stop, hi), lane, w, s);
-                bf16x8 pe[R][PARTS];
-                only(pe, p, t0, stop, !apart);
-                accumulate(pe);
-                if (!apart || stop == t0 + 32) break;
+                accumulate([&](int r) { return !apart || ends_at(r, t0, stop); });
+                if (stop == t0 + 32) break;
             }
         }
     };
@@ -700,7 +692,8 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             else pair(std::integral_constant<int, 1>{});
         }
     };
-    // What the values that were left out of 32 tokens add.
+    // What the values that were left out of 32 tokens add, to the rows of one
+    // end at a time.
     auto add_odd = [&](const bf16x8 (&p)[R][PARTS], int t0) {
         Tile<D> z;
         load_values<D>(a, pages, kvh, t0, lane, z);
@@ -708,9 +701,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
         for (int stop = t0 + 1; stop <= t0 + 32; ++stop) {
             uint32_t w[8];
             float s[8];
-            bf16x8 pe[R][PARTS];
             values_of<D, false>(z, t0, min(stop, hi_all), lane, w, s);
-            only(pe, p, t0, stop, false);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (!is_odd(s[e])) { w[e] = 0; s[e] = 1.f; }
@@ -720,10 +711,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int i = 0; i < PARTS; ++i)
-                            o[r][2 * decltype(I)::value + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c[h], pe[r][i], o[r][2 * decltype(I)::value + h], 0, 0, 0);
+                    for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], ends_at(r, t0, stop));
             };
             pair(std::integral_constant<int, 0>{});
             pair(std::integral_constant<int, 1>{});
@@ -806,7 +794,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
                 for (int r = 0; r < R; ++r) weigh(r, y[r] + 8, p[1][r]);
             }
         }
-        if (!all) {
+        if (T0 + 64 > see_all) {
             if (__builtin_amdgcn_readfirstlane(odd[buf][0])) add_odd(p[0], T0);
             if (__builtin_amdgcn_readfirstlane(odd[buf][1])) add_odd(p[1], T0 + 32);
         }

@@ -16,9 +16,9 @@ from typing import Optional
 from . import KdaError, _cu, _expect, _expect_workspace, _io_code, _stream, _torch, lib
 
 __all__ = ["HYBRID_EXPORTS", "Cache4", "plan_requests", "cache4_append", "cache4_read", "cache4_attention",
-           "cache4_attention_workspace_size", "recurrence_workspace_size", "recurrence_backward_workspace_size",
-           "recurrence_prefill", "recurrence_prefill_for_backward", "recurrence_backward", "recurrence_autograd",
-           "recurrence_step"]
+           "cache4_attention_workspace_size", "recurrence_problem", "recurrence_workspace_size",
+           "recurrence_backward_workspace_size", "recurrence_prefill", "recurrence_prefill_for_backward",
+           "recurrence_backward", "recurrence_autograd", "recurrence_step"]
 
 HYBRID_EXPORTS = ("kda_plan_requests", "kda_cache4_append", "kda_cache4_read", "kda_cache4_attention_workspace_size",
                   "kda_cache4_attention", "kda_recurrence_workspace_size", "kda_recurrence_backward_workspace_size",
@@ -225,7 +225,8 @@ def _attention_problem(q, cache, block_table, total_lens, cu_seqlens, scale, max
     T, heads, _ = q.shape
     n_seq, max_pages = T if cu_seqlens is None else _cu(cu_seqlens, dev), block_table.shape[1]
     io = _io_code(q.dtype)
-    ptrs = (_in("q", q, (T, heads, cache.d), q.dtype, dev), _in("block_table", block_table, (n_seq, max_pages), i32, dev),
+    ptrs = (_in("q", q, (T, heads, cache.d), q.dtype, dev),
+            _in("block_table", block_table, (n_seq, max_pages), i32, dev),
             _in("total_lens", total_lens, (n_seq,), i32, dev), _in("cu_seqlens", cu_seqlens, (n_seq + 1,), i32, dev))
     if heads % cache.heads:
         raise ValueError(f"{heads} query heads over {cache.heads} key/value heads")
@@ -289,11 +290,19 @@ def _recurrence_problem(x, log_alpha, log_alpha_min, g, state_in, cu_seqlens):
     return KdaRecurrenceProblem(B, T, D, n_seq, io, float(log_alpha_min)), states, ptrs
 
 
+def recurrence_problem(batch: int, seqlen: int, width: int, io_dtype, log_alpha_min: float,
+                       n_seq: int = -1) -> KdaRecurrenceProblem:
+    """The problem that the workspace sizes go by; n_seq: sequences of a packed batch."""
+    return KdaRecurrenceProblem(batch, seqlen, width, n_seq, _io_code(io_dtype), float(log_alpha_min))
+
+
 def recurrence_workspace_size(p: KdaRecurrenceProblem) -> int:
+    """Bytes of workspace that recurrence_prefill needs."""
     return _hlib().kda_recurrence_workspace_size(p)
 
 
 def recurrence_backward_workspace_size(p: KdaRecurrenceProblem) -> int:
+    """Bytes of workspace that the training pair needs."""
     return _hlib().kda_recurrence_backward_workspace_size(p)
 
 
@@ -374,6 +383,7 @@ def _recurrence_function():
                 return out, state
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, d_out, d_state):
                 x, log_alpha, g, state_in, cu_seqlens = ctx.saved_tensors
                 r = recurrence_backward(x, log_alpha, ctx.log_alpha_min, ctx.workspace, g=g, state_in=state_in,

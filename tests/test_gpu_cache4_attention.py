@@ -60,13 +60,15 @@ def i32(v):
 
 def check(c, q, g, table, total, cu, io, scale=None, decode=False, **kw):
     scale = 1 / math.sqrt(c.d) if scale is None else scale
-    out = torch.full_like(q, 77.0)
+    room = torch.full((q.shape[0] + 4, *q.shape[1:]), 77.0, dtype=q.dtype, device="cuda")
+    out = room[2:-2]                                      # nothing is written around it
     got = kda.cache4_attention(q, c, i32(table).reshape(len(total), -1), i32(total), cu_seqlens=None if decode else i32(cu), g=g,
                                scale=scale, out=out, **kw)
     torch.cuda.synchronize()
     assert got is out
     host = {n: getattr(c, n).cpu() for n in ("k", "k_scale", "v", "v_scale")}
     want, mag, size = ref.attention(q.cpu(), host, table, total, cu, scale, None if g is None else g.cpu())
+    assert (room[:2] == 77.0).all() and (room[-2:] == 77.0).all()
     got = out.cpu().double()
     none = torch.isnan(want).all(-1).all(-1)              # rows of no sequence stay as they were
     assert (got[none] == 77.0).all()
@@ -156,6 +158,51 @@ def test_nan_in_the_cache_reaches_only_its_queries():
     want[0, :2, 32:] = True
     want[1, 2:] = True
     assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(64, 20), (128, 3)])
+def test_nan_that_some_queries_do_not_see(d, heads, io):
+    """Values that are NaN or Inf reach the queries behind them and no others, wherever the block table's stretches end."""
+    total, new, page = [1200], [200], 16
+    c, q, g, table, cu = build(total, new, heads, 1, d, page, io)
+    for t, scale in ((1010, 255), (1100, 255), (1153, 254)):
+        c.v_scale[table[0][t // page], 0, t % page, 0] = scale
+        c.v[table[0][t // page], 0, t % page] = 0x77      # 6 and 6: 6 times 2^127 is Inf
+    out = kda.cache4_attention(q, c, i32(table), i32(total), cu_seqlens=i32(cu), g=g, max_q=200, max_len=1200)
+    torch.cuda.synchronize()
+    bad = ~torch.isfinite(out.cpu().float())
+    want = torch.zeros_like(bad)
+    want[10:, :, :32] = True                              # query i is at position 1000 + i
+    assert torch.equal(bad, want)
+
+
+def test_given_workspace():
+    total = [900, 40]
+    c, q, g, table, cu = build(total, [1, 1], 8, 2, 128, 16, "bf16")
+    t, n = i32(table), i32(total)
+    want = kda.cache4_attention(q, c, t, n, g=g)
+    size = kda.cache4_attention_workspace_size(q, c, t, n)
+    assert size > 0
+    for fill in (0, 255, 127):                            # whatever it holds before
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            got = kda.cache4_attention(q, c, t, n, g=g, workspace=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+    with pytest.raises(kda.KdaError) as e:
+        kda.cache4_attention(q, c, t, n, g=g, workspace=ws[:-256])
+    assert e.value.code == 3
+    with pytest.raises(ValueError):
+        kda.cache4_attention(q.transpose(0, 1).contiguous().transpose(0, 1), c, t, n)      # strides
+
+
+def test_many_blocks_without_dealing_out():
+    """More row blocks than prefix sums are kept for: a workgroup each."""
+    n = 4200
+    total = [1 + (7 * i) % 40 for i in range(n)]
+    c, q, g, table, cu = build(total, [1] * n, 2, 1, 64, 16, "bf16", gate=False)
+    check(c, q, None, table, total, cu, "bf16", decode=True)
 
 
 def test_offsets_past_32_bits():

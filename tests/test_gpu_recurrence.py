@@ -56,9 +56,11 @@ def check(i, io, cu=None, backward=True):
     top = lambda x: torch.nan_to_num(x).abs().flatten(0, -2).amax(0) if x.numel() else torch.zeros(x.shape[-1], dtype=torch.float64)
     s0 = torch.zeros(1, i["x"].shape[2], dtype=torch.float64) if cpu["s0"] is None else cpu["s0"].double()
     th = k * torch.maximum(top(want["h"]), top(s0))
-    out = torch.full_like(i["x"], 55.0)
+    room = torch.full((i["x"].numel() + 64,), 55.0, dtype=i["x"].dtype, device="cuda")
+    out = room[:i["x"].numel()].view(i["x"].shape)        # nothing is written behind it
     got, state = kda.recurrence_prefill(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], cu_seqlens=cut, out=out)
     torch.cuda.synchronize()
+    assert (room[i["x"].numel():] == 55.0).all()
     left = torch.isnan(want["out"])
     assert (out.cpu()[left] == 55.0).all()                # tokens of no sequence
     within(out, want["out"], th + 8 * U * want["out"].abs() + UO[io] * want["out"].abs(), "out")
@@ -231,6 +233,61 @@ def test_gradients_against_differences():
             diff = (loss(**{k: up}) - loss(**{k: down})) / (2 * eps)
             # differences of second order: eps^2 times third derivatives, and 1e-11 of the loss's rounding over eps
             assert abs(float(leaf.grad[at]) - diff) <= 1e-4 * max(1.0, abs(diff)), (k, at)
+
+
+def test_given_workspaces():
+    """Whatever a workspace holds before; too small a one is refused."""
+    i = made(2, 700, 34, "f32")
+    p = kda.recurrence_problem(2, 700, 34, torch.float32, FLOOR)
+    sizes = kda.recurrence_workspace_size(p), kda.recurrence_backward_workspace_size(p)
+    assert sizes[1] > sizes[0] > 0
+    want, state, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"])
+    grads = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, g=i["g"], state_in=i["s0"], d_out=i["d_out"])
+    for fill in (0, 255, 128):
+        ws = [torch.full((n,), fill, dtype=torch.uint8, device="cuda") for n in sizes]
+        for _ in range(2):
+            out, s1 = kda.recurrence_prefill(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], workspace=ws[0])
+            out2, s2, _ = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], workspace=ws[1])
+            r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws[1], g=i["g"], state_in=i["s0"], d_out=i["d_out"])
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(out2, want) and torch.equal(s1, state) and torch.equal(s2, state)
+            assert all(torch.equal(r[k], grads[k]) for k in r)
+    for call in (lambda: kda.recurrence_prefill(i["x"], i["la"], FLOOR, workspace=ws[0][:-256]),
+                 lambda: kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, workspace=ws[1][:-256]),
+                 lambda: kda.recurrence_backward(i["x"], i["la"], FLOOR, ws[1][:-256], d_out=i["d_out"])):
+        with pytest.raises(kda.KdaError) as e:
+            call()
+        assert e.value.code == 3
+
+
+def test_offsets_past_32_bits():
+    """Over 2^31 elements: the last of the rows is what it is alone."""
+    B, T, D = 3, 175000, 4100
+    x = torch.zeros(B, T, D, dtype=torch.bfloat16, device="cuda")
+    la = torch.full((B, T, D), -0.01, device="cuda")
+    assert x.numel() > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x[2, -500:] = torch.randn(500, D, generator=gen, device="cuda").bfloat16()
+    la[2, -300:] = -torch.rand(300, D, generator=gen, device="cuda")
+    out, state = kda.recurrence_prefill(x, la, FLOOR)
+    torch.cuda.synchronize()
+    assert not out[0].any() and not out[1].any() and not out[2, :-500].any()
+    ref_out, ref_state = kda.recurrence_prefill(x[2:, -500:].contiguous(), la[2:, -500:].contiguous(), FLOOR)
+    torch.cuda.synchronize()
+    # both are within (3 N + 16) u of the formula, N <= 100 here, and round once more
+    top = float(ref_state.abs().max()) * 2 + 10
+    assert torch.allclose(state[2:], ref_state, rtol=0, atol=2 * (3 * 100 + 16) * U * top)
+    assert torch.allclose(out[2:, -500:].float(), ref_out.float(), rtol=2 * UO["bf16"], atol=2 * (3 * 100 + 16) * U * top)
+    del x, la, out
+    torch.cuda.empty_cache()
+
+
+def test_autograd_refuses_second_derivatives():
+    x = torch.randn(1, 20, 4, device="cuda", requires_grad=True)
+    out, _ = kda.recurrence_autograd(x, -torch.rand(1, 20, 4, device="cuda"), FLOOR)
+    grad, = torch.autograd.grad(out.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        grad.sum().backward()
 
 
 def test_autograd_of_outputs_that_are_not_used():

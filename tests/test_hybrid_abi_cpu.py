@@ -215,3 +215,12 @@ def test_binding_refusals():
                 f(a["x"], a["la"], -0.5, g=a["g"], state_in=a["s"], cu_seqlens=a["cu"])
     with pytest.raises(ValueError):
         kda.recurrence_step(s, s, z(2, 5), -0.5)
+    # strides
+    turned = z(6, 2).t()
+    for f in (lambda: kda.recurrence_step(turned, turned, turned, -0.5),
+              lambda: kda.recurrence_prefill(z(1, 1, 6).expand(2, 5, 6), x, -0.5),
+              lambda: kda.cache4_append(c, z(2, 5, 128).transpose(0, 1), k, slots),
+              lambda: kda.cache4_attention(z(8, 3, 128).transpose(0, 1), c, table, total),
+              lambda: kda.plan_requests(z(6, dtype=i32)[::2], z(3, dtype=i32), z(3, 4, dtype=i32), z(5, dtype=i32), 64, 3)):
+        with pytest.raises(ValueError, match="contiguous"):
+            f()
