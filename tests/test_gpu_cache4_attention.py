@@ -177,6 +177,21 @@ def test_nan_that_some_queries_do_not_see(d, heads, io):
     assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,d", [(2, 64), (4, 128)])
+def test_nan_that_some_of_few_queries_do_not_see(heads, d, io):
+    """The same for as few rows as waves share: 6 queries of 2 or 4 heads."""
+    total, new = [40, 37], [6, 1]
+    c, q, g, table, cu = build(total, new, heads, 1, d, 16, io)
+    c.v_scale[table[0][2], 0, 5, 1] = 255                 # token 37 of sequence 0, channels 32..63
+    out = kda.cache4_attention(q, c, i32(table), i32(total), cu_seqlens=i32(cu), g=g, max_q=6)
+    torch.cuda.synchronize()
+    bad = torch.isnan(out.cpu().float())
+    want = torch.zeros_like(bad)
+    want[3:6, :, 32:64] = True                            # query i is at position 34 + i
+    assert torch.equal(bad, want)
+
+
 def test_given_workspace():
     total = [900, 40]
     c, q, g, table, cu = build(total, [1, 1], 8, 2, 128, 16, "bf16")
