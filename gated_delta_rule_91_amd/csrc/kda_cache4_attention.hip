@@ -46,6 +46,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // sums is rare.
 constexpr float kSlack = 8.f;
 
+typedef uint32_t u32x1 __attribute__((ext_vector_type(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -316,15 +317,103 @@ __device__ __forceinline__ void values_at(const Cache4AttentionArgs& a, int64_t 
     for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint32_t*>(vp + vo + i * (D / 2));
 }
 
+// 32 tokens of one key/value head as they lie in memory: 16 bytes a lane for
+// each KB of keys and values, 4 bytes a lane for all scales.
 template <int D>
-__device__ __forceinline__ void load_tile(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Tile<D>& x) {
+struct Raw {
+    u32x4 k[D / 64], v[D / 64];
+    uint32_t scales;
+    int ok;                     // which halves' pages exist
+};
+
+template <int D>
+__device__ __forceinline__ void load_raw(const Cache4AttentionArgs& a, Pages& pages, int kvh, int t0, int lane, Raw<D>& x) {
+    int64_t row[2];
+    x.ok = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int64_t row = cache_row(a, pages, kvh, t0 + 16 * u, x.ok[u]);
-        keys_at<D>(a, row, lane, x.k[u], x.ks[u]);
-        values_at<D>(a, row, lane, x.v[u], x.vs[u]);
+        bool ok;
+        row[u] = cache_row(a, pages, kvh, t0 + 16 * u, ok);
+        x.ok |= ok << u;
     }
+    if constexpr (D == 128) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            x.k[u] = *reinterpret_cast<const u32x4*>(a.c.k + row[u] * (D / 2) + (uint32_t)(16 * lane));
+            x.v[u] = *reinterpret_cast<const u32x4*>(a.c.v + row[u] * (D / 2) + (uint32_t)(16 * lane));
+        }
+    } else {
+        const int64_t at = (lane < 32 ? row[0] : row[1]) * (D / 2) + 16 * (lane & 31);
+        x.k[0] = *reinterpret_cast<const u32x4*>(a.c.k + at);
+        x.v[0] = *reinterpret_cast<const u32x4*>(a.c.v + at);
+    }
+    // scales of the keys of both halves, then of the values: D/8 lanes each
+    constexpr int N = D / 8;
+    const uint8_t* p = lane & (2 * N) ? a.c.v_scale : a.c.k_scale;
+    const int64_t at = (lane & N ? row[1] : row[0]) * (D / 32) + 4 * (lane & (N - 1));
+    x.scales = *reinterpret_cast<const uint32_t*>(p + at);
 }
+
+// A wave's staging area in LDS: loads that follow memory take a quarter of the
+// cache lookups that loads in operand order do (each of whose lanes has a row
+// of its own), and the operands are read from here.  Token r of a half has its
+// 16-byte chunk c at chunk c ^ (r / 4 mod chunks) of row r, and operand row m
+// is token m / 4 + 4 (m mod 4): both so that the lanes of a read lie in
+// different banks.  A result row 4 g + v then is token g + 4 v.
+template <int D>
+struct Stage {
+    static constexpr int CH = D / 32, HALF = 16 * CH * 16, V = 2 * HALF, SC = 4 * HALF, SH = 16 * (D / 32);
+    static constexpr int BYTES = SC + 4 * SH;
+    char* at;
+    int lane;
+    __device__ __forceinline__ int chunk(int r, int c) const { return (r * CH + (c ^ ((r >> 2) & (CH - 1)))) * 16; }
+    __device__ __forceinline__ void put(const Raw<D>& x) const {
+        if constexpr (D == 128) {
+            const int to = chunk(lane >> 2, lane & 3);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                *reinterpret_cast<u32x4*>(at + u * HALF + to) = x.k[u];
+                *reinterpret_cast<u32x4*>(at + V + u * HALF + to) = x.v[u];
+            }
+        } else {
+            const int to = (lane >> 5) * HALF + chunk((lane >> 1) & 15, lane & 1);
+            *reinterpret_cast<u32x4*>(at + to) = x.k[0];
+            *reinterpret_cast<u32x4*>(at + V + to) = x.v[0];
+        }
+        if (lane < D / 2) *reinterpret_cast<u32x1*>(at + SC + 4 * lane) = u32x1{x.scales};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    // Before the next put: all lanes have read.
+    __device__ __forceinline__ void done() const {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    // The words and the scale of this lane's key operands, of half u.
+    __device__ __forceinline__ void key(int u, uint32_t (&k)[D / 32], float& scale) const {
+        const int g = lane >> 4, n = lane & 15, r = (n >> 2) + 4 * (n & 3);
+        if constexpr (D == 128) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(at + u * HALF + chunk(r, g));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = w[j];
+        } else {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(at + u * HALF + chunk(r, g >> 1) + 8 * (g & 1));
+            k[0] = w[0]; k[1] = w[1];
+        }
+        scale = scale_bits(*reinterpret_cast<const uint8_t*>(at + SC + u * SH + r * (D / 32) + (D == 128 ? g : g >> 1)));
+    }
+    // The word and scale of this lane's channel group for its token 4 u + v.
+    __device__ __forceinline__ void value(int u, int v, uint32_t& w, uint32_t& scale) const {
+        const int g = lane >> 4, n = lane & 15, r = g + 4 * v;
+        if constexpr (D == 128) {
+            w = (*reinterpret_cast<const u32x1*>(at + V + u * HALF + chunk(r, n >> 2) + 4 * (n & 3)))[0];
+        } else {
+            w = (*reinterpret_cast<const u32x1*>(at + V + u * HALF + chunk(r, n >> 3) + 4 * ((n >> 1) & 3)))[0];
+            w >>= 16 * (n & 1);
+        }
+        scale = *reinterpret_cast<const uint8_t*>(at + SC + 2 * SH + u * SH + r * (D / 32) + (D == 128 ? n >> 2 : n >> 3));
+    }
+};
 
 // The keys of 16 tokens, as a tile's first half.
 template <int D>
@@ -339,24 +428,9 @@ __device__ __forceinline__ void load_values(const Cache4AttentionArgs& a, Pages&
     for (int u = 0; u < 2; ++u) values_at<D>(a, cache_row(a, pages, kvh, t0 + 16 * u, x.ok[u]), lane, x.v[u], x.vs[u]);
 }
 
-// Keeps the compiler from moving what both kinds of tiles compute alike ahead
-// of the branch between them, where all of it would lie in registers at once.
+// The words and scales of this lane's channel group for its 8 tokens; those at
+// or past `end`, or without a page, are zeros, whatever memory holds there.
 template <int D>
-__device__ __forceinline__ void opaque(Tile<D>& x) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        asm volatile("" : "+v"(x.ks[u]));
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) asm volatile("" : "+v"(x.k[u][j]), "+v"(x.vs[u][j]));
-#pragma unroll
-        for (int v = 0; v < 4; ++v) asm volatile("" : "+v"(x.v[u][v]));
-    }
-}
-
-// The words and scales of this lane's channel group for its 8 tokens.  ALL:
-// all of them count; else those at or past `end`, or without a page, are
-// zeros, whatever memory holds there.
-template <int D, bool ALL>
 __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int lane, uint32_t (&w)[8], float (&s)[8]) {
     const int g = lane >> 4, n = lane & 15;
 #pragma unroll
@@ -371,14 +445,9 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
                 b = x.vs[u][v >> 1] >> (16 * (v & 1) + 8 * (n >> 3));
                 c = x.v[u][v] >> (16 * (n & 1));
             }
-            b &= 255u;
-            if constexpr (!ALL) {
-                const bool in = x.ok[u] && t0 + 16 * u + 4 * g + v < end;
-                b = in ? b : 127u;
-                c = in ? c : 0u;
-            }
-            w[4 * u + v] = c;
-            s[4 * u + v] = scale_bits(b);
+            const bool in = x.ok[u] && t0 + 16 * u + 4 * g + v < end;
+            w[4 * u + v] = in ? c : 0u;
+            s[4 * u + v] = scale_bits(in ? b & 255u : 127u);
         }
 }
 
@@ -399,7 +468,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     constexpr int PER = D / 4;          // channels of a lane's result
     constexpr int ROWS = 16 * R;        // rows of a wave
     constexpr int LD = D + 4;
-    __shared__ float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
+    __shared__ __align__(16) float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
     // many rows: the converted tiles, two of 64 tokens in turn; then the prefix sums
     extern __shared__ __align__(16) char dynamic[];
     int32_t* before = reinterpret_cast<int32_t*>(dynamic + (SPLITW ? 0 : shared_tiles(D)));
@@ -548,39 +617,65 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     };
 
     if constexpr (SPLITW) {
-    // 32 tokens; ALL: every row sees all of them
-    auto run = [&](auto all, Tile<D> x, int t0) {
+    // 32 staged tokens; ALL: every row sees all of them
+    const Stage<D> stage = {reinterpret_cast<char*>(&so[wave][0][0]), lane};
+    static_assert(Stage<D>::BYTES <= (int)sizeof(so[0]), "a wave stages where its results go later");
+    auto run = [&](auto all, int ok, int t0) {
         constexpr bool ALL = decltype(all)::value;
-        if constexpr (!ALL) opaque(x);
-        bf16x8 p[R][PARTS];
         float y[R][8];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int u = 0; u < 2; ++u) {
+            uint32_t kw[KS];
+            float ks;
+            stage.key(u, kw, ks);
+            f32x4 acc[R];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    const bf16x8 k = eight_of(x.k[u][j], scale_bits(x.ks[u]));
+            for (int j = 0; j < KS; ++j) {
+                const bf16x8 k = eight_of(kw[j], ks);
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc, 0, 0, 0);
-                }
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    y[r][4 * u + v] = acc[v];
+                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc[r], 0, 0, 0);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int t = t0 + 16 * u + g + 4 * v;
+                const bool in = ALL || ((ok >> u & 1) && t < hi);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    y[r][4 * u + v] = acc[r][v];
                     if constexpr (!ALL) {
-                        const int t = t0 + 16 * u + 4 * g + v;
-                        if (!x.ok[u] || t >= end[r] || t >= hi) y[r][4 * u + v] = -INFINITY;
+                        if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
                     }
                 }
             }
         }
         raise(y);
+        bf16x8 p[R][PARTS];
 #pragma unroll
         for (int r = 0; r < R; ++r) weigh(r, y[r], p[r]);
 
         uint32_t w[8];
         float s[8];
+        // the values of tokens before `stop`; the others are zeros, whatever memory holds there
+        auto values = [&](int stop) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint32_t c, b;
+                    stage.value(u, v, c, b);
+                    if constexpr (!ALL) {
+                        const bool in = (ok >> u & 1) && t0 + 16 * u + g + 4 * v < stop;
+                        c = in ? c : 0u;
+                        b = in ? b : 127u;
+                    }
+                    w[4 * u + v] = c;
+                    s[4 * u + v] = scale_bits(b);
+                }
+        };
         auto accumulate = [&](auto counts) {
             auto pair = [&](auto I) {
                 bf16x8 c[2];
@@ -597,11 +692,10 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
                 pair(std::integral_constant<int, 3>{});
             }
         };
+        values(hi);
         if constexpr (ALL) {
-            values_of<D, true>(x, t0, hi, lane, w, s);
             accumulate([](int) { return true; });
         } else {
-            values_of<D, false>(x, t0, hi, lane, w, s);
             bool odd = false;       // a value that is no number, which some rows do not see
 #pragma unroll
             for (int e = 0; e < 8; ++e) odd = odd || is_odd(s[e]);
@@ -609,31 +703,35 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
             // Where apart, the rows of one end at a time, with the tokens behind
             // it cleared: 0 times NaN would reach rows that do not see it.
             for (int stop = apart ? t0 + 1 : t0 + 32;; ++stop) {
-                if (apart) values_of<D, false>(x, t0, min(stop, hi), lane, w, s);
+                if (apart) values(min(stop, hi));
                 accumulate([&](int r) { return !apart || ends_at(r, t0, stop); });
                 if (stop == t0 + 32) break;
             }
         }
+        stage.done();
     };
     // the next tile is on its way while one is worked on
     constexpr int STEP = 32 * kWaves;
     const int plain = min(all_see, hi) - 32;       // last tile that every row sees
     int t0 = lo + 32 * wave;
     if (t0 < hi) {
-        Tile<D> next;
-        load_tile<D>(a, pages, kvh, t0, lane, next);
+        Raw<D> x;
+        load_raw<D>(a, pages, kvh, t0, lane, x);
+        auto turn = [&] {           // stages one tile, sends for the next
+            const int ok = x.ok;
+            stage.put(x);
+            t0 += STEP;
+            if (t0 < hi) load_raw<D>(a, pages, kvh, t0, lane, x);
+            return ok;
+        };
         do {
-            while (t0 <= plain && next.ok[0] && next.ok[1]) {
-                const Tile<D> x = next;
-                t0 += STEP;
-                if (t0 < hi) load_tile<D>(a, pages, kvh, t0, lane, next);
-                run(std::true_type{}, x, t0 - STEP);
+            while (t0 <= plain && x.ok == 3) {
+                const int ok = turn();
+                run(std::true_type{}, ok, t0 - STEP);
             }
             if (t0 >= hi) break;
-            const Tile<D> x = next;
-            t0 += STEP;
-            if (t0 < hi) load_tile<D>(a, pages, kvh, t0, lane, next);
-            run(std::false_type{}, x, t0 - STEP);
+            const int ok = turn();
+            run(std::false_type{}, ok, t0 - STEP);
         } while (t0 < hi);
     }
     } else {
@@ -663,7 +761,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
         for (int j = 0; j < KS; ++j) to[(wave * KS + j) * 64] = eight_of(x.k[0][j], scale_bits(x.ks[0]));
         uint32_t w[8];
         float s[8];
-        values_of<D, false>(x, T0 + 32 * half, hi_all, lane, w, s);
+        values_of<D>(x, T0 + 32 * half, hi_all, lane, w, s);
         // Values that are no numbers, of tokens that some rows do not see, are
         // left out, as 0 times NaN would reach those rows; the others get them
         // one end at a time.
@@ -701,7 +799,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
         for (int stop = t0 + 1; stop <= t0 + 32; ++stop) {
             uint32_t w[8];
             float s[8];
-            values_of<D, false>(z, t0, min(stop, hi_all), lane, w, s);
+            values_of<D>(z, t0, min(stop, hi_all), lane, w, s);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (!is_odd(s[e])) { w[e] = 0; s[e] = 1.f; }
