@@ -157,18 +157,21 @@ struct Walk {
     }
 };
 
-// The channels [c, c + VEC) of a lane.  Where the width is no multiple of VEC
-// the last lane takes the last VEC ones, and computes and writes the same
-// values as its neighbour for those they share.  Lanes behind it (in false)
-// work on the last channels too, without writing.
+// The channels [c, c + VEC) of a lane.  Where the width is odd, the second lane
+// of all begins one channel early: it and the first compute and write the same
+// values of channel 1.  Both are of one wave, which has read what it needs of
+// the states before it writes any, as state_out may be state_in.  Lanes behind
+// the last channel (in false) work on the last ones, without writing.
 struct Channels {
     int64_t c;
     bool in;
 };
 template <int VEC>
 __device__ __forceinline__ Channels channels_of(int64_t D, int64_t block, int lane) {
-    const int64_t c = (block * 64 + lane) * VEC;
-    return Channels{c + VEC <= D ? c : D - VEC, c < D};
+    static_assert(VEC <= 2, "an odd width shares one channel");
+    int64_t c = (block * 64 + lane) * VEC;
+    if (VEC == 2 && c > 0 && (D & 1)) --c;
+    return Channels{c + VEC <= D ? c : D - VEC, c + VEC <= D};
 }
 
 struct TileGrid {

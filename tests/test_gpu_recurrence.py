@@ -193,6 +193,17 @@ def test_state_in_place():
         assert same is s and torch.equal(s, state) and torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("B,T,D", [(64, 40, 129), (3, 700, 129), (2, 300, 257), (5, 130, 127), (4, 200, 3)])
+def test_state_in_place_of_odd_widths(B, T, D):
+    """A channel that two lanes share: neither reads a state that the other has written."""
+    i = made(B, T, D, "bf16")
+    out, state = kda.recurrence_prefill(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"])
+    s = i["s0"].clone()
+    out2, same = kda.recurrence_prefill(i["x"], i["la"], FLOOR, g=i["g"], state_in=s, state_out=s)
+    torch.cuda.synchronize()
+    assert same is s and torch.equal(s, state) and torch.equal(out, out2)
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("N,D", [(1, 1), (3, 77), (7, 128), (300, 96)])
 def test_step(N, D, io):
