@@ -4,18 +4,16 @@
 //   out = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),  s_t = scale q . K_t,
 //   m = max s_t, kept as a running maximum and sum in fp32.
 //
-// The cache's values go from memory into MFMA operands without LDS.  A wave
-// takes 32 tokens of one key/value head at a time, against 16 R rows; a row is
-// a (query, head of the group) pair, so the heads that share keys share their
-// loads.  With lane = 16 g + n:
-//  * S^T = K Q^T.  A operand: token n of 16, its channels [D/4 g, D/4 g + D/4)
-//    as one 16-byte (D = 128) load, D/32 steps of 8 channels; one scale byte
-//    covers them.  B operand: the row n with the same channels.
-//  * The result holds row n's scores of the tokens 4 g + v (and 16 + 4 g + v of
-//    the second half): as they lie these are the B operand of O^T = V^T P^T, no
-//    exchange between lanes.  Maximum and sum of a row are in-lane, then two
-//    exchanges over g.
-//  * V^T as A operand needs 8 tokens of one channel a lane.  A lane loads, for
+// A wave takes 32 (few rows) or 64 (many) tokens of one key/value head at a
+// time, against 16 R rows; a row is a (query, head of the group) pair, so the
+// heads that share keys share their loads.  With lane = 16 g + n:
+//  * S^T = K Q^T.  A operand: token n of 16, its channels [D/4 g, D/4 g + D/4),
+//    D/32 steps of 8 channels; one scale byte covers them.  B operand: the row
+//    n with the same channels.
+//  * The result holds row n's scores of 4 tokens a half: as they lie these are
+//    the B operand of O^T = V^T P^T, no exchange between lanes.  Maximum and
+//    sum of a row are in-lane, then two exchanges over g.
+//  * V^T as A operand needs 8 tokens of one channel a lane.  A lane takes, for
 //    its 8 tokens, the word with the channels D/16 n + j: conversion gives
 //    channel pairs of one token, a byte permute pairs the tokens, and j runs
 //    over the MFMAs.  O^T then holds D/4 consecutive channels of row n.
@@ -23,13 +21,24 @@
 // exact too and the probabilities round once to bf16; fp32 queries and
 // probabilities are taken in three bf16 parts, which together hold 24 bits.
 //
-// Few rows (decode): the four waves of a workgroup take turns at the 32-token
-// tiles and join their results through LDS.  Many rows: each wave has rows of
-// its own.  Sequences are ragged and a query's tokens grow along a prompt, so
-// work is dealt out by tokens: the row blocks' tokens lie end to end in units
-// of 128, and each workgroup takes the same number of units, which may end one
-// block, hold several and begin another.  What a workgroup has of a block
-// that it does not hold whole is a part; a second kernel joins the parts.
+// Few rows (decode; at most kSplitMaxRows a sequence and head): the four waves
+// of a workgroup take turns at the 32-token tiles, each through LDS of its own,
+// and join their results.  Bound by the cache's bytes and by what a block costs
+// at its ends: 256 ragged contexts of up to 8192 tokens, 32 heads over 8 of
+// 128, take 82 us + 5 us for joining the parts where the bytes alone take 66
+// (5 us go into dealing out the work, about 20 into the ends of the blocks).
+// Loaded in the order of the operands, without LDS, it took 92.
+// Many rows (prompts): each wave has rows of its own, 64 tokens at a time are
+// converted once for all four waves, and operands come from LDS.  Bound by the
+// vector unit's work on the scores beside the products: 4 prompts of up to 1000
+// tokens at the end of contexts of up to 8192, the same heads, take 195 us + 20
+// us for the parts, the matrix units busy a quarter of it.  16 rows a wave
+// instead of 32 took 320 us, 48 or 64 (one workgroup a CU) 306 and 289.
+// Sequences are ragged and a query's tokens grow along a prompt, so work is
+// dealt out by tokens: the row blocks' tokens lie end to end in units of 128,
+// and each workgroup takes the same number of units, which may end one block,
+// hold several and begin another.  What a workgroup has of a block that it
+// does not hold whole is a part; a second kernel joins the parts.
 #include <type_traits>
 
 #include "kda_common.hpp"
@@ -52,7 +61,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;         // tokens that are dealt out at once
 // Units that a block counts for beside its own, as beginning one costs: 256
-// ragged contexts take 98 us with 2, 93 with 3, 91 with 5, 102 with 8, and 120
+// ragged contexts took 98 us with 2, 93 with 3, 91 with 5, 102 with 8 and 120
 // with none; prompts 197, 207, 201 and 213.
 constexpr int kBlockCost = 4;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
@@ -496,502 +505,502 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4
     }
 
     for (; at < stop; ++slot) {
-    const Block b = block_of(a, l, slot);
-    const int n_rows = b.n_rows;
-    int lo = 0, lim = b.total, part = -1;
-    if (l.groups > 0) {
-        // the block's own units are [p0, p1)
-        const int p0 = __builtin_amdgcn_readfirstlane(before[slot]) + kBlockCost, p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
-        const int from = max(at, p0), to = min(stop, p1);
-        at = max(at, min(stop, p1));
-        if (to <= from) continue;       // no rows, or the next workgroup has them all
-        lo = (from - p0) * kUnit;
-        lim = min(b.total, (to - p0) * kUnit);
-        if (from > p0) {
-            part = 2 * group;
-        } else if (to < p1) {
-            part = 2 * group + 1;
-            if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.row0, n_rows, b.begin, (p1 - 1) / each};
-        }
-    } else {
-        at = stop;
-        if (!b.any) continue;
-    }
-    const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
-    const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
-    const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
-    const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
-
-    // scores in powers of two, with the sign of the scale in the queries, so
-    // that the largest product is the largest score; not 0, which would make
-    // NaN of a masked score's -inf
-    const float to_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
-    const float sign = a.scale < 0.f ? -1.f : 1.f;
-
-    // queries: row n of each 16, channels [PER g, PER g + PER)
-    bf16x8 q[R][KS][PARTS];
-    int end[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int row = row0 + 16 * r + n;
-        end[r] = end_of(a, b, row);
-        const E* p = reinterpret_cast<const E*>(a.q) + (int64_t)place_of(a, b.row0, kvh, row < n_rows ? row : 0) * D + PER * g;
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if constexpr (PARTS == 1) {
-                    q[r][j][0][e] = (__bf16)(sign * to_f32(p[8 * j + e]));
-                } else {
-                    __bf16 s[PARTS];
-                    parts_of<PARTS>(sign * p[8 * j + e], s);
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) q[r][j][i][e] = s[i];
-                }
+        const Block b = block_of(a, l, slot);
+        const int n_rows = b.n_rows;
+        int lo = 0, lim = b.total, part = -1;
+        if (l.groups > 0) {
+            // the block's own units are [p0, p1)
+            const int p0 = __builtin_amdgcn_readfirstlane(before[slot]) + kBlockCost, p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
+            const int from = max(at, p0), to = min(stop, p1);
+            at = max(at, min(stop, p1));
+            if (to <= from) continue;       // no rows, or the next workgroup has them all
+            lo = (from - p0) * kUnit;
+            lim = min(b.total, (to - p0) * kUnit);
+            if (from > p0) {
+                part = 2 * group;
+            } else if (to < p1) {
+                part = 2 * group + 1;
+                if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.row0, n_rows, b.begin, (p1 - 1) / each};
             }
-    }
-
-    f32x4 o[R][VJ];
-    float m[R], sum[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        sum[r] = 0.f;
-#pragma unroll
-        for (int j = 0; j < VJ; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    Pages pages(a, b.s, lo);
-
-    // The running maxima, of N scores of a lane for each row tile.
-    auto raise = [&](const auto& y) {
-        constexpr int N = sizeof(y[0]) / sizeof(float);
-        float top[R];
-        bool more = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            top[r] = y[r][0];
-#pragma unroll
-            for (int e = 1; e < N; ++e) top[r] = larger(top[r], y[r][e]);
-            top[r] = over_g(top[r]) * to_log2;
-            more = more || top[r] > m[r] + kSlack;
-        }
-        if (__any(more)) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float mn = fmaxf(m[r], top[r]);
-                const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
-                sum[r] *= f;
-#pragma unroll
-                for (int j = 0; j < VJ; ++j) o[r][j] *= f;
-                m[r] = mn;
-            }
-        }
-    };
-    // 8 scores into probabilities of row tile r, whose sum is kept.
-    auto weigh = [&](int r, const float* y, bf16x8 (&p)[PARTS]) {
-        const float base = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float z = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
-            sum[r] += z;
-            if constexpr (PARTS == 1) {
-                p[0][e] = (__bf16)z;
-            } else {
-                __bf16 s[PARTS];
-                parts_of<PARTS>(z, s);
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) p[i][e] = s[i];
-            }
-        }
-    };
-    // Whether stop - 1 is the last token that this lane's row of row tile r sees
-    // of the 32 from t0 on.
-    auto ends_at = [&](int r, int t0, int stop) { return min(min(end[r], hi), t0 + 32) == stop; };
-    // to + values x probabilities, where the row counts.
-    auto product = [&](f32x4& to, bf16x8 value, const bf16x8 (&p)[PARTS], bool counts) {
-        f32x4 sum = to;
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value, p[i], sum, 0, 0, 0);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) to[v] = counts ? sum[v] : to[v];
-    };
-
-    if constexpr (SPLITW) {
-    // 32 staged tokens; ALL: every row sees all of them
-    const Stage<D> stage = {reinterpret_cast<char*>(&so[wave][0][0]), lane};
-    static_assert(Stage<D>::BYTES <= (int)sizeof(so[0]), "a wave stages where its results go later");
-    auto run = [&](auto all, int ok, int t0) {
-        constexpr bool ALL = decltype(all)::value;
-        float y[R][8];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            uint32_t kw[KS];
-            float ks;
-            stage.key(u, kw, ks);
-            f32x4 acc[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < KS; ++j) {
-                const bf16x8 k = eight_of(kw[j], ks);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc[r], 0, 0, 0);
-            }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int t = t0 + 16 * u + g + 4 * v;
-                const bool in = ALL || ((ok >> u & 1) && t < hi);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    y[r][4 * u + v] = acc[r][v];
-                    if constexpr (!ALL) {
-                        if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
-                    }
-                }
-            }
-        }
-        raise(y);
-        bf16x8 p[R][PARTS];
-#pragma unroll
-        for (int r = 0; r < R; ++r) weigh(r, y[r], p[r]);
-
-        uint32_t w[8];
-        float s[8];
-        // the values of tokens before `stop`; the others are zeros, whatever memory holds there
-        auto values = [&](int stop) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t c, b;
-                    stage.value(u, v, c, b);
-                    if constexpr (!ALL) {
-                        const bool in = (ok >> u & 1) && t0 + 16 * u + g + 4 * v < stop;
-                        c = in ? c : 0u;
-                        b = in ? b : 127u;
-                    }
-                    w[4 * u + v] = c;
-                    s[4 * u + v] = scale_bits(b);
-                }
-        };
-        auto accumulate = [&](auto counts) {
-            auto pair = [&](auto I) {
-                bf16x8 c[2];
-                two_channels<decltype(I)::value>(w, s, c[0], c[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], counts(r));
-            };
-            pair(std::integral_constant<int, 0>{});
-            pair(std::integral_constant<int, 1>{});
-            if constexpr (VJ == 8) {
-                pair(std::integral_constant<int, 2>{});
-                pair(std::integral_constant<int, 3>{});
-            }
-        };
-        values(hi);
-        if constexpr (ALL) {
-            accumulate([](int) { return true; });
         } else {
-            bool odd = false;       // a value that is no number, which some rows do not see
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd = odd || is_odd(s[e]);
-            const bool apart = __any(odd);
-            // Where apart, the rows of one end at a time, with the tokens behind
-            // it cleared: 0 times NaN would reach rows that do not see it.
-            for (int stop = apart ? t0 + 1 : t0 + 32;; ++stop) {
-                if (apart) values(min(stop, hi));
-                accumulate([&](int r) { return !apart || ends_at(r, t0, stop); });
-                if (stop == t0 + 32) break;
-            }
+            at = stop;
+            if (!b.any) continue;
         }
-        stage.done();
-    };
-    // the next tile is on its way while one is worked on
-    constexpr int STEP = 32 * kWaves;
-    const int plain = min(all_see, hi) - 32;       // last tile that every row sees
-    int t0 = lo + 32 * wave;
-    if (t0 < hi) {
-        Raw<D> x;
-        load_raw<D>(a, pages, kvh, t0, lane, x);
-        auto turn = [&] {           // stages one tile, sends for the next
-            const int ok = x.ok;
-            stage.put(x);
-            t0 += STEP;
-            if (t0 < hi) load_raw<D>(a, pages, kvh, t0, lane, x);
-            return ok;
-        };
-        do {
-            while (t0 <= plain && x.ok == 3) {
-                const int ok = turn();
-                run(std::true_type{}, ok, t0 - STEP);
-            }
-            if (t0 >= hi) break;
-            const int ok = turn();
-            run(std::false_type{}, ok, t0 - STEP);
-        } while (t0 < hi);
-    }
-    } else {
-    // 64 tokens at a time for all waves, as operands in LDS: [k | v] operands of
-    // 64 lanes x 16 bytes.  Wave w converts the keys of its 16 tokens and half
-    // of the channels of the values of 32, while the last 64 tokens' are used.
-    constexpr int KB = 4 * KS, OPS = KB + 2 * VJ;
-    __shared__ int odd[2][2];       // whether values of 32 tokens were left out (see below)
-    bf16x8* ops = reinterpret_cast<bf16x8*>(dynamic);
-    const int half = wave >> 1;
-    const int hi_all = min(end_of(a, b, min(b.begin + l.rows, n_rows) - 1), lim), see_all = end_of(a, b, b.begin);
-    Tile<D> x;                      // the values of 32 tokens; the keys of 16 in its first half
-    int ok = 0, ok_next = 0;        // which 16 tokens have a page
-    auto fetch = [&](int T0) {
-        ok_next = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int page = pages.of(T0 + 16 * u);
-            ok_next |= (page >= 0 && page < a.c.pages && T0 + 16 * u < hi_all) << u;
-        }
-        load_keys<D>(a, pages, kvh, T0 + 16 * wave, lane, x);
-        load_values<D>(a, pages, kvh, T0 + 32 * half, lane, x);
-    };
-    auto convert = [&](int T0, int buf) {
-        bf16x8* to = ops + buf * OPS * 64 + lane;
-#pragma unroll
-        for (int j = 0; j < KS; ++j) to[(wave * KS + j) * 64] = eight_of(x.k[0][j], scale_bits(x.ks[0]));
-        uint32_t w[8];
-        float s[8];
-        values_of<D>(x, T0 + 32 * half, hi_all, lane, w, s);
-        // Values that are no numbers, of tokens that some rows do not see, are
-        // left out, as 0 times NaN would reach those rows; the others get them
-        // one end at a time.
-        const bool partly = T0 + 64 > see_all;
-        bool some = false;
-        if (partly) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const bool no = is_odd(s[e]);
-                some = some || no;
-                if (no) { w[e] = 0; s[e] = 1.f; }
-            }
-        }
-        if ((wave & 1) == 0) {
-            const bool any = __any(some);
-            if (lane == 0) odd[buf][half] = any;
-        }
-        auto pair = [&](auto I) {
-            two_channels<decltype(I)::value>(w, s, to[(KB + half * VJ + 2 * decltype(I)::value) * 64], to[(KB + half * VJ + 2 * decltype(I)::value + 1) * 64]);
-        };
-        if constexpr (VJ == 8) {
-            if ((wave & 1) == 0) { pair(std::integral_constant<int, 0>{}); pair(std::integral_constant<int, 1>{}); }
-            else { pair(std::integral_constant<int, 2>{}); pair(std::integral_constant<int, 3>{}); }
-        } else {
-            if ((wave & 1) == 0) pair(std::integral_constant<int, 0>{});
-            else pair(std::integral_constant<int, 1>{});
-        }
-    };
-    // What the values that were left out of 32 tokens add, to the rows of one
-    // end at a time.
-    auto add_odd = [&](const bf16x8 (&p)[R][PARTS], int t0) {
-        Tile<D> z;
-        load_values<D>(a, pages, kvh, t0, lane, z);
-#pragma unroll 1
-        for (int stop = t0 + 1; stop <= t0 + 32; ++stop) {
-            uint32_t w[8];
-            float s[8];
-            values_of<D>(z, t0, min(stop, hi_all), lane, w, s);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (!is_odd(s[e])) { w[e] = 0; s[e] = 1.f; }
-            auto pair = [&](auto I) {
-                bf16x8 c[2];
-                two_channels<decltype(I)::value>(w, s, c[0], c[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], ends_at(r, t0, stop));
-            };
-            pair(std::integral_constant<int, 0>{});
-            pair(std::integral_constant<int, 1>{});
-            if constexpr (VJ == 8) {
-                pair(std::integral_constant<int, 2>{});
-                pair(std::integral_constant<int, 3>{});
-            }
-        }
-    };
-    // 64 tokens, of which every row sees all or not
-    auto use = [&](bool all, int T0, int buf) {
-        const bf16x8* from = ops + buf * OPS * 64 + lane;
-        // operands are read a group ahead of their products: left alone the
-        // compiler reads each right before its product and waits
-        float y[R][16];
-        bf16x8 k[2][KS];
-#pragma unroll
-        for (int j = 0; j < KS; ++j) k[0][j] = from[j * 64];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (u < 3) {
-#pragma unroll
-                for (int j = 0; j < KS; ++j) k[(u + 1) & 1][j] = from[((u + 1) * KS + j) * 64];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            f32x4 acc[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < KS; ++j)
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u & 1][j], q[r][j][i], acc[r], 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) y[r][4 * u + v] = acc[r][v];
-        }
-        if (!all) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool page = ok >> u & 1;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int t = T0 + 16 * u + 4 * g + v;
-                    const bool in = page && t < hi;
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
-                }
-            }
-        }
-        raise(y);
-        bf16x8 p[2][R][PARTS], v[2][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[0][j] = from[(KB + j) * 64];
-#pragma unroll
-        for (int r = 0; r < R; ++r) weigh(r, y[r], p[0][r]);
-#pragma unroll
-        for (int c = 0; c < 2 * VJ / 4; ++c) {         // four operands at a time
-            if (c + 1 < 2 * VJ / 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[(c + 1) & 1][j] = from[(KB + 4 * (c + 1) + j) * 64];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            const int hh = c / (VJ / 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        f32x4& to = o[r][4 * c % VJ + j];
-                        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c & 1][j], p[hh][r][i], to, 0, 0, 0);
-                    }
-            // the second half's exponentials go beside the first half's products
-            if (c == 0) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) weigh(r, y[r] + 8, p[1][r]);
-            }
-        }
-        if (T0 + 64 > see_all) {
-            if (__builtin_amdgcn_readfirstlane(odd[buf][0])) add_odd(p[0], T0);
-            if (__builtin_amdgcn_readfirstlane(odd[buf][1])) add_odd(p[1], T0 + 32);
-        }
-    };
-    const int plain = min(all_see, hi) - 64;       // last tile that every row of the wave sees
-    if (lo < hi_all) {
-        fetch(lo);
-        convert(lo, 0);
-        ok = ok_next;
-        __syncthreads();
-        int buf = 0;
-        for (int T0 = lo; T0 < hi_all; T0 += 64, buf ^= 1) {
-            if (T0 + 64 < hi_all) fetch(T0 + 64);
-            if (T0 < hi) use(T0 <= plain && ok == 15, T0, buf);
-            if (T0 + 64 < hi_all) convert(T0 + 64, buf ^ 1);
-            ok = ok_next;
-            __syncthreads();
-        }
-    }
-    }
+        const int row0 = b.begin + (SPLITW ? 0 : wave * ROWS);
+        const int last = min(row0 + ROWS, n_rows) - 1;          // may lie before row0: nothing for this wave
+        const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
+        const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
 
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        sum[r] += __shfl_xor(sum[r], 16);
-        sum[r] += __shfl_xor(sum[r], 32);
-    }
+        // scores in powers of two, with the sign of the scale in the queries, so
+        // that the largest product is the largest score; not 0, which would make
+        // NaN of a masked score's -inf
+        const float to_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
 
-    // what a row's result becomes: a part, or the output
-    auto put = [&](int row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
-        if (part >= 0) {
-            const int64_t i = ((int64_t)part * a.c.heads + kvh) * l.rows + (row - b.begin);
-            float* po = parts.o + i * D + c0;
-            *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
-            *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
-            if (c0 == 0) { parts.sums[2 * i] = mx; parts.sums[2 * i + 1] = sm; }
-            return;
-        }
-        const int64_t at = place_of(a, b.row0, kvh, row);
-        const float f = sm == 0.f ? 0.f : 1.f / sm;
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = y[e] * f;
-        if (a.g) {
-            const E* gp = reinterpret_cast<const E*>(a.g) + at * D + c0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] *= sigmoidf_(to_f32(gp[e]));
-        }
-        E* op = reinterpret_cast<E*>(a.out) + at * D + c0;
-        st4(op, f32x4{z[0], z[1], z[2], z[3]});
-        st4(op + 4, f32x4{z[4], z[5], z[6], z[7]});
-    };
-
-    if constexpr (!SPLITW) {
+        // queries: row n of each 16, channels [PER g, PER g + PER)
+        bf16x8 q[R][KS][PARTS];
+        int end[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int row = row0 + 16 * r + n;
-            if (row >= n_rows) continue;
-            // element (j, v) of the result is channel PER g + VJ v + j
+            end[r] = end_of(a, b, row);
+            const E* p = reinterpret_cast<const E*>(a.q) + (int64_t)place_of(a, b.row0, kvh, row < n_rows ? row : 0) * D + PER * g;
 #pragma unroll
-            for (int c = 0; c < PER; c += 8) {
-                float y[8];
+            for (int j = 0; j < KS; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = o[r][(c + e) % VJ][(c + e) / VJ];
-                put(row, PER * g + c, y, m[r], sum[r]);
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (PARTS == 1) {
+                        q[r][j][0][e] = (__bf16)(sign * to_f32(p[8 * j + e]));
+                    } else {
+                        __bf16 s[PARTS];
+                        parts_of<PARTS>(sign * p[8 * j + e], s);
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) q[r][j][i][e] = s[i];
+                    }
+                }
+        }
+
+        f32x4 o[R][VJ];
+        float m[R], sum[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            sum[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < VJ; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        Pages pages(a, b.s, lo);
+
+        // The running maxima, of N scores of a lane for each row tile.
+        auto raise = [&](const auto& y) {
+            constexpr int N = sizeof(y[0]) / sizeof(float);
+            float top[R];
+            bool more = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                top[r] = y[r][0];
+#pragma unroll
+                for (int e = 1; e < N; ++e) top[r] = larger(top[r], y[r][e]);
+                top[r] = over_g(top[r]) * to_log2;
+                more = more || top[r] > m[r] + kSlack;
+            }
+            if (__any(more)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float mn = fmaxf(m[r], top[r]);
+                    const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[r] - mn);
+                    sum[r] *= f;
+#pragma unroll
+                    for (int j = 0; j < VJ; ++j) o[r][j] *= f;
+                    m[r] = mn;
+                }
+            }
+        };
+        // 8 scores into probabilities of row tile r, whose sum is kept.
+        auto weigh = [&](int r, const float* y, bf16x8 (&p)[PARTS]) {
+            const float base = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
+                sum[r] += z;
+                if constexpr (PARTS == 1) {
+                    p[0][e] = (__bf16)z;
+                } else {
+                    __bf16 s[PARTS];
+                    parts_of<PARTS>(z, s);
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) p[i][e] = s[i];
+                }
+            }
+        };
+        // Whether stop - 1 is the last token that this lane's row of row tile r sees
+        // of the 32 from t0 on.
+        auto ends_at = [&](int r, int t0, int stop) { return min(min(end[r], hi), t0 + 32) == stop; };
+        // to + values x probabilities, where the row counts.
+        auto product = [&](f32x4& to, bf16x8 value, const bf16x8 (&p)[PARTS], bool counts) {
+            f32x4 sum = to;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(value, p[i], sum, 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) to[v] = counts ? sum[v] : to[v];
+        };
+
+        if constexpr (SPLITW) {
+            // 32 staged tokens; ALL: every row sees all of them
+            const Stage<D> stage = {reinterpret_cast<char*>(&so[wave][0][0]), lane};
+            static_assert(Stage<D>::BYTES <= (int)sizeof(so[0]), "a wave stages where its results go later");
+            auto run = [&](auto all, int ok, int t0) {
+                constexpr bool ALL = decltype(all)::value;
+                float y[R][8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t kw[KS];
+                    float ks;
+                    stage.key(u, kw, ks);
+                    f32x4 acc[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < KS; ++j) {
+                        const bf16x8 k = eight_of(kw[j], ks);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[r][j][i], acc[r], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int t = t0 + 16 * u + g + 4 * v;
+                        const bool in = ALL || ((ok >> u & 1) && t < hi);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            y[r][4 * u + v] = acc[r][v];
+                            if constexpr (!ALL) {
+                                if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
+                            }
+                        }
+                    }
+                }
+                raise(y);
+                bf16x8 p[R][PARTS];
+#pragma unroll
+                for (int r = 0; r < R; ++r) weigh(r, y[r], p[r]);
+
+                uint32_t w[8];
+                float s[8];
+                // the values of tokens before `stop`; the others are zeros, whatever memory holds there
+                auto values = [&](int stop) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t c, b;
+                            stage.value(u, v, c, b);
+                            if constexpr (!ALL) {
+                                const bool in = (ok >> u & 1) && t0 + 16 * u + g + 4 * v < stop;
+                                c = in ? c : 0u;
+                                b = in ? b : 127u;
+                            }
+                            w[4 * u + v] = c;
+                            s[4 * u + v] = scale_bits(b);
+                        }
+                };
+                auto accumulate = [&](auto counts) {
+                    auto pair = [&](auto I) {
+                        bf16x8 c[2];
+                        two_channels<decltype(I)::value>(w, s, c[0], c[1]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], counts(r));
+                    };
+                    pair(std::integral_constant<int, 0>{});
+                    pair(std::integral_constant<int, 1>{});
+                    if constexpr (VJ == 8) {
+                        pair(std::integral_constant<int, 2>{});
+                        pair(std::integral_constant<int, 3>{});
+                    }
+                };
+                values(hi);
+                if constexpr (ALL) {
+                    accumulate([](int) { return true; });
+                } else {
+                    bool odd = false;       // a value that is no number, which some rows do not see
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) odd = odd || is_odd(s[e]);
+                    const bool apart = __any(odd);
+                    // Where apart, the rows of one end at a time, with the tokens behind
+                    // it cleared: 0 times NaN would reach rows that do not see it.
+                    for (int stop = apart ? t0 + 1 : t0 + 32;; ++stop) {
+                        if (apart) values(min(stop, hi));
+                        accumulate([&](int r) { return !apart || ends_at(r, t0, stop); });
+                        if (stop == t0 + 32) break;
+                    }
+                }
+                stage.done();
+            };
+            // the next tile is on its way while one is worked on
+            constexpr int STEP = 32 * kWaves;
+            const int plain = min(all_see, hi) - 32;       // last tile that every row sees
+            int t0 = lo + 32 * wave;
+            if (t0 < hi) {
+                Raw<D> x;
+                load_raw<D>(a, pages, kvh, t0, lane, x);
+                auto turn = [&] {           // stages one tile, sends for the next
+                    const int ok = x.ok;
+                    stage.put(x);
+                    t0 += STEP;
+                    if (t0 < hi) load_raw<D>(a, pages, kvh, t0, lane, x);
+                    return ok;
+                };
+                do {
+                    while (t0 <= plain && x.ok == 3) {
+                        const int ok = turn();
+                        run(std::true_type{}, ok, t0 - STEP);
+                    }
+                    if (t0 >= hi) break;
+                    const int ok = turn();
+                    run(std::false_type{}, ok, t0 - STEP);
+                } while (t0 < hi);
+            }
+        } else {
+            // 64 tokens at a time for all waves, as operands in LDS: [k | v] operands of
+            // 64 lanes x 16 bytes.  Wave w converts the keys of its 16 tokens and half
+            // of the channels of the values of 32, while the last 64 tokens' are used.
+            constexpr int KB = 4 * KS, OPS = KB + 2 * VJ;
+            __shared__ int odd[2][2];       // whether values of 32 tokens were left out (see below)
+            bf16x8* ops = reinterpret_cast<bf16x8*>(dynamic);
+            const int half = wave >> 1;
+            const int hi_all = min(end_of(a, b, min(b.begin + l.rows, n_rows) - 1), lim), see_all = end_of(a, b, b.begin);
+            Tile<D> x;                      // the values of 32 tokens; the keys of 16 in its first half
+            int ok = 0, ok_next = 0;        // which 16 tokens have a page
+            auto fetch = [&](int T0) {
+                ok_next = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int page = pages.of(T0 + 16 * u);
+                    ok_next |= (page >= 0 && page < a.c.pages && T0 + 16 * u < hi_all) << u;
+                }
+                load_keys<D>(a, pages, kvh, T0 + 16 * wave, lane, x);
+                load_values<D>(a, pages, kvh, T0 + 32 * half, lane, x);
+            };
+            auto convert = [&](int T0, int buf) {
+                bf16x8* to = ops + buf * OPS * 64 + lane;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) to[(wave * KS + j) * 64] = eight_of(x.k[0][j], scale_bits(x.ks[0]));
+                uint32_t w[8];
+                float s[8];
+                values_of<D>(x, T0 + 32 * half, hi_all, lane, w, s);
+                // Values that are no numbers, of tokens that some rows do not see, are
+                // left out, as 0 times NaN would reach those rows; the others get them
+                // one end at a time.
+                const bool partly = T0 + 64 > see_all;
+                bool some = false;
+                if (partly) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const bool no = is_odd(s[e]);
+                        some = some || no;
+                        if (no) { w[e] = 0; s[e] = 1.f; }
+                    }
+                }
+                if ((wave & 1) == 0) {
+                    const bool any = __any(some);
+                    if (lane == 0) odd[buf][half] = any;
+                }
+                auto pair = [&](auto I) {
+                    two_channels<decltype(I)::value>(w, s, to[(KB + half * VJ + 2 * decltype(I)::value) * 64], to[(KB + half * VJ + 2 * decltype(I)::value + 1) * 64]);
+                };
+                if constexpr (VJ == 8) {
+                    if ((wave & 1) == 0) { pair(std::integral_constant<int, 0>{}); pair(std::integral_constant<int, 1>{}); }
+                    else { pair(std::integral_constant<int, 2>{}); pair(std::integral_constant<int, 3>{}); }
+                } else {
+                    if ((wave & 1) == 0) pair(std::integral_constant<int, 0>{});
+                    else pair(std::integral_constant<int, 1>{});
+                }
+            };
+            // What the values that were left out of 32 tokens add, to the rows of one
+            // end at a time.
+            auto add_odd = [&](const bf16x8 (&p)[R][PARTS], int t0) {
+                Tile<D> z;
+                load_values<D>(a, pages, kvh, t0, lane, z);
+#pragma unroll 1
+                for (int stop = t0 + 1; stop <= t0 + 32; ++stop) {
+                    uint32_t w[8];
+                    float s[8];
+                    values_of<D>(z, t0, min(stop, hi_all), lane, w, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!is_odd(s[e])) { w[e] = 0; s[e] = 1.f; }
+                    auto pair = [&](auto I) {
+                        bf16x8 c[2];
+                        two_channels<decltype(I)::value>(w, s, c[0], c[1]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < R; ++r) product(o[r][2 * decltype(I)::value + h], c[h], p[r], ends_at(r, t0, stop));
+                    };
+                    pair(std::integral_constant<int, 0>{});
+                    pair(std::integral_constant<int, 1>{});
+                    if constexpr (VJ == 8) {
+                        pair(std::integral_constant<int, 2>{});
+                        pair(std::integral_constant<int, 3>{});
+                    }
+                }
+            };
+            // 64 tokens, of which every row sees all or not
+            auto use = [&](bool all, int T0, int buf) {
+                const bf16x8* from = ops + buf * OPS * 64 + lane;
+                // operands are read a group ahead of their products: left alone the
+                // compiler reads each right before its product and waits
+                float y[R][16];
+                bf16x8 k[2][KS];
+#pragma unroll
+                for (int j = 0; j < KS; ++j) k[0][j] = from[j * 64];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (u < 3) {
+#pragma unroll
+                        for (int j = 0; j < KS; ++j) k[(u + 1) & 1][j] = from[((u + 1) * KS + j) * 64];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    f32x4 acc[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int i = 0; i < PARTS; ++i) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u & 1][j], q[r][j][i], acc[r], 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) y[r][4 * u + v] = acc[r][v];
+                }
+                if (!all) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const bool page = ok >> u & 1;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const int t = T0 + 16 * u + 4 * g + v;
+                            const bool in = page && t < hi;
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                if (!in || t >= end[r]) y[r][4 * u + v] = -INFINITY;
+                        }
+                    }
+                }
+                raise(y);
+                bf16x8 p[2][R][PARTS], v[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[0][j] = from[(KB + j) * 64];
+#pragma unroll
+                for (int r = 0; r < R; ++r) weigh(r, y[r], p[0][r]);
+#pragma unroll
+                for (int c = 0; c < 2 * VJ / 4; ++c) {         // four operands at a time
+                    if (c + 1 < 2 * VJ / 4) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[(c + 1) & 1][j] = from[(KB + 4 * (c + 1) + j) * 64];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    const int hh = c / (VJ / 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int i = 0; i < PARTS; ++i) {
+                                f32x4& to = o[r][4 * c % VJ + j];
+                                to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[c & 1][j], p[hh][r][i], to, 0, 0, 0);
+                            }
+                    // the second half's exponentials go beside the first half's products
+                    if (c == 0) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) weigh(r, y[r] + 8, p[1][r]);
+                    }
+                }
+                if (T0 + 64 > see_all) {
+                    if (__builtin_amdgcn_readfirstlane(odd[buf][0])) add_odd(p[0], T0);
+                    if (__builtin_amdgcn_readfirstlane(odd[buf][1])) add_odd(p[1], T0 + 32);
+                }
+            };
+            const int plain = min(all_see, hi) - 64;       // last tile that every row of the wave sees
+            if (lo < hi_all) {
+                fetch(lo);
+                convert(lo, 0);
+                ok = ok_next;
+                __syncthreads();
+                int buf = 0;
+                for (int T0 = lo; T0 < hi_all; T0 += 64, buf ^= 1) {
+                    if (T0 + 64 < hi_all) fetch(T0 + 64);
+                    if (T0 < hi) use(T0 <= plain && ok == 15, T0, buf);
+                    if (T0 + 64 < hi_all) convert(T0 + 64, buf ^ 1);
+                    ok = ok_next;
+                    __syncthreads();
+                }
             }
         }
-    } else {
-        // join the waves' results, in their order
-        if (g == 0) {
+
 #pragma unroll
-            for (int r = 0; r < R; ++r) { sm[wave][16 * r + n] = m[r]; ss[wave][16 * r + n] = sum[r]; }
+        for (int r = 0; r < R; ++r) {
+            sum[r] += __shfl_xor(sum[r], 16);
+            sum[r] += __shfl_xor(sum[r], 32);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int j = 0; j < VJ; j += 4)
-                    *reinterpret_cast<f32x4*>(&so[wave][16 * r + n][PER * g + VJ * v + j]) =
-                        f32x4{o[r][j][v], o[r][j + 1][v], o[r][j + 2][v], o[r][j + 3][v]};
-        __syncthreads();
-        const int here = min(ROWS, n_rows - row0);
-        for (int i = threadIdx.x; i < here * (D / 8); i += kWaves * 64) {
-            const int r = i / (D / 8), c0 = i % (D / 8) * 8;
-            float mx = -INFINITY, sum_r = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = sm[w][r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w][r] - mx);
-                sum_r += f * ss[w][r];
-                const f32x4 lo4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0]), hi4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0 + 4]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) { y[e] += f * lo4[e]; y[4 + e] += f * hi4[e]; }
+
+        // what a row's result becomes: a part, or the output
+        auto put = [&](int row, int c0, const float* y, float mx, float sm) {      // channels [c0, c0 + 8) of row
+            if (part >= 0) {
+                const int64_t i = ((int64_t)part * a.c.heads + kvh) * l.rows + (row - b.begin);
+                float* po = parts.o + i * D + c0;
+                *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
+                *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
+                if (c0 == 0) { parts.sums[2 * i] = mx; parts.sums[2 * i + 1] = sm; }
+                return;
             }
-            put(row0 + r, c0, y, mx, sum_r);
+            const int64_t at = place_of(a, b.row0, kvh, row);
+            const float f = sm == 0.f ? 0.f : 1.f / sm;
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = y[e] * f;
+            if (a.g) {
+                const E* gp = reinterpret_cast<const E*>(a.g) + at * D + c0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] *= sigmoidf_(to_f32(gp[e]));
+            }
+            E* op = reinterpret_cast<E*>(a.out) + at * D + c0;
+            st4(op, f32x4{z[0], z[1], z[2], z[3]});
+            st4(op + 4, f32x4{z[4], z[5], z[6], z[7]});
+        };
+
+        if constexpr (!SPLITW) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = row0 + 16 * r + n;
+                if (row >= n_rows) continue;
+                // element (j, v) of the result is channel PER g + VJ v + j
+#pragma unroll
+                for (int c = 0; c < PER; c += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = o[r][(c + e) % VJ][(c + e) / VJ];
+                    put(row, PER * g + c, y, m[r], sum[r]);
+                }
+            }
+        } else {
+            // join the waves' results, in their order
+            if (g == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) { sm[wave][16 * r + n] = m[r]; ss[wave][16 * r + n] = sum[r]; }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int j = 0; j < VJ; j += 4)
+                        *reinterpret_cast<f32x4*>(&so[wave][16 * r + n][PER * g + VJ * v + j]) =
+                            f32x4{o[r][j][v], o[r][j + 1][v], o[r][j + 2][v], o[r][j + 3][v]};
+            __syncthreads();
+            const int here = min(ROWS, n_rows - row0);
+            for (int i = threadIdx.x; i < here * (D / 8); i += kWaves * 64) {
+                const int r = i / (D / 8), c0 = i % (D / 8) * 8;
+                float mx = -INFINITY, sum_r = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][r]);
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const float f = sm[w][r] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(sm[w][r] - mx);
+                    sum_r += f * ss[w][r];
+                    const f32x4 lo4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0]), hi4 = *reinterpret_cast<const f32x4*>(&so[w][r][c0 + 4]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { y[e] += f * lo4[e]; y[4 + e] += f * hi4[e]; }
+                }
+                put(row0 + r, c0, y, mx, sum_r);
+            }
+            __syncthreads();                // before the next block's results
         }
-        __syncthreads();                // before the next block's results
-    }
     }
 }
 
@@ -1012,67 +1021,67 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     const int count = min(cut.last, l.groups - 1) - w0 + 1, rows = min(l.rows, cut.n_rows - cut.begin);
     if (cut.n_rows <= 0 || cut.begin < 0 || count < 2) return;
     for (int r = chunk * (kWaves / WAVES) + wave / WAVES; r < rows; r += chunks * (kWaves / WAVES)) {
-    const int64_t stride = 2 * (int64_t)a.c.heads * l.rows;
-    const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r, rest = first - stride / 2;
-    const int64_t at = place_of(a, cut.row0, kvh, cut.begin + r);
-    if (at < 0 || at >= a.tokens * a.heads) return;
-    auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
-    auto sums = [&](int i) { return i < count ? *reinterpret_cast<const f32x2*>(parts.sums + 2 * place(i)) : f32x2{-INFINITY, 0.f}; };
-    typedef typename std::conditional<PER == 2, f32x2, float>::type OV;
-    auto part = [&](int i) { return *reinterpret_cast<const OV*>(parts.o + place(i) * D + lane * PER); };
+        const int64_t stride = 2 * (int64_t)a.c.heads * l.rows;
+        const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r, rest = first - stride / 2;
+        const int64_t at = place_of(a, cut.row0, kvh, cut.begin + r);
+        if (at < 0 || at >= a.tokens * a.heads) return;
+        auto place = [&](int i) { return i == 0 ? first : rest + i * stride; };
+        auto sums = [&](int i) { return i < count ? *reinterpret_cast<const f32x2*>(parts.sums + 2 * place(i)) : f32x2{-INFINITY, 0.f}; };
+        typedef typename std::conditional<PER == 2, f32x2, float>::type OV;
+        auto part = [&](int i) { return *reinterpret_cast<const OV*>(parts.o + place(i) * D + lane * PER); };
 
-    // the first parts are on their way while their weights are found
-    constexpr int AHEAD = 8;
-    f32x2 ms = sums(lane);
-    OV x[AHEAD];
+        // the first parts are on their way while their weights are found
+        constexpr int AHEAD = 8;
+        f32x2 ms = sums(lane);
+        OV x[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) x[k] = part(min(turn + k * WAVES, count - 1));
-    E gate[PER];
+        for (int k = 0; k < AHEAD; ++k) x[k] = part(min(turn + k * WAVES, count - 1));
+        E gate[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) gate[e] = a.g ? reinterpret_cast<const E*>(a.g)[at * D + lane * PER + e] : (E)0.f;
-    float mx = ms[0];
-    for (int i = lane + 64; i < count; i += 64) mx = fmaxf(mx, sums(i)[0]);
+        for (int e = 0; e < PER; ++e) gate[e] = a.g ? reinterpret_cast<const E*>(a.g)[at * D + lane * PER + e] : (E)0.f;
+        float mx = ms[0];
+        for (int i = lane + 64; i < count; i += 64) mx = fmaxf(mx, sums(i)[0]);
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-    float sum = 0.f;
-    OV o = OV(0.f);
-    for (int i0 = 0; i0 < count; i0 += 64) {
-        if (i0 > 0) ms = sums(i0 + lane);
-        const float w = ms[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[0] - mx);
-        sum += w * ms[1];
-        auto weight = [&](int k) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k)); };
-        const int most = min(count - i0, 64);
-        int k = turn;
-        if (i0 == 0) {
+        for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
+        float sum = 0.f;
+        OV o = OV(0.f);
+        for (int i0 = 0; i0 < count; i0 += 64) {
+            if (i0 > 0) ms = sums(i0 + lane);
+            const float w = ms[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[0] - mx);
+            sum += w * ms[1];
+            auto weight = [&](int k) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k)); };
+            const int most = min(count - i0, 64);
+            int k = turn;
+            if (i0 == 0) {
 #pragma unroll
-            for (int q = 0; q < AHEAD; ++q)
-                if (turn + q * WAVES < most) o += weight(turn + q * WAVES) * x[q];
-            k += AHEAD * WAVES;
-        }
+                for (int q = 0; q < AHEAD; ++q)
+                    if (turn + q * WAVES < most) o += weight(turn + q * WAVES) * x[q];
+                k += AHEAD * WAVES;
+            }
 #pragma unroll 8
-        for (; k < most; k += WAVES) o += weight(k) * part(i0 + k);
-    }
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
-    if constexpr (WAVES > 1) {
-        *reinterpret_cast<OV*>(&acc[wave][lane * PER]) = o;
-        __syncthreads();
-        if (turn == 0) {
-#pragma unroll
-            for (int k = 1; k < WAVES; ++k) o += *reinterpret_cast<const OV*>(&acc[wave + k][lane * PER]);
+            for (; k < most; k += WAVES) o += weight(k) * part(i0 + k);
         }
-        __syncthreads();
-        if (turn != 0) continue;
-    }
-    float y[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        if constexpr (PER == 2) y[e] = o[e];
-        else y[e] = o;
-        y[e] = sum == 0.f ? 0.f : y[e] / sum;
-        if (a.g) y[e] *= sigmoidf_(to_f32(gate[e]));
-        reinterpret_cast<E*>(a.out)[at * D + lane * PER + e] = from_f32<E>(y[e]);
-    }
+        for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
+        if constexpr (WAVES > 1) {
+            *reinterpret_cast<OV*>(&acc[wave][lane * PER]) = o;
+            __syncthreads();
+            if (turn == 0) {
+#pragma unroll
+                for (int k = 1; k < WAVES; ++k) o += *reinterpret_cast<const OV*>(&acc[wave + k][lane * PER]);
+            }
+            __syncthreads();
+            if (turn != 0) continue;
+        }
+        float y[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if constexpr (PER == 2) y[e] = o[e];
+            else y[e] = o;
+            y[e] = sum == 0.f ? 0.f : y[e] / sum;
+            if (a.g) y[e] *= sigmoidf_(to_f32(gate[e]));
+            reinterpret_cast<E*>(a.out)[at * D + lane * PER + e] = from_f32<E>(y[e]);
+        }
     }
 }
 
@@ -1096,12 +1105,15 @@ Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
     p.l.per_seq = (a.group + p.l.rows - 1) / p.l.rows;
     // with or without offsets: enough slots for both
     const int64_t packed = a.tokens * a.group / p.l.rows + a.n_seq, plain = a.n_seq * p.l.per_seq;
-    p.l.slots = (int)(packed > plain ? packed : plain);
+    const int64_t slots = packed > plain ? packed : plain;
+    p.l.slots = (int)(slots < INT32_MAX ? slots : INT32_MAX);
     // as many workgroups as run at once, but none for less than a unit of
     // every block's longest
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
     const int64_t len = a.max_len < cap ? a.max_len : cap;
     const int64_t units = (int64_t)p.l.slots * ((len + kUnit - 1) / kUnit + kBlockCost);
+    // (3 a CU with one row tile in bf16, else 2; with 256 or 1024 instead of
+    // 512 the prompts above take 319 and 222 us instead of 195)
     int64_t groups = ((p.splitw && p.r == 1 && bf16 ? 768 : 512) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
     const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= INT32_MAX;
@@ -1151,6 +1163,11 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
 }
 
 }  // namespace
+
+bool cache4_attention_fits(bool bf16, const Cache4AttentionArgs& a) {
+    const Plan p = plan_of(bf16, a);
+    return p.l.groups > 0 || (int64_t)p.l.slots * a.c.heads <= UINT32_MAX / (kWaves * 64);
+}
 
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
     const Plan p = plan_of(bf16, a);

@@ -55,7 +55,8 @@ kda_status check_rows(const kda_cache4* c, int64_t tokens, kda_dtype io, const v
     kda_status st = check_cache(c);
     if (st != KDA_OK) return st;
     if (tokens < 0 || !ok_io(io)) return KDA_ERR_INVALID_ARGUMENT;
-    if (mul_sat(tokens, c->heads) > INT32_MAX) return KDA_ERR_UNSUPPORTED;   // rows are 32-bit in the kernels
+    // rows are 32-bit in the kernels, and so are the threads of a launch: d / 8 a row, whole workgroups
+    if (tokens > INT32_MAX || mul_sat(mul_sat(tokens + 31, c->heads), c->d / 8) > UINT32_MAX) return KDA_ERR_UNSUPPORTED;
     const bool any = tokens > 0;
     if (!ok_ptr(k, any) || !ok_ptr(v, any) || !ok_elem(slot_map, any, 8)) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
@@ -79,11 +80,14 @@ Cache4AttentionArgs attention_args(const kda_cache4* c, const kda_cache4_attenti
     a.c = cache_args(c);
     a.n_seq = p->n_seq; a.tokens = p->tokens; a.heads = p->heads; a.group = p->heads / c->heads;
     a.max_pages = c->pages > 0 ? p->max_pages : 0;   // a cache without pages counts no tokens
-     a.max_q = p->max_q; a.max_len = p->max_len; a.scale = p->scale;
+    a.max_q = p->max_q; a.max_len = p->max_len; a.scale = p->scale;
     return a;
 }
 
 bool no_rows(const kda_cache4_attention_problem* p) { return p->n_seq == 0 || p->tokens == 0; }
+bool fits(const kda_cache4* c, const kda_cache4_attention_problem* p) {
+    return no_rows(p) || cache4_attention_fits(p->io_dtype == KDA_BF16, attention_args(c, p));
+}
 
 kda_status check_recurrence(const kda_recurrence_problem* p) {
     if (!p || p->batch < 0 || p->seqlen < 0 || p->width <= 0 || p->n_seq < -1 || !ok_io(p->io_dtype))
@@ -91,11 +95,12 @@ kda_status check_recurrence(const kda_recurrence_problem* p) {
     if (!(p->log_alpha_min < 0.0f)) return KDA_ERR_INVALID_ARGUMENT;
     const bool packed = p->n_seq >= 0;
     if (packed && p->batch != 1) return KDA_ERR_INVALID_ARGUMENT;
-    // token indices are 32-bit, and so are grids; elements are 64-bit
+    // token indices are 32-bit, and so are the threads of a launch; elements are 64-bit
     if (p->seqlen > (1 << 30) || p->width > (1 << 30) || p->batch > (1 << 24) || p->n_seq > (1 << 24) ||
         mul_sat(mul_sat(p->batch, p->seqlen), p->width) > ((int64_t)1 << 40) ||
         mul_sat(packed ? p->n_seq : p->batch, p->width) > ((int64_t)1 << 38) ||
-        mul_sat(mul_sat(p->batch, p->seqlen / 64 + 1), p->width / 64 + 1) > INT32_MAX)
+        // threads of a launch: 1024 for 128 tokens x 128 channels
+        mul_sat(mul_sat(p->batch, (p->seqlen + 127) / 128), (p->width + 127) / 128) > UINT32_MAX / 1024)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
@@ -186,7 +191,7 @@ kda_status kda_cache4_read(const kda_cache4* c, int64_t tokens, kda_dtype io_dty
 }
 
 size_t kda_cache4_attention_workspace_size(const kda_cache4* c, const kda_cache4_attention_problem* p) {
-    if (check_attention(c, p) != KDA_OK || no_rows(p)) return 0;
+    if (check_attention(c, p) != KDA_OK || no_rows(p) || !fits(c, p)) return 0;
     return cache4_attention_workspace_bytes(p->io_dtype == KDA_BF16, c->d, attention_args(c, p));
 }
 
@@ -196,6 +201,7 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
     kda_status st = check_attention(c, p);
     if (st != KDA_OK) return st;
     if (!cu_seqlens && p->tokens != p->n_seq) return KDA_ERR_INVALID_ARGUMENT;
+    if (!fits(c, p)) return KDA_ERR_UNSUPPORTED;
     if (no_rows(p)) return KDA_OK;
     const size_t need = kda_cache4_attention_workspace_size(c, p);
     if (!ok_ptr(q, true) || !ok_elem(block_table, p->max_pages > 0, 4) || !ok_elem(total_lens, true, 4) ||
@@ -203,6 +209,7 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
         !ok_ptr(workspace, need > 0))
         return KDA_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    if (out == q) return KDA_ERR_INVALID_ARGUMENT;       // several workgroups read a row of q
     if ((st = device_ready()) != KDA_OK) return st;
     Cache4AttentionArgs a = attention_args(c, p);
     a.q = q; a.g = g; a.out = out; a.block_table = block_table; a.total_lens = total_lens; a.cu_seqlens = cu_seqlens;
@@ -259,7 +266,7 @@ kda_status kda_recurrence_backward(const kda_recurrence_problem* p, const void* 
 kda_status kda_recurrence_step(int64_t N, int64_t width, kda_dtype io_dtype, float log_alpha_min, const void* x,
                                const float* log_alpha, const void* g, float* state, void* out, void* stream) {
     if (N < 0 || width <= 0 || !ok_io(io_dtype) || !(log_alpha_min < 0.0f)) return KDA_ERR_INVALID_ARGUMENT;
-    if (mul_sat(N, width) > ((int64_t)1 << 38)) return KDA_ERR_UNSUPPORTED;
+    if (mul_sat(N, width) > ((int64_t)1 << 33)) return KDA_ERR_UNSUPPORTED;      // threads of a launch, four elements each
     const bool any = N > 0;
     if (!ok_ptr(x, any) || !ok_ptr(log_alpha, any) || !ok_opt_ptr(g) || !ok_ptr(state, any) || !ok_ptr(out, any))
         return KDA_ERR_INVALID_ARGUMENT;

@@ -9,6 +9,9 @@
  * an asynchronous call on `stream`, memory owned by the caller, nothing
  * launched after a refused argument, nothing on the stream but kernel
  * launches (so every call can be captured into a HIP graph and replayed).
+ * Outputs may not overlap each other or the inputs except where a call says
+ * so, and a workspace serves one call at a time.  A launch holds fewer than
+ * 2^32 threads; a problem that takes more is KDA_ERR_UNSUPPORTED.
  * What lies in device memory is not checked by the host; where a value there
  * is an index (lengths, offsets, pages, slots), the kernels bound it, so that
  * no value makes an access leave the arrays.
@@ -47,8 +50,7 @@ extern "C" {
  *     more than n_free means that the list was too short.
  * The list is read, not changed: the caller drops its first pages_taken
  * entries.  page_size is a power of two, 16 to 256; n_req <= 8192, and
- * tokens, n_free and n_req * max_pages <= INT32_MAX (more: KDA_ERR_UNSUPPORTED).  The outputs may not overlap
- * each other or the inputs. */
+ * tokens, n_free and n_req * max_pages <= INT32_MAX (more: KDA_ERR_UNSUPPORTED). */
 kda_status kda_plan_requests(int64_t n_req, int64_t tokens, int32_t page_size, int32_t max_pages,
                              const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
                              int64_t n_free, const int32_t* free_pages, int32_t* cu_seqlens, int32_t* total_lens,
@@ -143,8 +145,7 @@ size_t kda_recurrence_backward_workspace_size(const kda_recurrence_problem* p);
 /*   x, g, out: [batch, seqlen, width] io_dtype; log_alpha: the same, fp32;
  *   state_in, state_out: [batch or n_seq, width] fp32, either may be NULL and
  *   they may be one array; cu_seqlens: NULL where p->n_seq is -1.  Tokens of
- *   no sequence are not written; an empty sequence passes its state through.
- *   A workspace serves one call at a time. */
+ *   no sequence are not written; an empty sequence passes its state through. */
 kda_status kda_recurrence_prefill(const kda_recurrence_problem* p, const void* x, const float* log_alpha,
                                   const void* g, const float* state_in, const int32_t* cu_seqlens, void* out,
                                   float* state_out, void* workspace, size_t workspace_bytes, void* stream);
@@ -161,8 +162,8 @@ kda_status kda_recurrence_prefill_for_backward(const kda_recurrence_problem* p, 
  * too: not the array that state_out went to).  Where log_alpha <=
  * log_alpha_min, or is NaN, dlog_alpha is 0.  d_out, d_state may be NULL
  * (zero); dg is written where g is given and may be NULL otherwise;
- * d_state_in may be NULL.  Outputs are overwritten and may not overlap each
- * other or the inputs; tokens of no sequence are not written.  The workspace can serve further backward calls, one at a time. */
+ * d_state_in may be NULL.  Outputs are overwritten; tokens of no sequence are
+ * not written.  The workspace can serve further backward calls. */
 kda_status kda_recurrence_backward(const kda_recurrence_problem* p, const void* x, const float* log_alpha,
                                    const void* g, const float* state_in, const int32_t* cu_seqlens,
                                    const void* d_out, const float* d_state, void* dx, float* dlog_alpha, void* dg,

@@ -171,6 +171,20 @@ def test_recurrence_backward_and_step_refusals(L):
     assert step(N=0, x=None, la=None, s=None, o=None) == 0
 
 
+def test_launches_of_too_many_threads_are_refused(L):
+    """The limits lie where a launch of 32-bit threads ends, and no lower."""
+    rows = lambda tokens, **kw: L.kda_cache4_append(cache(heads=8, d=128, **kw), tokens, kda.KDA_BF16, FAKE, FAKE, None, None)
+    assert rows(2 ** 25 - 32) == BAD and rows(2 ** 25) == UNSUPPORTED          # no slots, too many rows
+    call = lambda **kw: L.kda_cache4_attention(cache(), problem(**kw), None, FAKE, FAKE, None, None, FAKE, None, 0, None)
+    assert call(n_seq=2 ** 22, tokens=2 ** 22) == BAD and call(n_seq=2 ** 23, tokens=2 ** 23) == UNSUPPORTED
+    fwd = lambda **kw: L.kda_recurrence_prefill(rec(**kw), None, FAKE, None, None, None, FAKE, None, FAKE, 1 << 50, None)
+    assert fwd(batch=2 ** 22 - 1, seqlen=100, width=100) == BAD and fwd(batch=2 ** 22, seqlen=100, width=100) == UNSUPPORTED
+    step = lambda n: L.kda_recurrence_step(n, 1, kda.KDA_F32, -0.5, None, FAKE, None, FAKE, FAKE, None)
+    assert step(2 ** 33) == BAD and step(2 ** 33 + 1) == UNSUPPORTED
+    # the attention does not write over its queries
+    assert L.kda_cache4_attention(cache(), problem(), FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 1 << 40, None) == BAD
+
+
 def test_binding_refusals():
     """What the Python calls refuse, on tensors that never reach a device."""
     torch = pytest.importorskip("torch")
