@@ -21,13 +21,14 @@
 // exact too and the probabilities round once to bf16; fp32 queries and
 // probabilities are taken in three bf16 parts, which together hold 24 bits.
 //
-// Few rows (decode; at most kSplitMaxRows a sequence and head): the four waves
+// Few rows (decode; at most split_max_rows of a sequence and head): the four waves
 // of a workgroup take turns at the 32-token tiles, each through LDS of its own,
 // and join their results.  Bound by the cache's bytes and by what a block costs
 // at its ends: 256 ragged contexts of up to 8192 tokens, 32 heads over 8 of
-// 128, take 82 us + 5 us for joining the parts where the bytes alone take 66
-// (5 us go into dealing out the work, about 20 into the ends of the blocks).
-// Loaded in the order of the operands, without LDS, it took 92.
+// 128, take 74 us + 5 us for joining the parts where the bytes alone take 66 at
+// the rate of a copy (5 us go into dealing out the work); 64 contexts of 32768
+// take 396 us, 5.8 TB/s.  Loaded in the order of the operands, without LDS, the
+// first took 92.
 // Many rows (prompts): each wave has rows of its own, 64 tokens at a time are
 // converted once for all four waves, and operands come from LDS.  Bound by the
 // vector unit's work on the scores beside the products: 4 prompts of up to 1000
@@ -60,9 +61,9 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;         // tokens that are dealt out at once
-// Units that a block counts for beside its own, as beginning one costs: 256
-// ragged contexts took 98 us with 2, 93 with 3, 91 with 5, 102 with 8 and 120
-// with none; prompts 197, 207, 201 and 213.
+// Units that a block counts for beside its own, as beginning one costs: the
+// 256 ragged contexts above take 83 us with 2, 77 with 3, 82 with 6, the
+// prompts 195, 201 and 204.
 constexpr int kBlockCost = 4;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
 
@@ -463,14 +464,18 @@ __device__ __forceinline__ void values_of(const Tile<D>& x, int t0, int end, int
 // Bytes of two tiles of 64 tokens as operands.
 __host__ __device__ constexpr int shared_tiles(int d) { return 2 * 64 * d * 2 * 2; }
 
-// Waves per SIMD that registers are kept for: what fits without spilling.
-template <typename E, int D, int R> constexpr int waves_of() {
-    if (sizeof(E) == 2) return R == 1 ? 3 : 2;
-    return R == 2 && D == 128 ? 1 : 2;
+// Waves per SIMD that registers are kept for, and so workgroups per CU that work
+// is dealt to: what fits without spilling.  (With 3 instead of 2 in bf16 and
+// D = 128, R = 1, 56 bytes of spills: 64 contexts of 32768 tokens took 417 us
+// instead of 396, of 2048 36 instead of 30; with 2 instead of 3 and D = 64, 256
+// contexts of 4096 take 147 instead of 134.)
+constexpr int waves_of(bool bf16, int d, int r) {
+    if (bf16) return r == 1 && d == 64 ? 3 : 2;
+    return r == 2 && d == 128 ? 1 : 2;
 }
 
 template <typename E, int D, int R, bool SPLITW>
-__global__ __launch_bounds__(kWaves * 64, (waves_of<E, D, R>())) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
+__global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
     constexpr int PARTS = sizeof(E) == 2 ? 1 : 3;
     constexpr int KS = D / 32;          // MFMA steps over the channels
     constexpr int VJ = D / 16;          // MFMAs of a value tile
@@ -1085,7 +1090,11 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
     }
 }
 
-constexpr int kSplitMaxRows = 32;      // rows that the waves of a workgroup share
+// Rows of a sequence and head up to which the waves of a workgroup share those
+// of a block, of 16 or 32 rows.  64 sequences of 4096 tokens, 8 heads of 128: in
+// bf16 32 rows take 78 us this way and 187 as many rows, 64 take 134 and 204, 96
+// take 184 and 208; in fp32 32 take 143 and 218, 48 take 264 and 222.
+constexpr int split_max_rows(bool bf16) { return bf16 ? 96 : 32; }
 // bf16 rows of a wave in the many-rows form; fp32 takes three times the
 // registers for its queries
 constexpr int rows_r(bool bf16) { return bf16 ? 2 : 1; }
@@ -1096,10 +1105,10 @@ struct Plan {
     int r;
 };
 
-Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
+Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a) {
     Plan p = {};
     const int64_t rows = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
-    p.splitw = rows <= kSplitMaxRows;
+    p.splitw = rows <= split_max_rows(bf16);
     p.r = p.splitw ? (rows <= 16 ? 1 : 2) : rows_r(bf16);
     p.l.rows = p.splitw ? 16 * p.r : 16 * p.r * kWaves;
     p.l.per_seq = (a.group + p.l.rows - 1) / p.l.rows;
@@ -1112,9 +1121,9 @@ Plan plan_of(bool bf16, const Cache4AttentionArgs& a) {
     const int64_t cap = (int64_t)a.max_pages << a.c.page_shift;
     const int64_t len = a.max_len < cap ? a.max_len : cap;
     const int64_t units = (int64_t)p.l.slots * ((len + kUnit - 1) / kUnit + kBlockCost);
-    // (3 a CU with one row tile in bf16, else 2; with 256 or 1024 instead of
-    // 512 the prompts above take 319 and 222 us instead of 195)
-    int64_t groups = ((p.splitw && p.r == 1 && bf16 ? 768 : 512) + a.c.heads - 1) / a.c.heads;
+    // (twice as many groups in the many-rows form: 704 us instead of 686 for
+    // 4 x 1000 tokens at the end of 8192)
+    int64_t groups = (256 * (p.splitw && waves_of(bf16, d, p.r) == 3 ? 3 : 2) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
     const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= INT32_MAX;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
@@ -1139,7 +1148,7 @@ hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, const
 template <typename E, int D>
 hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_t s) {
     constexpr bool bf16 = sizeof(E) == 2;
-    const Plan p = plan_of(bf16, a);
+    const Plan p = plan_of(bf16, D, a);
     Parts parts = {};
     if (p.l.groups > 0) {
         parts.cut = reinterpret_cast<Cut*>(ws);
@@ -1151,10 +1160,12 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
     else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, parts, s);
     else e = launch_attention_r<E, D, 2, true>(a, p, parts, s);
     if (e != hipSuccess || p.l.groups < 2) return e;
-    // Where a block has many parts, four waves share those of a row.
+    // Where a block has many parts, four waves share those of a row: 37 parts
+    // of a row take 11.7 us instead of 14.2 (with the first kernel), 64 take
+    // 35 instead of 48, but 6 take 38 instead of 36 and 8 take 30 instead of 24.
     const int64_t most = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
     const int rows = (int)(most < p.l.rows ? most : p.l.rows);
-    const bool wide = p.l.slots * 4 <= p.l.groups;
+    const bool wide = p.l.slots * 16 <= p.l.groups;
     const int chunks = wide ? rows : (rows + kWaves - 1) / kWaves;
     const dim3 grid((unsigned)((p.l.groups - 1) * a.c.heads * chunks));
     if (wide) hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
@@ -1164,13 +1175,13 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
 
 }  // namespace
 
-bool cache4_attention_fits(bool bf16, const Cache4AttentionArgs& a) {
-    const Plan p = plan_of(bf16, a);
+bool cache4_attention_fits(bool bf16, int d, const Cache4AttentionArgs& a) {
+    const Plan p = plan_of(bf16, d, a);
     return p.l.groups > 0 || (int64_t)p.l.slots * a.c.heads <= UINT32_MAX / (kWaves * 64);
 }
 
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
-    const Plan p = plan_of(bf16, a);
+    const Plan p = plan_of(bf16, d, a);
     if (p.l.groups == 0) return 0;
     return cut_bytes(p) + part_places(a, p) * (size_t)(d + 2) * sizeof(float);
 }

@@ -86,7 +86,7 @@ Cache4AttentionArgs attention_args(const kda_cache4* c, const kda_cache4_attenti
 
 bool no_rows(const kda_cache4_attention_problem* p) { return p->n_seq == 0 || p->tokens == 0; }
 bool fits(const kda_cache4* c, const kda_cache4_attention_problem* p) {
-    return no_rows(p) || cache4_attention_fits(p->io_dtype == KDA_BF16, attention_args(c, p));
+    return no_rows(p) || cache4_attention_fits(p->io_dtype == KDA_BF16, c->d, attention_args(c, p));
 }
 
 kda_status check_recurrence(const kda_recurrence_problem* p) {

@@ -97,7 +97,7 @@ hipError_t launch_plan(const PlanArgs& a, hipStream_t s);
 hipError_t launch_cache4_append(bool bf16, int d, const Cache4RowsArgs& a, hipStream_t s);
 hipError_t launch_cache4_read(bool bf16, int d, const Cache4RowsArgs& a, hipStream_t s);
 // Whether a launch can have as many threads as the problem takes.
-bool cache4_attention_fits(bool bf16, const Cache4AttentionArgs& a);
+bool cache4_attention_fits(bool bf16, int d, const Cache4AttentionArgs& a);
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a);
 hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s);
 // backward: the workspace of the training pair; else of the prefill alone

@@ -102,6 +102,16 @@ def test_many_queries(total, new, heads, kv, d, page, io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv,d", [(8, 2, 128), (8, 1, 64), (3, 1, 128)])
+@pytest.mark.parametrize("new", [4, 5, 8, 9, 12, 13, 24, 25])
+def test_few_queries(new, heads, kv, d, io):
+    """Around the sizes of a row block and the rule that chooses how its rows are shared."""
+    total, many = [150, new, 1100, 40], [new, new, new, 1]
+    c, q, g, table, cu = build(total, many, heads, kv, d, 32, io)
+    check(c, q, g, table, total, cu, io, max_q=new, max_len=max(total))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_rows_that_see_nothing_and_rows_of_no_sequence(io):
     total, new = [4, 0, 20, 3], [6, 2, 0, 1]              # more queries than tokens: the first see nothing
     c, q, g, table, cu = build(total, new, 8, 2, 128, 16, io)
