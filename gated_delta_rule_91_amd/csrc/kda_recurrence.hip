@@ -8,10 +8,14 @@
 //   dx_t = dh_t,  dlog_alpha_t = dh_t e^lambda_t h_(t-1)    (0 where the floor binds)
 //   dg_t = d_out_t h_t sigmoid'(g_t),  d_state_in = e^lambda_0 dh_0
 //
-// Both directions are bound by HBM (10 bytes an element forward, 20 in the
+// Both directions are bound by HBM (10 bytes an element forward, 18 in the
 // training pass's backward, with a gate in bf16), so each reads its inputs
 // once: a workgroup holds a tile of 128 or 64 tokens x 128 channels in
-// registers while the state that enters it is found.
+// registers while the state that enters it is found.  65536 tokens of 4096
+// channels take 507 us (5.3 TB/s); 4 x 4096 tokens of 2048 84 us, backward 140
+// (4.0 and 4.3 TB/s); 60000 of 256, where the chain of tiles bounds it, 72 and
+// 121.  Tiles of 64 tokens forward instead of 128: 608 us for the first instead
+// of 541 at the time, 100 instead of 91 for the second.
 //  * A wave runs its stretch of the tile from nothing: (A, H), the product of
 //    its decays and the state it ends with.  A stretch is the map
 //    h -> A h + H; maps are joined through LDS.
@@ -44,7 +48,10 @@ namespace {
 
 // Tokens that a workgroup holds, and that its waves share.
 constexpr int kTile = 128, kBackTile = 64;
-constexpr int kWindow = 8;        // tiles that a look-back reads at once
+// Tiles that a look-back reads at once.  With 4, 60000 tokens of 256 channels
+// take 101 us instead of 72 (backward 188 instead of 121), with 16 56 (89), but
+// the 64K tokens above 549 instead of 507, for its registers.
+constexpr int kWindow = 8;
 // Polls after which a wait gives up with NaN: a tenth of a second, where a tile takes
 // microseconds.  Only a workspace that another call is using can get there.
 constexpr int kMaxPolls = 1 << 17;
@@ -192,39 +199,30 @@ __device__ __forceinline__ void publish(uint64_t* p, uint64_t w) {
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The state that leaves tile i - 1 in the order of the scan, per channel:
-// words + k * stride is channel 0's word of tile i - 1 - k, k < i.
-template <int VEC>
-__device__ __forceinline__ void look_back(const uint64_t* words, int64_t stride, int64_t i, float (&h)[VEC]) {
+// The state that leaves tile i - 1 in the order of the scan, for a lane's
+// channel: words + k * stride is its word of tile i - 1 - k, k < i.
+__device__ __forceinline__ float look_back(const uint64_t* words, int64_t stride, int64_t i) {
     const int64_t most = i < kWindow ? i : kWindow;
-    bool have[VEC];
+    float h = 0.f;
+    bool have = false;
     for (int polls = 0; polls < kMaxPolls; ++polls) {
-        uint64_t w[kWindow][VEC];
+        uint64_t w[kWindow];
 #pragma unroll
         for (int k = 0; k < kWindow; ++k)
+            w[k] = k < most ? __hip_atomic_load(const_cast<uint64_t*>(words) + k * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+        have = false;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                w[k][v] = k < most ? __hip_atomic_load(const_cast<uint64_t*>(words) + k * stride + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-        bool all = true;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            have[v] = false;
-#pragma unroll
-            for (int k = kWindow - 1; k >= 0; --k) {       // from the earliest tile on
-                const uint32_t high = (uint32_t)(w[k][v] >> 32);
-                const float H = __uint_as_float((uint32_t)w[k][v]);
-                const bool final = high == kFinal;
-                h[v] = final ? H : fmaf(__uint_as_float(high & 0x7fffffffu), h[v], H);
-                have[v] = final || (have[v] && high != 0);
-            }
-            all = all && have[v];
+        for (int k = kWindow - 1; k >= 0; --k) {           // from the earliest tile on
+            const uint32_t high = (uint32_t)(w[k] >> 32);
+            const float H = __uint_as_float((uint32_t)w[k]);
+            const bool final = high == kFinal;
+            h = final ? H : fmaf(__uint_as_float(high & 0x7fffffffu), h, H);
+            have = final || (have && high != 0);
         }
-        if (__all(all)) return;
+        if (__all(have)) return h;
         __builtin_amdgcn_s_sleep(1);
     }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-        if (!have[v]) h[v] = __uint_as_float(0x7fc00000u);
+    return have ? h : __uint_as_float(0x7fc00000u);
 }
 
 // Where a workgroup works: a tile taken off the counter where tiles wait for
@@ -315,37 +313,28 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_kernel(Recurrenc
     if (lane == 0) sCut[wave] = cut;
     __syncthreads();
 
-    if (wave == 0) {
-        // the tile's map, and the state that enters it
-        float A[VEC], H[VEC], hin[VEC];
+    // The tile's map, and the state that enters it: wave v has channel c + v.
+    // (One wave with both took twice the registers beside its tokens: the 64K
+    // tokens above 541 us instead of 507.)
+    if (wave < VEC) {
+        const int at = lane * VEC + wave;
+        float A = 1.f, H = 0.f, hin = 0.f;
         bool constant = false;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; H[v] = 0.f; hin[v] = 0.f; }
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const bool cw = sCut[w] != 0;
             constant = constant || cw;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float Aw = sA[w][lane * VEC + v], Hw = sH[w][lane * VEC + v];
-                H[v] = cw ? Hw : fmaf(Aw, H[v], Hw);
-                A[v] *= Aw;
-            }
+            H = cw ? sH[w][at] : fmaf(sA[w][at], H, sH[w][at]);
+            A *= sA[w][at];
         }
         if (grid.tiles > 1) {
-            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
-            if (ch.in && i + 1 < grid.tiles) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, H[v]) : map_word(A[v], H[v]));
-            }
-            if (i > 0) look_back<VEC>(mine - a.D, -a.D, i, hin);
-            if (ch.in && !constant && i + 1 < grid.tiles) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], hin[v], H[v])));
-            }
+            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c + wave;
+            const bool tells = ch.in && i + 1 < grid.tiles;
+            if (tells) publish(mine, constant ? word(kFinal, H) : map_word(A, H));
+            if (i > 0) hin = look_back(mine - a.D, -a.D, i);
+            if (tells && !constant) publish(mine, word(kFinal, fmaf(A, hin, H)));
         }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sIn[lane * VEC + v] = hin[v];
+        sIn[at] = hin;
     }
     __syncthreads();
 
@@ -501,38 +490,27 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_backward_kernel(
     if (lane == 0) { sFirst[wave] = first; sLast[wave] = last; }
     __syncthreads();
 
-    if (wave == 0) {
-        // the tile's map of the gradient, and the gradient that enters it from behind
-        float A[VEC], C[VEC], ein[VEC];
+    // the tile's map of the gradient, and the gradient that enters it from behind
+    if (wave < VEC) {
+        const int at = lane * VEC + wave;
+        float A = 1.f, C = 0.f, ein = 0.f;
         bool constant = false;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; C[v] = 0.f; ein[v] = 0.f; }
 #pragma unroll
         for (int w = WAVES - 1; w >= 0; --w) {
             const bool cw = sLast[w] != 0;
             constant = constant || cw;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float Aw = sA[w][lane * VEC + v], Cw = sC[w][lane * VEC + v];
-                C[v] = cw ? Cw : fmaf(Aw, C[v], Cw);
-                A[v] *= Aw;
-            }
+            C = cw ? sC[w][at] : fmaf(sA[w][at], C, sC[w][at]);
+            A *= sA[w][at];
         }
         if (grid.tiles > 1) {
-            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c;
+            uint64_t* mine = words + (row * grid.tiles + i) * a.D + c + wave;
             const int64_t behind = grid.tiles - 1 - i;
-            if (ch.in && i > 0) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) publish(mine + v, constant ? word(kFinal, C[v]) : map_word(A[v], C[v]));
-            }
-            if (behind > 0) look_back<VEC>(mine + a.D, a.D, behind, ein);
-            if (ch.in && !constant && i > 0) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) publish(mine + v, word(kFinal, fmaf(A[v], ein[v], C[v])));
-            }
+            const bool tells = ch.in && i > 0;
+            if (tells) publish(mine, constant ? word(kFinal, C) : map_word(A, C));
+            if (behind > 0) ein = look_back(mine + a.D, a.D, behind);
+            if (tells && !constant) publish(mine, word(kFinal, fmaf(A, ein, C)));
         }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) sIn[lane * VEC + v] = ein[v];
+        sIn[at] = ein;
     }
     __syncthreads();
     if (!ch.in) return;
@@ -657,8 +635,8 @@ __device__ __forceinline__ void step_elements(const RecurrenceStepArgs& a, int64
     put<E, N>(reinterpret_cast<E*>(a.out) + i, y);
 }
 
-// Bound by HBM, by latency when small: four elements a thread, the last ones
-// one by one.
+// Bound by HBM, by latency when small (256 x 4096 in bf16 with a gate, 18 MB:
+// 5 us): four elements a thread, the last ones one by one.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void kda_recurrence_step_kernel(RecurrenceStepArgs a) {
     const int64_t i = 4 * ((int64_t)blockIdx.x * kThreads + threadIdx.x);
@@ -677,7 +655,8 @@ size_t words_bytes(int64_t B, int64_t T, int64_t D, int tile) {
 }
 constexpr size_t kCounterBytes = 256;
 
-// Tokens of a wave: 16 in bf16, 8 in fp32, whose registers hold half as many.
+// Tokens of a wave: 16 in bf16, 8 in fp32, whose registers hold half as many
+// (16 in fp32 spill with a gate; without one 34 us instead of 36 for 16384 x 515).
 template <typename E> constexpr int kForwardWaves = sizeof(E) == 2 ? 8 : 16;
 constexpr int kBackwardWaves = 8;
 
