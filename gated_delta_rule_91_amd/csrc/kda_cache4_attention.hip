@@ -32,7 +32,7 @@
 // Many rows (prompts): each wave has rows of its own, 64 tokens at a time are
 // converted once for all four waves, and operands come from LDS.  Bound by the
 // vector unit's work on the scores beside the products: 4 prompts of up to 1000
-// tokens at the end of contexts of up to 8192, the same heads, take 195 us + 20
+// tokens at the end of contexts of up to 8192, the same heads, take 195 us + 18
 // us for the parts, the matrix units busy a quarter of it.  16 rows a wave
 // instead of 32 took 320 us, 48 or 64 (one workgroup a CU) 306 and 289.
 // Sequences are ragged and a query's tokens grow along a prompt, so work is
@@ -73,20 +73,22 @@ struct Layout {
     int slots;       // upper bound of row blocks over all sequences
     int per_seq;     // without offsets: row blocks of each sequence
     int groups;      // workgroups of a key/value head that units are dealt to; 0: a block each
+    bool by_slot;    // where a block's cut is found: at its slot, else at the workgroup it begins in
 };
 
 // Workgroup w has two parts at most, 2 w of a block that began before it and
 // 2 w + 1 of one that begins in it and goes on.  Part i of row r of a block and
 // key/value head h is at (i * heads + h) * rows + r.  The second kernel finds
-// by cut[w] the block that begins in w and goes on.
+// the blocks that several workgroups have by their cuts, of which there are
+// as many as slots or workgroups, whichever are fewer.
 struct Cut {
     int row0;        // first row of q of its sequence
     int n_rows;      // (query, head) rows of its sequence, 0: there is no such block
     int begin;       // its first one of them
-    int last;        // last workgroup that has a part of it
+    int from, last;  // first and last workgroup that have a part of it
 };
 struct Parts {
-    Cut* cut;        // [groups]
+    Cut* cut;        // [slots or groups]
     float* sums;     // maximum and sum
     float* o;        // D channels
 };
@@ -496,7 +498,12 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
     if (l.groups > 0) {
         const int all = deal_out(a, l, before);
         each = max((all + l.groups - 1) / l.groups, 1);
-        if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{0, 0, 0, group};
+        if (kvh == 0 && !l.by_slot) {
+            if (threadIdx.x == 0) parts.cut[group] = Cut{};
+        } else if (kvh == 0 && group == 0) {
+            for (int i = threadIdx.x; i < l.slots; i += kWaves * 64)
+                if (before[i] == before[i + 1]) parts.cut[i] = Cut{};      // the others have a workgroup that writes them
+        }
         at = (int)min((int64_t)group * each, (int64_t)all);
         stop = min(at + each, all);
         int lo = 0, hi = l.slots;  // the last block that begins at or before `at`: empty ones lie before it
@@ -521,12 +528,10 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
             if (to <= from) continue;       // no rows, or the next workgroup has them all
             lo = (from - p0) * kUnit;
             lim = min(b.total, (to - p0) * kUnit);
-            if (from > p0) {
-                part = 2 * group;
-            } else if (to < p1) {
-                part = 2 * group + 1;
-                if (kvh == 0 && threadIdx.x == 0) parts.cut[group] = Cut{b.row0, n_rows, b.begin, (p1 - 1) / each};
-            }
+            const bool begins = from == p0, goes_on = to < p1;
+            if (!begins || goes_on) part = 2 * group + (begins ? 1 : 0);
+            if (begins && (goes_on || l.by_slot) && kvh == 0 && threadIdx.x == 0)
+                parts.cut[l.by_slot ? slot : group] = goes_on ? Cut{b.row0, n_rows, b.begin, group, (p1 - 1) / each} : Cut{};
         } else {
             at = stop;
             if (!b.any) continue;
@@ -1014,18 +1019,21 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
 // the parts of a row, and their sums are joined through LDS in the order of
 // the waves.
 template <typename E, int D, int WAVES>
-__global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts, int chunks) {
+__global__ __launch_bounds__((WAVES > kWaves ? WAVES : kWaves) * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts, int chunks) {
     constexpr int PER = D / 64;
-    __shared__ __align__(16) float acc[kWaves][D];
+    constexpr int ROWS = WAVES > kWaves ? 1 : kWaves / WAVES;      // rows of a workgroup at a time
+    __shared__ __align__(16) float acc[ROWS * WAVES][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % WAVES;
-    // chunks of rows, key/value heads, workgroups of the first kernel
-    const int chunk = (int)(blockIdx.x % chunks), kvh = (int)(blockIdx.x / chunks % a.c.heads), w0 = (int)(blockIdx.x / chunks / a.c.heads);
-    const Cut cut = parts.cut[w0];
+    // chunks of rows, key/value heads, cuts
+    const int chunk = (int)(blockIdx.x % chunks), kvh = (int)(blockIdx.x / chunks % a.c.heads);
+    const Cut cut = parts.cut[blockIdx.x / chunks / a.c.heads];
     // bounded, so that a workspace that another call writes meanwhile gives
     // wrong values but no access outside the arrays
-    const int count = min(cut.last, l.groups - 1) - w0 + 1, rows = min(l.rows, cut.n_rows - cut.begin);
-    if (cut.n_rows <= 0 || cut.begin < 0 || count < 2) return;
-    for (int r = chunk * (kWaves / WAVES) + wave / WAVES; r < rows; r += chunks * (kWaves / WAVES)) {
+    const int w0 = cut.from, rows = min(l.rows, cut.n_rows - cut.begin);
+    if (cut.n_rows <= 0 || cut.begin < 0 || w0 < 0 || w0 >= l.groups) return;
+    const int count = min(cut.last, l.groups - 1) - w0 + 1;
+    if (count < 2) return;
+    for (int r = chunk * ROWS + wave / WAVES; r < rows; r += chunks * ROWS) {
         const int64_t stride = 2 * (int64_t)a.c.heads * l.rows;
         const int64_t first = ((int64_t)(2 * w0 + 1) * a.c.heads + kvh) * l.rows + r, rest = first - stride / 2;
         const int64_t at = place_of(a, cut.row0, kvh, cut.begin + r);
@@ -1056,15 +1064,13 @@ __global__ __launch_bounds__(kWaves * 64) void kda_cache4_combine_kernel(Cache4A
             sum += w * ms[1];
             auto weight = [&](int k) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k)); };
             const int most = min(count - i0, 64);
-            int k = turn;
-            if (i0 == 0) {
 #pragma unroll
-                for (int q = 0; q < AHEAD; ++q)
-                    if (turn + q * WAVES < most) o += weight(turn + q * WAVES) * x[q];
-                k += AHEAD * WAVES;
+            for (int q = 0; q < AHEAD; ++q) {
+                const int k = turn + q * WAVES - i0;
+                if (k >= 0 && k < most) o += weight(k) * x[q];
             }
 #pragma unroll 8
-            for (; k < most; k += WAVES) o += weight(k) * part(i0 + k);
+            for (int k = turn + max(AHEAD * WAVES - i0, 0); k < most; k += WAVES) o += weight(k) * part(i0 + k);
         }
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off);
@@ -1099,6 +1105,10 @@ constexpr int split_max_rows(bool bf16) { return bf16 ? 96 : 32; }
 // registers for its queries
 constexpr int rows_r(bool bf16) { return bf16 ? 2 : 1; }
 
+// 4 take 42 us for one head's 50000 tokens instead of 28, 16 take 24 but 22
+// instead of 18 for 2 sequences of 4096 and 32 rows.
+constexpr int kWideWaves = 8;
+
 struct Plan {
     Layout l;
     bool splitw;
@@ -1127,11 +1137,13 @@ Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a) {
     groups = groups < units ? groups : units;
     const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= INT32_MAX;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
+    p.l.by_slot = p.l.slots < p.l.groups;
     return p;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-size_t cut_bytes(const Plan& p) { return round256((size_t)p.l.groups * sizeof(Cut)); }
+int cuts(const Plan& p) { return p.l.by_slot ? p.l.slots : p.l.groups; }
+size_t cut_bytes(const Plan& p) { return round256((size_t)cuts(p) * sizeof(Cut)); }
 size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
     return 2 * (size_t)p.l.groups * (size_t)a.c.heads * (size_t)p.l.rows;
 }
@@ -1160,15 +1172,16 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
     else if (p.r == 1) e = launch_attention_r<E, D, 1, true>(a, p, parts, s);
     else e = launch_attention_r<E, D, 2, true>(a, p, parts, s);
     if (e != hipSuccess || p.l.groups < 2) return e;
-    // Where a block has many parts, four waves share those of a row: 37 parts
-    // of a row take 11.7 us instead of 14.2 (with the first kernel), 64 take
-    // 35 instead of 48, but 6 take 38 instead of 36 and 8 take 30 instead of 24.
+    // Where a block has many parts, kWideWaves waves share those of a row:
+    // both kernels take 10.7 us instead of 13.3 for one of 4097 tokens (37
+    // parts), 16 instead of 18 for 4 of 8192 (16 parts), 28 instead of 112 for
+    // one head's 50000; with 4 parts 33 instead of 23 for 8 of 4096, 32 rows.
     const int64_t most = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
     const int rows = (int)(most < p.l.rows ? most : p.l.rows);
-    const bool wide = p.l.slots * 16 <= p.l.groups;
+    const bool wide = p.l.slots * 8 <= p.l.groups;
     const int chunks = wide ? rows : (rows + kWaves - 1) / kWaves;
-    const dim3 grid((unsigned)((p.l.groups - 1) * a.c.heads * chunks));
-    if (wide) hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWaves>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
+    const dim3 grid((unsigned)(cuts(p) * a.c.heads * chunks));
+    if (wide) hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWideWaves>), grid, dim3(kWideWaves * 64), 0, s, a, p.l, parts, chunks);
     else hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
     return hipGetLastError();
 }

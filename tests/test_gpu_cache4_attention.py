@@ -222,6 +222,21 @@ def test_given_workspace():
         kda.cache4_attention(q.transpose(0, 1).contiguous().transpose(0, 1), c, t, n)      # strides
 
 
+def test_what_a_workspace_held_does_not_count():
+    """Sequences without queries or tokens leave nothing in it."""
+    total, new = [2000, 70, 0, 40, 3000], [1, 0, 2, 9, 0]
+    c, q, g, table, cu = build(total, new, 8, 2, 128, 16, "bf16")
+    t, n, cut = i32(table), i32(total), i32(cu)
+    want = kda.cache4_attention(q, c, t, n, cut, g=g, max_q=9)
+    size = kda.cache4_attention_workspace_size(q, c, t, n, cut, max_q=9)
+    assert size > 0
+    for fill in (0, 1, 127, 255):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+        got = kda.cache4_attention(q, c, t, n, cut, g=g, max_q=9, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_many_blocks_without_dealing_out():
     """More row blocks than prefix sums are kept for: a workgroup each."""
     n = 4200
