@@ -398,7 +398,11 @@ def _recurrence_function():
 
 def recurrence_autograd(x, log_alpha, log_alpha_min: float, g=None, state_in=None, cu_seqlens=None):
     """Differentiable recurrence_prefill: returns (out, final states), and
-    loss.backward() fills the gradients of x, log_alpha, g and state_in."""
+    loss.backward() fills the gradients of x, log_alpha, g and state_in.
+
+    To capture a training pass into a graph, call the pair above, or drop every
+    eager result of the same leaves first: while one lives, PyTorch accumulates
+    their gradients on the stream it was made on, outside the capture."""
     return _recurrence_function().apply(x, log_alpha, g, state_in, float(log_alpha_min), cu_seqlens)
 
 

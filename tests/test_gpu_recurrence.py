@@ -193,6 +193,27 @@ def test_state_in_place():
         assert same is s and torch.equal(s, state) and torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 2, 3, 127])
+def test_narrow_and_long(D, io):
+    """The chain of tiles alone: widths below, at and around a pair of channels."""
+    check(made(2, 1500, D, io), io)
+    cu = [0, 130, 130, 131, 900, 1500]
+    check(made(1, 1500, D, io, n=5), io, cu=cu)
+
+
+def test_same_bits_every_time():
+    i = made(1, 6000, 514, "bf16")
+    first = None
+    for _ in range(6):
+        out, state, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"])
+        r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, g=i["g"], state_in=i["s0"], d_out=i["d_out"], d_state=i["d_state"])
+        torch.cuda.synchronize()
+        now = [out, state] + [r[k] for k in ("dx", "dlog_alpha", "dg", "dstate0")]
+        first = first or now
+        assert all(torch.equal(a, b) for a, b in zip(now, first))
+
+
 @pytest.mark.parametrize("B,T,D", [(64, 40, 129), (3, 700, 129), (2, 300, 257), (5, 130, 127), (4, 200, 3)])
 def test_state_in_place_of_odd_widths(B, T, D):
     """A channel that two lanes share: neither reads a state that the other has written."""
