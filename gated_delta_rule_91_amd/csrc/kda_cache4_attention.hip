@@ -115,41 +115,31 @@ __device__ __forceinline__ void sequence_of(const Cache4AttentionArgs& a, int s,
     b.total = min(total, a.max_pages << a.c.page_shift);
 }
 
-// The sequence that holds row `row` of q, with offsets: the last one that
-// begins at or before it.
-__device__ __forceinline__ int sequence_at(const Cache4AttentionArgs& a, int row) {
+// Row blocks of sequence s with offsets begin at slot floor(cu[s] G / rows) + s,
+// which leaves each its ceil(m G / rows) slots and can be searched: the first
+// term, of an offset.
+__device__ __forceinline__ int first_slot(const Cache4AttentionArgs& a, const Layout& l, int offset) {
+    const int c = min(max(offset, 0), (int)a.tokens);
+    return (int)((uint32_t)c * (uint32_t)a.group / (uint32_t)l.rows);
+}
+
+// The sequence of a slot (n_seq or more: none); cu: the offsets, or a copy of them.
+__device__ __forceinline__ int sequence_at(const Cache4AttentionArgs& a, const Layout& l, const int32_t* cu, int slot) {
+    if (!a.cu_seqlens) return l.per_seq == 1 ? slot : (int)((uint32_t)slot / (uint32_t)l.per_seq);
     int lo = 0, hi = (int)a.n_seq;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu_seqlens[mid] <= row) lo = mid; else hi = mid;
+        if (first_slot(a, l, cu[mid]) + mid <= slot) lo = mid; else hi = mid;
     }
     return lo;
 }
 
-// Row blocks of sequence s with offsets begin at slot floor(cu[s] G / rows) + s,
-// which leaves each its ceil(m G / rows) slots and can be searched.
-__device__ __forceinline__ int first_slot(const Cache4AttentionArgs& a, const Layout& l, int s) {
-    const int c = min(max(a.cu_seqlens[s], 0), (int)a.tokens);
-    return (int)((uint32_t)c * (uint32_t)a.group / (uint32_t)l.rows) + s;
-}
-
-__device__ __forceinline__ Block block_of(const Cache4AttentionArgs& a, const Layout& l, int slot) {
+// The row block of a slot of sequence s.
+__device__ __forceinline__ Block block_of(const Cache4AttentionArgs& a, const Layout& l, int s, int slot) {
     Block b = {};
-    int at = 0;
-    if (a.cu_seqlens) {
-        int lo = 0, hi = (int)a.n_seq;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (first_slot(a, l, mid) <= slot) lo = mid; else hi = mid;
-        }
-        sequence_of(a, lo, b);
-        at = slot - first_slot(a, l, lo);
-    } else {
-        const int s = l.per_seq == 1 ? slot : (int)((uint32_t)slot / (uint32_t)l.per_seq);
-        if (s >= a.n_seq) return b;         // more slots than row blocks
-        sequence_of(a, s, b);
-        at = slot - s * l.per_seq;
-    }
+    if (s >= a.n_seq) return b;             // more slots than row blocks
+    sequence_of(a, s, b);
+    const int at = slot - (a.cu_seqlens ? first_slot(a, l, a.cu_seqlens[s]) + s : s * l.per_seq);
     b.any = at >= 0 && (int64_t)at * l.rows < b.n_rows;
     b.begin = b.any ? at * l.rows : 0;
     return b;
@@ -170,15 +160,22 @@ __device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, int row0, 
 
 // before[i]: units that the row blocks before i count for, i <= slots; returns
 // those of all.  A block with rows has one of its own at least, though its
-// output may be zeros.
-__device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* before) {
+// output may be zeros.  of[i]: the sequence of slot i.  cu: LDS for n_seq + 1
+// offsets, which are searched there.
+__device__ int deal_out(const Cache4AttentionArgs& a, const Layout& l, int32_t* before, uint16_t* of, int32_t* cu) {
     __shared__ int32_t part[kWaves];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    if (a.cu_seqlens) {
+        for (int i = t; i <= (int)a.n_seq; i += kWaves * 64) cu[i] = a.cu_seqlens[i];
+        __syncthreads();
+    }
     int sum = 0;
     for (int base = 0; base < l.slots; base += kWaves * 64) {
         int c = 0;
         if (base + t < l.slots) {
-            const Block b = block_of(a, l, base + t);
+            const int s = sequence_at(a, l, cu, base + t);
+            const Block b = block_of(a, l, s, base + t);
+            of[base + t] = (uint16_t)s;
             if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) + kUnit - 1) / kUnit, 1) + kBlockCost;
         }
         int in = c;
@@ -488,6 +485,8 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
     // many rows: the converted tiles, two of 64 tokens in turn; then the prefix sums
     extern __shared__ __align__(16) char dynamic[];
     int32_t* before = reinterpret_cast<int32_t*>(dynamic + (SPLITW ? 0 : shared_tiles(D)));
+    uint16_t* of = reinterpret_cast<uint16_t*>(before + l.slots + 1);
+    static_assert((SPLITW ? sizeof(so) : shared_tiles(D)) >= (kMaxDealt + 1) * sizeof(int32_t), "the offsets lie there for a while");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, n = lane & 15;
 
     // key/value heads alternate fastest, so workgroups that share keys and
@@ -496,7 +495,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
     int slot = group;
     int at = 0, stop = 1, each = 1;     // this workgroup's units
     if (l.groups > 0) {
-        const int all = deal_out(a, l, before);
+        const int all = deal_out(a, l, before, of, reinterpret_cast<int32_t*>(SPLITW ? reinterpret_cast<char*>(so) : dynamic));
         each = max((all + l.groups - 1) / l.groups, 1);
         if (kvh == 0 && !l.by_slot) {
             if (threadIdx.x == 0) parts.cut[group] = Cut{};
@@ -517,7 +516,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
     }
 
     for (; at < stop; ++slot) {
-        const Block b = block_of(a, l, slot);
+        const Block b = block_of(a, l, l.groups > 0 ? __builtin_amdgcn_readfirstlane(of[slot]) : sequence_at(a, l, a.cu_seqlens, slot), slot);
         const int n_rows = b.n_rows;
         int lo = 0, lim = b.total, part = -1;
         if (l.groups > 0) {
@@ -1151,7 +1150,7 @@ size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
 template <typename E, int D, int R, bool SPLITW>
 hipError_t launch_attention_r(const Cache4AttentionArgs& a, const Plan& p, const Parts& parts, hipStream_t s) {
     const int64_t blocks = (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
-    const unsigned lds = (SPLITW ? 0u : (unsigned)shared_tiles(D)) + (p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * (unsigned)sizeof(int32_t) : 0u);
+    const unsigned lds = (SPLITW ? 0u : (unsigned)shared_tiles(D)) + (p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * (unsigned)(sizeof(int32_t) + sizeof(uint16_t)) : 0u);
     hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW>), dim3((unsigned)blocks), dim3(kWaves * 64), lds, s, a, p.l,
                        parts);
     return hipGetLastError();
