@@ -68,9 +68,10 @@ kda_status check_attention(const kda_cache4* c, const kda_cache4_attention_probl
     if (!p || p->n_seq < 0 || p->tokens < 0 || p->heads <= 0 || p->max_pages < 0 || p->max_q < 1 || p->max_len < 0 ||
         !ok_io(p->io_dtype) || !isfinite(p->scale) || p->heads % c->heads != 0)
         return KDA_ERR_INVALID_ARGUMENT;
-    // row tiles, (row, head) pairs and positions are 32-bit in the kernels
+    // row tiles, (row, head) pairs and positions are 32-bit in the kernels, which step
+    // through the positions in tiles of up to 128 tokens and look one tile ahead
     if (p->n_seq > (1 << 24) || mul_sat(p->tokens, p->heads) > (1 << 30) ||
-        mul_sat(p->n_seq, p->heads) > (1 << 30) || mul_sat(p->max_pages, c->page_size) > INT32_MAX)
+        mul_sat(p->n_seq, p->heads) > (1 << 30) || mul_sat(p->max_pages, c->page_size) > INT32_MAX - 256)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

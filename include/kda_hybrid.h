@@ -104,7 +104,8 @@ size_t kda_cache4_attention_workspace_size(const kda_cache4* c, const kda_cache4
 
 /* Causal grouped-query attention over the cache, for packed queries.
  * Sequence s holds total_lens[s] tokens, in the pages block_table[s, :]
- * (at most max_pages * page_size of them), the newest of which are its
+ * (at most max_pages * page_size of them, itself at most INT32_MAX - 256:
+ * more is KDA_ERR_UNSUPPORTED), the newest of which are its
  * queries: rows [cu_seqlens[s], cu_seqlens[s+1]) of q, or row s alone where
  * cu_seqlens is NULL (one new token each; then tokens == n_seq).  Query i of
  * m sees the tokens at positions <= total_lens[s] - m + i:

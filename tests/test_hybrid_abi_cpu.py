@@ -238,3 +238,19 @@ def test_binding_refusals():
               lambda: kda.plan_requests(z(6, dtype=i32)[::2], z(3, dtype=i32), z(3, 4, dtype=i32), z(5, dtype=i32), 64, 3)):
         with pytest.raises(ValueError, match="contiguous"):
             f()
+
+
+def attention_without_queries(c, p):
+    """What the call says to a problem before it looks at the queries, which are missing."""
+    L = hybrid._hlib()
+    return L.kda_cache4_attention(c, p, None, FAKE, FAKE, FAKE, None, FAKE, FAKE, 1 << 50, None)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_attention_refuses_positions_that_tiles_would_carry_past_32_bits(L, page):
+    """Positions go up in tiles and units of up to 128 tokens: the last one has to stay below 2^31."""
+    room = 2 ** 31 - 1 - 256
+    for most, want in ((room // page, BAD), (room // page + 1, UNSUPPORTED), ((2 ** 31 - 1) // page, UNSUPPORTED)):
+        p = problem(max_pages=most, tokens=9, max_q=9, max_len=2 ** 31)
+        assert attention_without_queries(cache(page_size=page), p) == want, (page, most)
+        assert (L.kda_cache4_attention_workspace_size(cache(page_size=page), p) > 0) == (want == BAD)
