@@ -1189,7 +1189,7 @@ hipError_t launch_attention_t(const Cache4AttentionArgs& a, char* ws, hipStream_
 
 bool cache4_attention_fits(bool bf16, int d, const Cache4AttentionArgs& a) {
     const Plan p = plan_of(bf16, d, a);
-    return p.l.groups > 0 || (int64_t)p.l.slots * a.c.heads <= UINT32_MAX / (kWaves * 64);
+    return (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads <= UINT32_MAX / (kWaves * 64);
 }
 
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {

@@ -254,3 +254,12 @@ def test_attention_refuses_positions_that_tiles_would_carry_past_32_bits(L, page
         p = problem(max_pages=most, tokens=9, max_q=9, max_len=2 ** 31)
         assert attention_without_queries(cache(page_size=page), p) == want, (page, most)
         assert (L.kda_cache4_attention_workspace_size(cache(page_size=page), p) > 0) == (want == BAD)
+
+
+def test_attention_of_too_many_heads_is_refused(L):
+    """A workgroup of 256 threads for every key/value head and share of the work: 2^32 threads are too many."""
+    one = dict(n_seq=1, tokens=1, max_pages=1, max_len=0)
+    for heads, want in ((2 ** 24 - 1, BAD), (2 ** 24, UNSUPPORTED), (2 ** 28, UNSUPPORTED)):
+        c, p = cache(pages=1, page_size=16, d=64, heads=heads), problem(heads=heads, **one)
+        assert attention_without_queries(c, p) == want, heads
+        assert (L.kda_cache4_attention_workspace_size(c, p) > 0) == (want == BAD)
