@@ -66,6 +66,9 @@ constexpr int kUnit = 128;         // tokens that are dealt out at once
 // prompts 195, 201 and 204.
 constexpr int kBlockCost = 4;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
+// Units that can be dealt out: a workgroup's end, at most a unit for each of
+// the workgroups (768) past all of them, is a 32-bit number too.
+constexpr int kMaxUnits = INT32_MAX - 1024;
 
 // How the work is laid out (host and kernels).
 struct Layout {
@@ -1134,7 +1137,7 @@ Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a) {
     // 4 x 1000 tokens at the end of 8192)
     int64_t groups = (256 * (p.splitw && waves_of(bf16, d, p.r) == 3 ? 3 : 2) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
-    const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= INT32_MAX;
+    const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= kMaxUnits;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
     p.l.by_slot = p.l.slots < p.l.groups;
     return p;

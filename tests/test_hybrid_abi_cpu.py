@@ -263,3 +263,11 @@ def test_attention_of_too_many_heads_is_refused(L):
         c, p = cache(pages=1, page_size=16, d=64, heads=heads), problem(heads=heads, **one)
         assert attention_without_queries(c, p) == want, heads
         assert (L.kda_cache4_attention_workspace_size(c, p) > 0) == (want == BAD)
+
+
+def test_attention_units_are_dealt_out_below_2_to_the_31(L):
+    """Sequences whose units come close to 2^31 have a workgroup a block: a share's end is formed in 32 bits."""
+    units = lambda n: (2 ** 31 - 1) // (n + n // 16)          # of n sequences' slots: one page each, 5 for a block
+    size = lambda n, pages: L.kda_cache4_attention_workspace_size(
+        cache(page_size=128, heads=1, d=64), problem(n_seq=n, tokens=n, heads=1, max_pages=pages, max_len=2 ** 40))
+    assert size(128, units(128) - 5 - 16) > 0 and size(128, units(128) - 5) == 0
