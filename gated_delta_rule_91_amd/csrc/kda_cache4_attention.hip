@@ -545,9 +545,9 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
 
         // scores in powers of two, with the sign of the scale in the queries, so
         // that the largest product is the largest score; not 0, which would make
-        // NaN of a masked score's -inf
-        const float to_log2 = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
-        const float sign = a.scale < 0.f ? -1.f : 1.f;
+        // NaN of a masked score's -inf: a scale of 0 is in the queries too
+        const float to_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+        const float sign = a.scale < 0.f ? -1.f : (a.scale == 0.f ? 0.f : 1.f);
 
         // queries: row n of each 16, channels [PER g, PER g + PER)
         bf16x8 q[R][KS][PARTS];

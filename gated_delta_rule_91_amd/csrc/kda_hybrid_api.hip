@@ -2,6 +2,7 @@
 // include/kda_hybrid.h).  As in kda_api.hip every entry point validates its
 // arguments synchronously, before any launch, and launches on the caller's
 // stream; nothing here allocates or keeps state.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -73,6 +74,9 @@ kda_status check_attention(const kda_cache4* c, const kda_cache4_attention_probl
     if (p->n_seq > (1 << 24) || mul_sat(p->tokens, p->heads) > (1 << 30) ||
         mul_sat(p->n_seq, p->heads) > (1 << 30) || mul_sat(p->max_pages, c->page_size) > INT32_MAX - 256)
         return KDA_ERR_UNSUPPORTED;
+    // the kernels multiply scores by scale * log2(e), which has to be a normal number or 0
+    const float factor = fabsf(p->scale) * 1.4426950408889634f;
+    if (p->scale != 0.0f && !(factor >= FLT_MIN && factor <= FLT_MAX)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -96,7 +96,7 @@ typedef struct {
     int64_t max_q;          /* about the most queries of a sequence, >= 1  (these two   */
     int64_t max_len;        /* about the longest sequence, >= 0     steer the split only) */
     kda_dtype io_dtype;     /* dtype of q, g and out                             */
-    float scale;            /* of the scores; finite                             */
+    float scale;            /* of the scores; 0 or 2^-126 to 2^127 in size       */
 } kda_cache4_attention_problem;
 
 /* Bytes of partial results; 0 where the call needs none, or p or c is invalid. */

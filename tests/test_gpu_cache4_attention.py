@@ -268,3 +268,13 @@ def test_offsets_past_32_bits():
     assert ((out.cpu().double()[0] - want).abs() <= tol).all()
     del c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [[2, 1], [200, 30]])
+def test_a_scale_of_zero_weighs_all_alike(new, io):
+    """However large the products are that it takes away."""
+    total = [300, 40]
+    c, q, g, table, cu = build(total, new, 4, 2, 64, 16, io)
+    check(c, (q.float() * 1e35).to(q.dtype), g, table, total, cu, io, scale=0.0, max_q=max(new))
+    check(c, (q.float() * 1e35).to(q.dtype), g, table, total, cu, io, scale=-0.0, max_q=max(new))

@@ -271,3 +271,10 @@ def test_attention_units_are_dealt_out_below_2_to_the_31(L):
     size = lambda n, pages: L.kda_cache4_attention_workspace_size(
         cache(page_size=128, heads=1, d=64), problem(n_seq=n, tokens=n, heads=1, max_pages=pages, max_len=2 ** 40))
     assert size(128, units(128) - 5 - 16) > 0 and size(128, units(128) - 5) == 0
+
+
+def test_attention_refuses_scales_whose_exponents_end(L):
+    """Scores are formed in powers of two: scale * log2(e) has to be a normal number, or 0."""
+    for scale, want in ((0.0, BAD), (-0.0, BAD), (1e-37, BAD), (-2.3e38, BAD), (2.0 ** 127, BAD), (2.0 ** -126, BAD),
+                        (2.4e38, UNSUPPORTED), (-3.4e38, UNSUPPORTED), (1e-39, UNSUPPORTED), (-1e-45, UNSUPPORTED)):
+        assert attention_without_queries(cache(), problem(tokens=9, scale=scale)) == want, scale
