@@ -366,6 +366,15 @@ def recurrence_backward(x, log_alpha, log_alpha_min: float, workspace, g=None, s
 _RECURRENCE_FUNCTION = None
 
 
+def _gradient(d):
+    """A gradient as the calls take it: contiguous and 16-byte aligned.  That of
+    a concatenated output is a view, which may begin anywhere."""
+    if d is None:
+        return None
+    d = d.contiguous()
+    return d if d.data_ptr() % 16 == 0 else d.clone()
+
+
 def _recurrence_function():
     """The torch.autograd.Function over the training pair, created on first use."""
     global _RECURRENCE_FUNCTION
@@ -387,8 +396,7 @@ def _recurrence_function():
             def backward(ctx, d_out, d_state):
                 x, log_alpha, g, state_in, cu_seqlens = ctx.saved_tensors
                 r = recurrence_backward(x, log_alpha, ctx.log_alpha_min, ctx.workspace, g=g, state_in=state_in,
-                                        cu_seqlens=cu_seqlens, d_out=None if d_out is None else d_out.contiguous(),
-                                        d_state=None if d_state is None else d_state.contiguous(),
+                                        cu_seqlens=cu_seqlens, d_out=_gradient(d_out), d_state=_gradient(d_state),
                                         want_dstate=state_in is not None and ctx.needs_input_grad[3])
                 return r["dx"], r["dlog_alpha"], r["dg"], r["dstate0"], None, None
 

@@ -331,3 +331,27 @@ def test_autograd_of_outputs_that_are_not_used():
     r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, d_state=torch.ones(2, 10, device="cuda"))
     torch.cuda.synchronize()
     assert torch.equal(x.grad, r["dx"])
+
+
+@pytest.mark.parametrize("D", [5, 515])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_autograd_of_outputs_that_are_joined(D, io):
+    """The gradients of a concatenation are views of one array, wherever they begin: the second's is at an odd place."""
+    parts = [made(1, T, D, io, seed=T) for T in (3, 70, 9)]
+
+    def leaves(i):
+        return [i[k].clone().requires_grad_(True) for k in ("x", "la", "g", "s0")]
+
+    def go(l):
+        return kda.recurrence_autograd(l[0], l[1], FLOOR, g=l[2], state_in=l[3])
+
+    joined, alone = [leaves(i) for i in parts], [leaves(i) for i in parts]
+    outs = [go(l) for l in joined]
+    d_out = torch.cat([i["d_out"] for i in parts], 1)
+    d_state = torch.cat([i["d_state"] for i in parts], 1)
+    torch.autograd.backward([torch.cat([o for o, _ in outs], 1), torch.cat([s for _, s in outs], 1)], [d_out, d_state])
+    for l, i in zip(alone, parts):
+        torch.autograd.backward(list(go(l)), [i["d_out"], i["d_state"]])
+    torch.cuda.synchronize()
+    for a, b in zip(joined, alone):
+        assert all(torch.equal(x.grad, y.grad) for x, y in zip(a, b))

@@ -278,3 +278,13 @@ def test_attention_refuses_scales_whose_exponents_end(L):
     for scale, want in ((0.0, BAD), (-0.0, BAD), (1e-37, BAD), (-2.3e38, BAD), (2.0 ** 127, BAD), (2.0 ** -126, BAD),
                         (2.4e38, UNSUPPORTED), (-3.4e38, UNSUPPORTED), (1e-39, UNSUPPORTED), (-1e-45, UNSUPPORTED)):
         assert attention_without_queries(cache(), problem(tokens=9, scale=scale)) == want, scale
+
+
+def test_gradients_are_aligned_before_the_call():
+    torch = pytest.importorskip("torch")
+    room = torch.arange(40, dtype=torch.float32)
+    for d in (None, room[:12], room[4:16].view(3, 4), room[3:15].view(3, 4), room[:12].view(3, 4).t(), room[:1].expand(3, 4),
+              room.bfloat16()[1:5]):
+        got = hybrid._gradient(d)
+        assert got is None if d is None else got.is_contiguous() and got.data_ptr() % 16 == 0 and torch.equal(got, d)
+    assert hybrid._gradient(room) is room               # nothing is copied without need
