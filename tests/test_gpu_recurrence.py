@@ -355,3 +355,31 @@ def test_autograd_of_outputs_that_are_joined(D, io):
     torch.cuda.synchronize()
     for a, b in zip(joined, alone):
         assert all(torch.equal(x.grad, y.grad) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("cu,T", [([0, 90, 300], 420), ([7, 7, 60], 61), ([0, 0], 150)])
+def test_autograd_of_a_padded_batch(cu, T):
+    """Tokens of no sequence: zeros come out and go back, whatever their inputs and what the memory held."""
+    i = made(1, T, 66, "bf16", n=len(cu) - 1)
+    outside = torch.ones(T, dtype=torch.bool)
+    outside[cu[0]:cu[-1]] = False
+    for k in ("x", "la", "g"):
+        i[k][:, outside.cuda()] = math.nan
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    leaves = [i[k].clone().requires_grad_(True) for k in ("x", "la", "g", "s0")]
+    junk = [torch.full_like(i[k], math.nan) for k in ("x", "la", "x", "la", "x", "x") for _ in range(3)]
+    torch.cuda.synchronize()
+    del junk                                              # what the outputs' memory holds
+    out, state = kda.recurrence_autograd(leaves[0], leaves[1], FLOOR, g=leaves[2], state_in=leaves[3], cu_seqlens=cut)
+    torch.autograd.backward([out, state], [i["d_out"], i["d_state"]])
+    torch.cuda.synchronize()
+    for t in (out, *(l.grad for l in leaves[:3])):
+        assert not t[0, outside.cuda()].any()
+    o, s, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=i["s0"], cu_seqlens=cut)
+    r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, g=i["g"], state_in=i["s0"], cu_seqlens=cut, d_out=i["d_out"],
+                                d_state=i["d_state"])
+    torch.cuda.synchronize()
+    inside = ~outside.cuda()
+    assert torch.equal(state, s) and torch.equal(leaves[3].grad, r["dstate0"])
+    for a, b in zip((out, *(l.grad for l in leaves[:3])), (o, r["dx"], r["dlog_alpha"], r["dg"])):
+        assert torch.equal(a[0, inside], b[0, inside])
