@@ -132,7 +132,12 @@ def plan_requests(past_lens, new_lens, block_table, free_pages, page_size: int, 
     free_pages (int32 [m], read only); tokens: rows of the packed batch, the
     sum of new_lens or more.  Returns (cu_seqlens int32 [n+1], total_lens
     int32 [n], slot_map int64 [tokens], pages_taken int32 [1]); the caller
-    drops the first pages_taken entries of free_pages."""
+    drops the first pages_taken entries of free_pages.
+
+    Where the sum of new_lens passes tokens, the last requests are cut off:
+    cu_seqlens.diff() is below new_lens there, while total_lens and the pages
+    taken go by new_lens.  cache4_attention then takes past_lens +
+    cu_seqlens.diff() in the place of total_lens."""
     torch = _torch()
     dev, i32 = past_lens.device, torch.int32
     if past_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:

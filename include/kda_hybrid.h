@@ -38,7 +38,8 @@ extern "C" {
  * lengths alone the call writes
  *   cu_seqlens [n_req+1] int32: offsets of the requests' new tokens in the
  *     packed batch, cut off at `tokens` -- what the kda_varlen_* calls, the
- *     attention and the recurrence take;
+ *     attention and the recurrence take (the attention with other lengths
+ *     where a request was cut off, see below);
  *   total_lens [n_req] int32: past + new (at most INT32_MAX);
  *   block_table [n_req, max_pages] int32, in place: the entries of the pages
  *     that the new tokens begin, taken off free_pages [n_free] in the order
@@ -49,7 +50,15 @@ extern "C" {
  *   pages_taken [1] int32: how many pages the step needs (at most INT32_MAX);
  *     more than n_free means that the list was too short.
  * The list is read, not changed: the caller drops its first pages_taken
- * entries.  page_size is a power of two, 16 to 256; n_req <= 8192, and
+ * entries.
+ * Where the new lengths add up to more than `tokens` (in a replayed graph the
+ * host cannot see it), the last requests are cut off: request r keeps the rows
+ * kept_r = cu_seqlens[r+1] - cu_seqlens[r] < new_lens[r], which is how a kernel
+ * tells.  total_lens, block_table and pages_taken still go by new_lens.  Such a
+ * request's total_lens[r] counts tokens that have no row and no slot, so it is
+ * no input for the attention, which takes a sequence's rows for its newest
+ * tokens: give it past_lens[r] + kept_r, which is total_lens[r] for every other
+ * request.  page_size is a power of two, 16 to 256; n_req <= 8192, and
  * tokens, n_free and n_req * max_pages <= INT32_MAX (more: KDA_ERR_UNSUPPORTED). */
 kda_status kda_plan_requests(int64_t n_req, int64_t tokens, int32_t page_size, int32_t max_pages,
                              const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,

@@ -178,3 +178,30 @@ def test_other_streams_and_calls_at_once():
         for got, want in zip(outs, alone):
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
+
+
+def test_requests_that_were_cut_off():
+    """More new tokens than rows: the offsets tell on the device, and the rows that are left attend as they would in a
+    step that brings them alone."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    page, kv, heads, d = 16, 2, 4, 64
+    past, new, kept = [10, 30, 3], [5, 20, 4], [5, 3, 0]
+    pk, pv = ([r(p, kv, d) for p in past] for _ in range(2))
+    k, v, q = r(8, kv, d), r(8, kv, d), r(8, heads, d)
+    outs = []
+    for lens in (new, kept):
+        cache = kda.Cache4.empty(20, page, kv, d)
+        for t in (cache.k_scale, cache.v_scale):
+            t.fill_(255)                                  # what no token has written stands for NaN
+        table, free, none = i32([[-1] * 5] * 3), torch.arange(20, dtype=torch.int32, device="cuda"), i32([0] * 3)
+        _, _, slots, taken = kda.plan_requests(none, i32(past), table, free, page, sum(past))
+        kda.cache4_append(cache, torch.cat(pk), torch.cat(pv), slots)
+        cu, total, slots, more = kda.plan_requests(i32(past), i32(lens), table, free[int(taken):].contiguous(), page, 8)
+        kda.cache4_append(cache, k, v, slots)
+        assert (cu.diff() < i32(lens)).tolist() == [a < b for a, b in zip(kept, lens)]
+        total = i32(past) + cu.diff()
+        assert total.tolist() == [p + m for p, m in zip(past, kept)]
+        outs.append(kda.cache4_attention(q, cache, table, total, cu_seqlens=cu, max_q=5))
+    torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all() and torch.equal(*outs)
