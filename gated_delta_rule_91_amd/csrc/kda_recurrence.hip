@@ -87,6 +87,11 @@ __device__ __forceinline__ void put(E* p, const float (&x)[N]) {
     __builtin_memcpy(p, &v, N * sizeof(E));
 }
 
+// The least that a decay counts as: e^lambda of a finite lambda is no 0, so that
+// an infinite state stays infinite however fast it decays, while a finite one
+// leaves less than 2^-20.  Only lambda = -inf leaves nothing, and NaN of Inf.
+constexpr float kLeast = 1.40129846e-45f;        // 2^-149
+
 // One token's decay, of lambda = max(log_alpha, floor): `c` is expm1(lambda)
 // where `slow` and e^lambda elsewhere.  expm1 is the Taylor series to the 5th
 // power (the rest is below 2^-29 of the value), e^lambda the hardware exp2.
@@ -100,12 +105,19 @@ struct Decay {
         p = fmaf(p, x, 0.5f);
         p = fmaf(p * x, x, x);
         slow = fabsf(x) <= 0.0625f;
-        c = slow ? p : __builtin_amdgcn_exp2f(1.4426950408889634f * x);
+        // 0 times -inf is NaN, which the maximum leaves out
+        c = slow ? p : fmaxf(__builtin_amdgcn_exp2f(1.4426950408889634f * x), fmaf(0.f, x, kLeast));
     }
     __device__ __forceinline__ Decay(float c_, bool slow_) : c(c_), slow(slow_) {}
+    // What expm1(lambda) multiplies: of an infinite state the largest number, as
+    // -Inf or NaN beside the state itself would be NaN.  (This and kLeast cost
+    // the 64K tokens above 4 us of 499.)
+    __device__ __forceinline__ float part(float h) const {
+        return slow ? __builtin_amdgcn_fmed3f(h, -3.40282347e38f, 3.40282347e38f) : h;
+    }
     // e^lambda h, and e^lambda h + x
-    __device__ __forceinline__ float times(float h) const { return fmaf(c, h, slow ? h : 0.f); }
-    __device__ __forceinline__ float step(float h, float x) const { return fmaf(c, h, x) + (slow ? h : 0.f); }
+    __device__ __forceinline__ float times(float h) const { return fmaf(c, part(h), slow ? h : 0.f); }
+    __device__ __forceinline__ float step(float h, float x) const { return fmaf(c, part(h), x) + (slow ? h : 0.f); }
 };
 
 // e^sum; next to 1 rounded from 1 + expm1, since the hardware exp2 falls short
@@ -114,6 +126,9 @@ __device__ __forceinline__ float product_of(float sum) {
     const Decay d(sum);
     return d.slow ? 1.f + d.c : d.c;
 }
+
+// The product of two decays, which vanishes only where one of them does.
+__device__ __forceinline__ float both(float a, float b) { return fmaxf(a * b, fminf(fminf(a, b), kLeast)); }
 
 // The sequence of a token, walked along the tokens of one wave (all of it the
 // same in every lane).
@@ -325,7 +340,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_kernel(Recurrenc
             const bool cw = sCut[w] != 0;
             constant = constant || cw;
             H = cw ? sH[w][at] : fmaf(sA[w][at], H, sH[w][at]);
-            A *= sA[w][at];
+            A = both(A, sA[w][at]);
         }
         if (grid.tiles > 1) {
             uint64_t* mine = words + (row * grid.tiles + i) * a.D + c + wave;
@@ -500,7 +515,7 @@ __global__ __launch_bounds__(WAVES * 64, 4) void kda_recurrence_backward_kernel(
             const bool cw = sLast[w] != 0;
             constant = constant || cw;
             C = cw ? sC[w][at] : fmaf(sA[w][at], C, sC[w][at]);
-            A *= sA[w][at];
+            A = both(A, sA[w][at]);
         }
         if (grid.tiles > 1) {
             uint64_t* mine = words + (row * grid.tiles + i) * a.D + c + wave;

@@ -138,7 +138,9 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
  * KDA's retention and output gate on a diagonal memory.  Rows are
  * independent; a packed batch (batch == 1, cu_seqlens of n_seq + 1 offsets,
  * as for kda_varlen_prepare) starts a state at each sequence's first token.
- * A NaN log_alpha acts as the floor. */
+ * A NaN log_alpha acts as the floor.  An infinite state stays infinite under
+ * every finite lambda; with lambda = -inf, which leaves nothing of a finite
+ * state, it gives NaN. */
 typedef struct {
     int64_t batch;          /* rows; 1 for a packed batch                        */
     int64_t seqlen;         /* tokens of a row                                   */

@@ -383,3 +383,51 @@ def test_autograd_of_a_padded_batch(cu, T):
     assert torch.equal(state, s) and torch.equal(leaves[3].grad, r["dstate0"])
     for a, b in zip((out, *(l.grad for l in leaves[:3])), (o, r["dx"], r["dlog_alpha"], r["dg"])):
         assert torch.equal(a[0, inside], b[0, inside])
+
+
+def same_where_not_finite(got, want, label):
+    """Inf where the 64-bit form has Inf, of the same sign, and NaN where it has NaN."""
+    got = got.detach().cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), label
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf) and torch.equal(got[inf], want[inf]), label
+
+
+# decays of a channel: none, slow ones on both sides of 1/16, fast ones, ones that vanish in 32 bits, mixed, and a reset
+INF_DECAYS = [0.0, -1e-9, -0.001, -0.0625, -0.0626, -0.4, -3.0, -30.0, -95.0, -300.0, None, "reset"]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,at", [(9, 4), (300, 130), (700, 3)])
+def test_infinite_states_stay_infinite(T, at, io):
+    D = len(INF_DECAYS)
+    i = made(2, T, D, io, gate=False)
+    for c, l in enumerate(INF_DECAYS):
+        if l is None:
+            i["la"][:, ::3, c], i["la"][:, 1::3, c] = -0.02, -2.0
+        elif l == "reset":
+            i["la"][:, at + 2, c] = -math.inf            # nothing of it is left, which for Inf is NaN
+        else:
+            i["la"][:, :, c] = l
+    i["s0"][1] = -math.inf
+    x, d = i["x"].clone(), i["d_out"].clone()
+    x[0, at], d[:, -3], d[1, 1] = math.inf, -math.inf, -math.inf
+    run = lambda x, d_out: ref.recurrence(x.cpu(), i["la"].cpu(), -math.inf, None, i["s0"].cpu(), None, d_out.cpu(), i["d_state"].cpu())
+    want = run(x, i["d_out"])
+    assert torch.isinf(want["out"][0, at:, :-1]).all() and torch.isnan(want["out"][0, at + 2:, -1]).all()
+    out, state = kda.recurrence_prefill(x, i["la"], -math.inf, state_in=i["s0"])
+    step = [kda.recurrence_step(x[:, t].contiguous(), i["la"][:, t].contiguous(), s, -math.inf)
+            for s in [i["s0"].clone()] for t in range(min(T, 20))]
+    torch.cuda.synchronize()
+    same_where_not_finite(out, want["out"], "out")
+    same_where_not_finite(state, want["state"], "state")
+    same_where_not_finite(torch.stack(step, 1), want["out"][:, :20], "step")
+    # the gradient runs the same recurrence in the other direction
+    i["s0"][1] = 1.0
+    want = run(i["x"], d)
+    assert torch.isinf(want["dx"][:, :-2, :-1]).all()
+    _, _, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], -math.inf, state_in=i["s0"])
+    r = kda.recurrence_backward(i["x"], i["la"], -math.inf, ws, state_in=i["s0"], d_out=d, d_state=i["d_state"])
+    torch.cuda.synchronize()
+    for k in ("dx", "dlog_alpha", "dstate0"):
+        same_where_not_finite(r[k], want[k], k)
