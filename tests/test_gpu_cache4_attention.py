@@ -278,3 +278,54 @@ def test_a_scale_of_zero_weighs_all_alike(new, io):
     c, q, g, table, cu = build(total, new, 4, 2, 64, 16, io)
     check(c, (q.float() * 1e35).to(q.dtype), g, table, total, cu, io, scale=0.0, max_q=max(new))
     check(c, (q.float() * 1e35).to(q.dtype), g, table, total, cu, io, scale=-0.0, max_q=max(new))
+
+
+@pytest.mark.parametrize("io,total,new", [("bf16", [5300, 0, 2000, 40, 1500], [4800, 3, 1900, 0, 1500]),
+                                          ("f32", [2600, 0, 1000, 40, 800], [2400, 3, 950, 0, 800])])
+@pytest.mark.parametrize("heads,kv,d", [(64, 1, 64), (64, 1, 128)])
+def test_many_blocks_of_many_rows(heads, kv, d, io, total, new):
+    """Prompts of more row blocks than prefix sums are kept for, with offsets; some rows against the 64-bit form."""
+    rows = {"bf16": 128, "f32": 64}[io]
+    assert sum(new) * heads // kv // rows + len(new) > 4096
+    c, q, g, table, cu = build(total, new, heads, kv, d, 64, io)
+    out = torch.full((q.shape[0] + 2, *q.shape[1:]), 77.0, dtype=q.dtype, device="cuda")
+    kda.cache4_attention(q, c, i32(table), i32(total), cu_seqlens=i32(cu), g=g, out=out[:-2], max_q=max(new), max_len=max(total))
+    assert kda.cache4_attention_workspace_size(q, c, i32(table), i32(total), i32(cu), max_q=max(new)) == 0
+    torch.cuda.synchronize()
+    assert (out[-2:] == 77.0).all() and (out[cu[1]:cu[2]] == 0).all()
+    k, v = (ref.values(getattr(c, n).cpu(), getattr(c, n + "_scale").cpu()) for n in ("k", "v"))
+    u32, scale = 2.0 ** -24, 1 / math.sqrt(d)
+    for s in (0, 2, 4):
+        m = new[s]
+        at = torch.tensor([table[s][t // 64] * 64 + t % 64 for t in range(total[s])])
+        kk, vv = (x[:, 0].reshape(-1, d)[at] for x in (k, v))
+        for i in {0, 1, 63, 64, m // 3, m // 2, m - 2, m - 1}:
+            end, row = total[s] - m + i + 1, cu[s] + i
+            qq = q[row].cpu().double()
+            p = torch.softmax(qq @ kk[:end].T * scale, -1)
+            want, mag = p @ vv[:end], p @ vv[:end].abs()
+            sig = torch.sigmoid(g[row].cpu().double())
+            size = float((qq.abs() @ kk[:end].abs().T).max()) * scale
+            tol = (2 * (d + 8) * u32 * size + end * u32 + 16 * u32 + (U[io] if io == "bf16" else u32)) * mag * sig + U[io] * (want * sig).abs() + 1e-30
+            assert ((out[row].cpu().double() - want * sig).abs() <= tol).all(), (s, i)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_many_ragged_sequences_without_dealing_out(io):
+    """The offsets of over 4096 sequences, searched in memory: some without queries, some of two blocks."""
+    n = 4300
+    new = [(5 * i) % 3 if i % 97 else 12 for i in range(n)]
+    total = [m + (7 * i) % 30 for i, m in enumerate(new)]
+    c, q, g, table, cu = build(total, new, 2, 1, 64, 16, io)
+    check(c, q, g, table, total, cu, io, max_q=3)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,heads", [(64, 4), (128, 2)])
+@pytest.mark.parametrize("others", [0, 69, 600])
+def test_joins_of_more_parts_than_lanes(others, d, heads, io):
+    """A context whose parts a wave joins in more than one turn: alone, and beside few and many short ones."""
+    total, new = [45000 if others < 600 else 60000] + [1] * others, [2] + [1] * others
+    c, q, g, table, cu = build(total, new, heads, 1, d, 256, io)
+    check(c, q, g, table, total, cu, io, max_q=2, max_len=max(total))
+    check(c, q, g, table, total, cu, io, max_q=2, max_len=max(total), scale=3.0)
