@@ -50,7 +50,6 @@ namespace kda {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr float kLog2e = 1.4426950408889634f;
 // The running maximum moves only when a score passes it by this much (in
 // powers of two): probabilities then stay below 2^8 and the rescaling of the
 // sums is rare.
@@ -543,12 +542,6 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
         const int hi = last < row0 ? lo : min(end_of(a, b, last), lim);
         const int all_see = end_of(a, b, row0);                  // the first row sees the fewest
 
-        // scores in powers of two, with the sign of the scale in the queries, so
-        // that the largest product is the largest score; not 0, which would make
-        // NaN of a masked score's -inf: a scale of 0 is in the queries too
-        const float to_log2 = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-        const float sign = a.scale < 0.f ? -1.f : (a.scale == 0.f ? 0.f : 1.f);
-
         // queries: row n of each 16, channels [PER g, PER g + PER)
         bf16x8 q[R][KS][PARTS];
         int end[R];
@@ -562,10 +555,10 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if constexpr (PARTS == 1) {
-                        q[r][j][0][e] = (__bf16)(sign * to_f32(p[8 * j + e]));
+                        q[r][j][0][e] = (__bf16)(a.sign * to_f32(p[8 * j + e]));
                     } else {
                         __bf16 s[PARTS];
-                        parts_of<PARTS>(sign * p[8 * j + e], s);
+                        parts_of<PARTS>(a.sign * p[8 * j + e], s);
 #pragma unroll
                         for (int i = 0; i < PARTS; ++i) q[r][j][i][e] = s[i];
                     }
@@ -593,7 +586,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
                 top[r] = y[r][0];
 #pragma unroll
                 for (int e = 1; e < N; ++e) top[r] = larger(top[r], y[r][e]);
-                top[r] = over_g(top[r]) * to_log2;
+                top[r] = over_g(top[r]) * a.to_log2;
                 more = more || top[r] > m[r] + kSlack;
             }
             if (__any(more)) {
@@ -613,7 +606,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
             const float base = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float z = __builtin_amdgcn_exp2f(fmaf(y[e], to_log2, -base));
+                const float z = __builtin_amdgcn_exp2f(fmaf(y[e], a.to_log2, -base));
                 sum[r] += z;
                 if constexpr (PARTS == 1) {
                     p[0][e] = (__bf16)z;

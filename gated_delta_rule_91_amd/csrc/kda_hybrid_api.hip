@@ -21,6 +21,8 @@ int page_shift(int32_t page_size) {
     return -1;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool ok_io(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
 
 // a * b, or INT64_MAX where that does not fit (a, b >= 0)
@@ -75,7 +77,7 @@ kda_status check_attention(const kda_cache4* c, const kda_cache4_attention_probl
         mul_sat(p->n_seq, p->heads) > (1 << 30) || mul_sat(p->max_pages, c->page_size) > INT32_MAX - 256)
         return KDA_ERR_UNSUPPORTED;
     // the kernels multiply scores by scale * log2(e), which has to be a normal number or 0
-    const float factor = fabsf(p->scale) * 1.4426950408889634f;
+    const float factor = fabsf(p->scale) * kLog2e;
     if (p->scale != 0.0f && !(factor >= FLT_MIN && factor <= FLT_MAX)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
@@ -85,7 +87,9 @@ Cache4AttentionArgs attention_args(const kda_cache4* c, const kda_cache4_attenti
     a.c = cache_args(c);
     a.n_seq = p->n_seq; a.tokens = p->tokens; a.heads = p->heads; a.group = p->heads / c->heads;
     a.max_pages = c->pages > 0 ? p->max_pages : 0;   // a cache without pages counts no tokens
-    a.max_q = p->max_q; a.max_len = p->max_len; a.scale = p->scale;
+    a.max_q = p->max_q; a.max_len = p->max_len;
+    a.to_log2 = p->scale == 0.0f ? 1.0f : fabsf(p->scale) * kLog2e;
+    a.sign = p->scale < 0.0f ? -1.0f : (p->scale == 0.0f ? 0.0f : 1.0f);
     return a;
 }
 

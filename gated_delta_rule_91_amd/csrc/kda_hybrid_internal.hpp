@@ -59,7 +59,12 @@ struct Cache4AttentionArgs {
     const int32_t* block_table;
     const int32_t* total_lens;
     const int32_t* cu_seqlens;   // or null: one query a sequence
-    float scale;
+    // Scores are formed in powers of two, with the sign of the scale in the
+    // queries, so that the largest product is the largest score.  to_log2 is not
+    // 0, which would make NaN of a masked score's -inf: a scale of 0 is in the
+    // queries too.  (Formed in the kernel, they cost the prompts' form registers
+    // that it spills.)
+    float to_log2, sign;
 };
 
 struct RecurrenceArgs {
