@@ -168,13 +168,33 @@ struct Walk {
     // Whether tokens [t, t + n) lie within one sequence, neither its first nor
     // its last token among them.
     __device__ __forceinline__ bool inside(int t, int n) const { return t > first && t + n < end; }
-    // Whether a sequence holds token t, for t going up, and going down.
+    // The last of sequences [lo, hi) that begins at or before t; lo if none
+    // does.  (Not in the lanes: some may have left by then.)
+    __device__ __forceinline__ void find(int t, int lo, int hi) {
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        s = lo;
+        bounds();
+    }
+    // Whether a sequence holds token t, for t going up, and going down.  Mostly
+    // the next sequence does; over empty ones, of which there may be any number
+    // at one place, it is searched.
     __device__ __forceinline__ bool up(int t) {
-        if (cu) while (t >= end && s + 1 < n) { ++s; bounds(); }
+        if (cu && t >= end && s + 1 < n) {
+            ++s;
+            bounds();
+            if (t >= end && s + 1 < n) find(t, s, n);
+        }
         return t >= first && t < end;
     }
     __device__ __forceinline__ bool down(int t) {
-        if (cu) while (t < first && s > 0) { --s; bounds(); }
+        if (cu && t < first && s > 0) {
+            --s;
+            bounds();
+            if (t < first && s > 0) find(t, 0, s);
+        }
         return t >= first && t < end;
     }
 };

@@ -431,3 +431,35 @@ def test_infinite_states_stay_infinite(T, at, io):
     torch.cuda.synchronize()
     for k in ("dx", "dlog_alpha", "dstate0"):
         same_where_not_finite(r[k], want[k], k)
+
+
+@pytest.mark.parametrize("D", [3, 130])
+@pytest.mark.parametrize("many", [1, 2, 1 << 19])
+def test_any_number_of_empty_sequences(many, D):
+    """Wherever they lie they pass their states through, and the others are what they are without them."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    ends, T = [0, 5, 130, 131, 500, 700], 700
+    i = made(1, T, D, "f32", n=len(ends) - 1)
+    full = []                                             # offsets with `many` empty ones in front of four of the sequences and behind the last
+    for k, e in enumerate(ends):
+        full += [e] * (1 + (many if k in (0, 1, 2, 4, 5) else 0))
+    full = i32(full)
+    held = (full.diff() > 0).nonzero()[:, 0]              # the sequences that have tokens
+    assert len(held) == len(ends) - 1 and len(full) == len(ends) + 5 * many
+
+    def go(cu, s0, ds):
+        out, state, ws = kda.recurrence_prefill_for_backward(i["x"], i["la"], FLOOR, g=i["g"], state_in=s0, cu_seqlens=cu)
+        r = kda.recurrence_backward(i["x"], i["la"], FLOOR, ws, g=i["g"], state_in=s0, cu_seqlens=cu, d_out=i["d_out"], d_state=ds)
+        return [out, r["dx"], r["dlog_alpha"], r["dg"]], [state, r["dstate0"]]
+
+    s0, ds = (torch.randn(len(full) - 1, D, device="cuda") for _ in range(2))
+    s0[held], ds[held] = i["s0"], i["d_state"]
+    rows, states = go(full, s0, ds)
+    want_rows, want_states = go(i32(ends), i["s0"], i["d_state"])
+    torch.cuda.synchronize()
+    for a, b in zip(rows, want_rows):
+        assert torch.equal(a, b)
+    for got, want, before in zip(states, want_states, (s0, ds)):
+        expected = before.clone()
+        expected[held] = want
+        assert torch.equal(got, expected)
