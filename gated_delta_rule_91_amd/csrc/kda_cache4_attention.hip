@@ -18,8 +18,11 @@
 //    channel pairs of one token, a byte permute pairs the tokens, and j runs
 //    over the MFMAs.  O^T then holds D/4 consecutive channels of row n.
 // 4-bit values times their power of two are exact in bf16.  bf16 queries are
-// exact too and the probabilities round once to bf16; fp32 queries and
-// probabilities are taken in three bf16 parts, which together hold 24 bits.
+// exact too and the probabilities round once to bf16, which is half a step each
+// and the size of the output's own rounding (1.8e-3 of the values against 64
+// bits, where probabilities in fp32 leave 1.7e-3); their sum is taken before
+// that, in fp32.  fp32 queries and probabilities are taken in three bf16 parts,
+// which together hold 24 bits.
 //
 // Few rows (decode; at most split_max_rows of a sequence and head): the four waves
 // of a workgroup take turns at the 32-token tiles, each through LDS of its own,
@@ -32,9 +35,10 @@
 // Many rows (prompts): each wave has rows of its own, 64 tokens at a time are
 // converted once for all four waves, and operands come from LDS.  Bound by the
 // vector unit's work on the scores beside the products: 4 prompts of up to 1000
-// tokens at the end of contexts of up to 8192, the same heads, take 195 us + 18
+// tokens at the end of contexts of up to 8192, the same heads, take 197 us + 20
 // us for the parts, the matrix units busy a quarter of it.  16 rows a wave
-// instead of 32 took 320 us, 48 or 64 (one workgroup a CU) 306 and 289.
+// instead of 32 took 320 us, 48 or 64 (one workgroup a CU) 306 and 289.  In fp32
+// the ragged contexts take 98 us + 5, the prompts 413 + 19.
 // Sequences are ragged and a query's tokens grow along a prompt, so work is
 // dealt out by tokens: the row blocks' tokens lie end to end in units of 128,
 // and each workgroup takes the same number of units, which may end one block,
@@ -469,7 +473,9 @@ __host__ __device__ constexpr int shared_tiles(int d) { return 2 * 64 * d * 2 * 
 // is dealt to: what fits without spilling.  (With 3 instead of 2 in bf16 and
 // D = 128, R = 1, 56 bytes of spills: 64 contexts of 32768 tokens took 417 us
 // instead of 396, of 2048 36 instead of 30; with 2 instead of 3 and D = 64, 256
-// contexts of 4096 take 147 instead of 134.)
+// contexts of 4096 take 147 instead of 134.  With 3 instead of 2 in fp32 and
+// D = 64, R = 1, 56 bytes too: two contexts of up to 131072 tokens, 24 heads over
+// 4, take 20.3 us and 8.8 for the parts instead of 19.8 and 6.0.)
 constexpr int waves_of(bool bf16, int d, int r) {
     if (bf16) return r == 1 && d == 64 ? 3 : 2;
     return r == 2 && d == 128 ? 1 : 2;

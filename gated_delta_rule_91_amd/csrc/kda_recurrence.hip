@@ -12,10 +12,11 @@
 // training pass's backward, with a gate in bf16), so each reads its inputs
 // once: a workgroup holds a tile of 128 or 64 tokens x 128 channels in
 // registers while the state that enters it is found.  65536 tokens of 4096
-// channels take 507 us (5.3 TB/s); 4 x 4096 tokens of 2048 84 us, backward 140
-// (4.0 and 4.3 TB/s); 60000 of 256, where the chain of tiles bounds it, 72 and
-// 121.  Tiles of 64 tokens forward instead of 128: 608 us for the first instead
-// of 541 at the time, 100 instead of 91 for the second.
+// channels take 517 us (5.2 TB/s); 4 x 4096 tokens of 2048 92 us, backward 138
+// (3.6 and 4.4 TB/s); 60000 of 256, where the chain of tiles bounds it, 81 and
+// 126.  In fp32 the first take 841 us (5.1 TB/s), the second 131 and 182 (4.1 and
+// 5.2).  Tiles of 64 tokens forward instead of 128 in bf16: 608 us for the first
+// instead of 541 at the time, 100 instead of 91 for the second.
 //  * A wave runs its stretch of the tile from nothing: (A, H), the product of
 //    its decays and the state it ends with.  A stretch is the map
 //    h -> A h + H; maps are joined through LDS.
@@ -49,8 +50,9 @@ namespace {
 // Tokens that a workgroup holds, and that its waves share.
 constexpr int kTile = 128, kBackTile = 64;
 // Tiles that a look-back reads at once.  With 4, 60000 tokens of 256 channels
-// take 101 us instead of 72 (backward 188 instead of 121), with 16 56 (89), but
-// the 64K tokens above 549 instead of 507, for its registers.
+// take 108 us instead of 81 (backward 188 instead of 128), with 16 68 (97), but
+// the 64K tokens above 8% more than with 8, for its registers (in fp32 880 us
+// instead of 838).
 constexpr int kWindow = 8;
 // Polls after which a wait gives up with NaN: a tenth of a second, where a tile takes
 // microseconds.  Only a workspace that another call is using can get there.
@@ -111,7 +113,7 @@ struct Decay {
     __device__ __forceinline__ Decay(float c_, bool slow_) : c(c_), slow(slow_) {}
     // What expm1(lambda) multiplies: of an infinite state the largest number, as
     // -Inf or NaN beside the state itself would be NaN.  (This and kLeast cost
-    // the 64K tokens above 4 us of 499.)
+    // the 64K tokens above 4 us.)
     __device__ __forceinline__ float part(float h) const {
         return slow ? __builtin_amdgcn_fmed3f(h, -3.40282347e38f, 3.40282347e38f) : h;
     }
@@ -691,7 +693,8 @@ size_t words_bytes(int64_t B, int64_t T, int64_t D, int tile) {
 constexpr size_t kCounterBytes = 256;
 
 // Tokens of a wave: 16 in bf16, 8 in fp32, whose registers hold half as many
-// (16 in fp32 spill with a gate; without one 34 us instead of 36 for 16384 x 515).
+// (16 in fp32 spill with a gate: 978 us instead of 838 for 65536 x 4096; without
+// one 37 instead of 38 for 16384 x 515, 29 instead of 32 for 16384 x 512).
 template <typename E> constexpr int kForwardWaves = sizeof(E) == 2 ? 8 : 16;
 constexpr int kBackwardWaves = 8;
 

@@ -6,6 +6,12 @@ recurrence with its gradients.
 As in the package itself this module only checks tensors, passes device
 pointers and the stream, and allocates outputs and workspaces; the work is in
 the library's HIP kernels.  Everything here is re-exported by the package.
+
+Calls run on the current stream, or on `stream`.  A workspace made by a call is
+of that stream's pool; outputs are of the current stream's, as everywhere in the
+package, so a caller who gives another stream orders the two: the stream waits
+for the current one before the call, and the current one for the stream before
+it uses or frees the outputs.
 """
 from __future__ import annotations
 
@@ -260,7 +266,8 @@ def cache4_attention(q, cache: Cache4, block_table, total_lens, cu_seqlens=None,
     max_pages]; total_lens int32 [n], the tokens each sequence has, its
     queries the newest of them (append their keys and values first); g
     [T, heads, d]: the read-out gate, out = attention * sigmoid(g); scale
-    defaults to 1/sqrt(d).  max_q and max_len, about the most queries and the
+    defaults to 1/sqrt(d).  bf16 queries have their probabilities rounded to
+    bf16, fp32 ones do not.  max_q and max_len, about the most queries and the
     most tokens of a sequence, steer how the work is split, and nothing else.
     Returns out [T, heads, d]."""
     dev = cache.device

@@ -122,10 +122,12 @@ size_t kda_cache4_attention_workspace_size(const kda_cache4* c, const kda_cache4
  *                 * sigmoid(g[row, h])
  * q, g, out: [tokens, heads, d] io_dtype; g may be NULL (no gate).  A query
  * that sees nothing gives 0.  Pages outside the cache are left out, as if
- * their tokens were masked.  Rows of no sequence are not written.  With fp32
- * the products take the queries and probabilities in three bf16 parts, which
- * is fp32 accuracy (4-bit values are exact in bf16).  cu_seqlens must not
- * decrease (offsets are bounded; others give unspecified rows). */
+ * their tokens were masked.  Rows of no sequence are not written.  Scores,
+ * softmax and sums are fp32.  With bf16 the probabilities round to bf16 for
+ * the product with the values; with fp32 the products take the queries and
+ * probabilities in three bf16 parts, which is fp32 accuracy (4-bit values are
+ * exact in bf16).  cu_seqlens must not decrease (offsets are bounded; others
+ * give unspecified rows). */
 kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_problem* p, const void* q,
                                 const int32_t* block_table, const int32_t* total_lens, const int32_t* cu_seqlens,
                                 const void* g, void* out, void* workspace, size_t workspace_bytes, void* stream);
@@ -138,9 +140,9 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
  * KDA's retention and output gate on a diagonal memory.  Rows are
  * independent; a packed batch (batch == 1, cu_seqlens of n_seq + 1 offsets,
  * as for kda_varlen_prepare) starts a state at each sequence's first token.
- * A NaN log_alpha acts as the floor.  An infinite state stays infinite under
- * every finite lambda; with lambda = -inf, which leaves nothing of a finite
- * state, it gives NaN. */
+ * log_alpha is at most 0, as in kda.h (not checked); NaN acts as the floor.
+ * An infinite state stays infinite under every finite lambda; with lambda =
+ * -inf, which leaves nothing of a finite state, it gives NaN. */
 typedef struct {
     int64_t batch;          /* rows; 1 for a packed batch                        */
     int64_t seqlen;         /* tokens of a row                                   */
