@@ -22,6 +22,13 @@ The operators beside KDA in a hybrid stack (``include/kda_hybrid.h``,
 ``hybrid.py``): plan_requests; Cache4 with cache4_append, cache4_read and
 cache4_attention; recurrence_prefill, recurrence_step and, for training,
 recurrence_prefill_for_backward, recurrence_backward and recurrence_autograd.
+
+The short causal convolution and the selective state space
+(``include/kda_selective.h``, ``selective.py``): short_conv_prefill,
+short_conv_step, short_conv_backward and short_conv_autograd;
+selective_scan_prefill, selective_scan_step and, for training,
+selective_scan_prefill_for_backward, selective_scan_backward and
+selective_scan_autograd.
 """
 from __future__ import annotations
 
@@ -745,3 +752,5 @@ def to_device(inp, device="cuda"):
 
 # the operators beside KDA in a hybrid stack (include/kda_hybrid.h)
 from .hybrid import *  # noqa: E402,F401,F403
+# the short convolution and the selective scan (include/kda_selective.h)
+from .selective import *  # noqa: E402,F401,F403

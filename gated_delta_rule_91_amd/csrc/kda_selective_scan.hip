@@ -1,0 +1,790 @@
+// kda_selective_scan.hip -- a selective state space of N states a channel, its
+// gradients and its single-token step.
+//
+//   delta_t = softplus(dt_t + dt_bias),  a_t[n] = exp(delta_t A[n])
+//   h_t[n] = a_t[n] h_(t-1)[n] + delta_t x_t B_t[n]
+//   y_t = sum_n C_t[n] h_t[n] + skip x_t,  out_t = y_t silu(z_t)
+// and in reverse, with dy_t = d_out_t silu(z_t) and r_t the gradient of h_t that
+// comes from later tokens (d_state at the end):
+//   dh_t = C_t dy_t + r_t,  r_(t-1) = a_t dh_t
+//   dx_t = delta_t sum_n dh_t B_t + skip dy_t
+//   ddelta_t = x_t sum_n dh_t B_t + sum_n A r_(t-1) h_(t-1),  ddt = ddelta sigmoid(dt + dt_bias)
+//   dA = sum_t delta_t r_(t-1) h_(t-1),  dB_t = sum_d dh_t delta_t x_t,  dC_t = sum_d dy_t h_t
+//
+// Every channel and state fades at its own speed, so there is no matrix product
+// in it: it is bound by the vector unit, by an exponential and some four
+// operations for each of N states of an element.  A lane has a channel with all
+// its states in registers; B and C, the same for all channels, come through the
+// scalar cache as scalar operands.
+//
+// Time is split into tiles, a wave each, where there are too few channels to
+// fill the card:
+//  1. each tile's state from nothing, sum_t exp(A sum_(s>t) delta_s) delta_t x_t B_t:
+//     taken from the last token back, so that no step depends on the one before;
+//  2. the tiles' states are joined in order, h <- exp(A sum delta) h + state;
+//  3. each tile runs from its true state and writes the outputs.
+// The backward does the same from the other end.  A sequence's first token
+// starts its state anew, so a tile that holds one hands on a state of its own.
+#include <type_traits>
+
+#include "kda_packed.hpp"
+#include "kda_selective_internal.hpp"
+
+namespace kda {
+
+namespace {
+
+constexpr int kScanWaves = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+// A tile whose incoming state does not reach its end has this for its sum of delta.
+constexpr float kCut = -1.f;
+
+// How time and channels are split (host and kernels).
+struct ScanGrid {
+    int tile, tiles;     // tokens of a tile, tiles of a row
+    int blocks;          // of 64 channels
+};
+
+// Tokens between the states that a forward call keeps for the backward, which
+// forms the states between them anew in registers.
+template <int N> constexpr int kKeep = 128 / N;
+
+struct Place {
+    int row, i, block;   // of batch, tile, channel block
+    int t0, t1;
+    int64_t c;           // a lane's channel, the last one where it has none
+    bool in;             // whether it has
+    bool any;
+    int64_t at;          // index of (row, tile, block)
+};
+__device__ __forceinline__ Place place_of(const SelectiveArgs& a, const ScanGrid& g, int skipped_tiles = 0, int first_tile = 0) {
+    const int64_t w = (int64_t)blockIdx.x * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = g.tiles - skipped_tiles;
+    Place p;
+    p.block = (int)(w % g.blocks);
+    const int64_t rest = w / g.blocks;
+    p.i = (int)(rest % tiles) + first_tile;
+    p.any = rest / tiles < a.B;
+    p.row = (int)(rest / tiles);
+    p.t0 = p.i * g.tile;
+    p.t1 = (int)min((int64_t)p.t0 + g.tile, a.T);
+    const int64_t c = (int64_t)p.block * 64 + (threadIdx.x & 63);
+    p.in = c < a.D;
+    p.c = min(c, a.D - 1);
+    p.at = ((int64_t)p.row * g.tiles + p.i) * g.blocks + p.block;
+    return p;
+}
+
+// softplus(y) to half an ulp or so of itself, also where it is next to 0: with
+// e = exp(-|y|), max(y, 0) + log(1 + e) = max(y, 0) + 2 atanh(e / (2 + e)), whose
+// series is taken to the 15th power (the rest is below 2^-27 of it).
+__device__ __forceinline__ float exp_of(float y) {        // y <= 0
+    const float t = y * kLog2e;
+    const float lost = fmaf(y, kLog2e, -t) + y * 1.92596303e-8f;   // of the product, and of log2 e itself
+    const float e = __builtin_amdgcn_exp2f(t);
+    return t <= -150.f ? 0.f : fmaf(e * kLn2, lost, e);    // also for -inf, where `lost` is NaN
+}
+__device__ __forceinline__ float softplus(float y) {
+    const float e = exp_of(-fabsf(y));
+    const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
+    float p = 1.f / 15.f;
+    p = fmaf(p, q, 1.f / 13.f);
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    return fmaxf(y, 0.f) + 2.f * fmaf(p * q, s, s);
+}
+
+// One row of B or C, in scalar registers.
+typedef const __attribute__((address_space(4))) uint32_t* scalar_words;
+template <typename E, int N>
+struct Shared {
+    static constexpr int WORDS = N * sizeof(E) / 4;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const void* base, int64_t row) {
+        const scalar_words p = (scalar_words)(uintptr_t)(reinterpret_cast<const E*>(base) + row * N);
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = p[i];
+    }
+    __device__ __forceinline__ float operator[](int n) const {
+        if constexpr (sizeof(E) == 4) return __uint_as_float(w[n]);
+        else return __uint_as_float(n & 1 ? w[n >> 1] & 0xffff0000u : w[n >> 1] << 16);
+    }
+};
+
+// A lane's parameters: A in powers of two.
+template <int N>
+struct Params {
+    float A2[N], skip, bias;
+    __device__ __forceinline__ Params(const SelectiveArgs& a, int64_t c) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) A2[n] = a.A[c * N + n] * kLog2e;
+        skip = a.skip ? a.skip[c] : 0.f;
+        bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+    }
+};
+
+// N states of a lane's channel as the caller has them, and as the workspace
+// does: [N][64 lanes].
+template <int N>
+__device__ __forceinline__ void get_state(const float* state, int64_t s, const SelectiveArgs& a, int64_t c, float (&h)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        const f32x4 x = state ? *reinterpret_cast<const f32x4*>(state + (s * a.D + c) * N + n) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[n + i] = x[i];
+    }
+}
+template <int N>
+__device__ __forceinline__ void put_state(float* state, int64_t s, const SelectiveArgs& a, int64_t c, const float (&h)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; n += 4)
+        *reinterpret_cast<f32x4*>(state + (s * a.D + c) * N + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
+}
+template <int N>
+__device__ __forceinline__ void get_kept(const float* at, float (&h)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = at[n * 64 + (threadIdx.x & 63)];
+}
+template <int N>
+__device__ __forceinline__ void put_kept(float* at, const float (&h)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) at[n * 64 + (threadIdx.x & 63)] = h[n];
+}
+
+// The parts of a workspace: for each tile its sum of delta and its states, which
+// the join replaces by those that enter it; of packed batches the state that
+// the last sequence which begins in the tile begins with (state_out may be
+// state_in, and is written by another wave); the backward's kept states and sums.
+struct ScanWorkspace {
+    float* sums;         // [row][tile][block][64]
+    float* ends;         // [row][tile][block][N][64]
+    float* begins;       // the same
+    float* keep;         // [row][T / kKeep][block][N][64]
+    float* params;       // [row][tile][N + 2][D]: sums for dA, dskip, ddt_bias
+    float* shared;       // [block][row][T][2 N]: sums for dB, dC
+};
+
+// ---- 1. each tile's state from nothing ------------------------------------------
+template <typename E, int N>
+__global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    const Place p = place_of(a, g, 1);
+    if (!p.any) return;
+    const Params<N> par(a, p.c);
+    float h[N], sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = 0.f;
+    Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t1 - 1);
+    // the join hands a uniform row's first tile its state
+    const bool begins = a.cu_seqlens && q.first >= p.t0;
+    if (q.end <= p.t1 || q.first >= p.t1) {     // the next tile takes nothing from this one
+        sum = kCut;
+    } else {
+        const int b = max(q.first, p.t0);
+        const int64_t row = (int64_t)p.row * a.T;
+        const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
+        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
+        constexpr int U = 4;
+        E xs[2][U], ds[2][U];
+        auto fetch = [&](int t, E (&xv)[U], E (&dv)[U]) {     // tokens t - 1, t - 2, ...
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)max(t - 1 - u, b) * a.D;
+                xv[u] = x[at];
+                dv[u] = dt[at];
+            }
+        };
+        auto tokens = [&](int t, const E (&xv)[U], const E (&dv)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t - 1 - u < b) break;
+                Shared<E, N> B;
+                B.load(a.Bm, row + t - 1 - u);
+                const float delta = softplus(to_f32(dv[u]) + par.bias), w = delta * to_f32(xv[u]);
+#pragma unroll
+                for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), w * B[n], h[n]);
+                sum += delta;
+            }
+        };
+        fetch(p.t1, xs[0], ds[0]);
+        for (int t = p.t1; t > b; t -= 2 * U) {
+            fetch(t - U, xs[1], ds[1]);
+            tokens(t, xs[0], ds[0]);
+            if (t - U <= b) break;
+            fetch(t - 2 * U, xs[0], ds[0]);
+            tokens(t - U, xs[1], ds[1]);
+        }
+        if (begins) {
+            float s[N];
+            get_state<N>(a.state_in, q.s, a, p.c, s);
+            put_kept<N>(ws.begins + p.at * N * 64, s);
+#pragma unroll
+            for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), s[n], h[n]);
+            sum = kCut;
+        }
+    }
+    ws.sums[p.at * 64 + (threadIdx.x & 63)] = sum;
+    put_kept<N>(ws.ends + p.at * N * 64, h);
+}
+
+// ---- 2. the tiles joined, in their order or from the last to the first -----------
+// A thread has one state of one channel of a row.  Tile i's state becomes the
+// one that enters it.
+template <int N, bool BACK>
+__global__ __launch_bounds__(256) void kda_selective_join_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    const int64_t w = (int64_t)blockIdx.x * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, n = (int)(w % N), block = (int)(w / N % g.blocks);
+    const int64_t row = w / N / g.blocks, c = min((int64_t)block * 64 + lane, a.D - 1);
+    if (row >= a.B) return;
+    const float A2 = a.A[c * N + n] * kLog2e;
+    const float* from = BACK ? a.d_state : a.state_in;
+    float h = !a.cu_seqlens && from ? from[(row * a.D + c) * N + n] : 0.f;
+    auto place = [&](int i) { return (row * g.tiles + (BACK ? g.tiles - 1 - i : i)) * g.blocks + block; };
+    constexpr int U = 8;
+    int i = 0;
+    for (; i + U < g.tiles; i += U) {
+        float e[U], s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            e[u] = ws.ends[(place(i + u) * N + n) * 64 + lane];
+            s[u] = ws.sums[place(i + u) * 64 + lane];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ws.ends[(place(i + u) * N + n) * 64 + lane] = h;
+            h = s[u] < 0.f ? e[u] : fmaf(__builtin_amdgcn_exp2f(s[u] * A2), h, e[u]);
+        }
+    }
+    for (; i < g.tiles; ++i) {
+        float e = 0.f, s = 0.f;
+        if (i + 1 < g.tiles) {
+            e = ws.ends[(place(i) * N + n) * 64 + lane];
+            s = ws.sums[place(i) * 64 + lane];
+        }
+        ws.ends[(place(i) * N + n) * 64 + lane] = h;
+        h = s < 0.f ? e : fmaf(__builtin_amdgcn_exp2f(s * A2), h, e);
+    }
+}
+
+// ---- 3. each tile from its true state ---------------------------------------------
+template <typename E, int N, bool KEEP>
+__global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    const Place p = place_of(a, g);
+    if (!p.any) return;
+    const Params<N> par(a, p.c);
+    const int64_t row = (int64_t)p.row * a.T;
+    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
+    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
+    const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
+    E* out = reinterpret_cast<E*>(a.out) + row * a.D + p.c;
+    Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t0);
+    do {
+        const int b = max(q.first, p.t0), e = min(q.end, p.t1);
+        if (b >= e) continue;
+        float h[N];
+        if (g.tiles > 1 && (!a.cu_seqlens || b > q.first)) get_kept<N>(ws.ends + p.at * N * 64, h);
+        else if (q.end > p.t1) get_kept<N>(ws.begins + p.at * N * 64, h);
+        else get_state<N>(a.state_in, q.s, a, p.c, h);
+
+        constexpr int U = 4;
+        E xs[2][U], ds[2][U], zs[2][U];
+        auto fetch = [&](int t, E (&xv)[U], E (&dv)[U], E (&zv)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
+                xv[u] = x[at];
+                dv[u] = dt[at];
+                zv[u] = z ? z[at] : (E)0.f;
+            }
+        };
+        auto tokens = [&](int t, const E (&xv)[U], const E (&dv)[U], const E (&zv)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= e) break;
+                if constexpr (KEEP) {
+                    if ((t + u) % kKeep<N> == 0) {
+                        const int64_t kept = (a.T + kKeep<N> - 1) / kKeep<N>;
+                        put_kept<N>(ws.keep + ((p.row * kept + (t + u) / kKeep<N>) * g.blocks + p.block) * N * 64, h);
+                    }
+                }
+                Shared<E, N> B, C;
+                B.load(a.Bm, row + t + u);
+                C.load(a.Cm, row + t + u);
+                const float xf = to_f32(xv[u]), delta = softplus(to_f32(dv[u]) + par.bias), w = delta * xf;
+                float y[4] = {par.skip * xf, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    h[n] = fmaf(__builtin_amdgcn_exp2f(delta * par.A2[n]), h[n], w * B[n]);
+                    y[n & 3] = fmaf(C[n], h[n], y[n & 3]);
+                }
+                float o = (y[0] + y[1]) + (y[2] + y[3]);
+                if (z) {
+                    const float zf = to_f32(zv[u]);
+                    o *= zf * sigmoidf_(zf);
+                }
+                if (p.in) out[(int64_t)(t + u) * a.D] = from_f32<E>(o);
+            }
+        };
+        fetch(b, xs[0], ds[0], zs[0]);
+        for (int t = b; t < e; t += 2 * U) {
+            fetch(t + U, xs[1], ds[1], zs[1]);
+            tokens(t, xs[0], ds[0], zs[0]);
+            if (t + U >= e) break;
+            fetch(t + 2 * U, xs[0], ds[0], zs[0]);
+            tokens(t + U, xs[1], ds[1], zs[1]);
+        }
+        if (a.state_out && e == q.end && p.in) put_state<N>(a.state_out, q.s, a, p.c, h);
+    } while (q.end < p.t1 && q.next());
+}
+
+// The states of sequences without tokens, and their gradients: as they came.
+template <int N>
+__global__ __launch_bounds__(256) void kda_selective_empty_kernel(SelectiveArgs a, const float* from, float* to) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t s = i / (a.D * N);
+    if (s >= a.n_seq) return;
+    int64_t first = 0, end = a.T;
+    if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.T, first, end);
+    if (first < end) return;
+    *reinterpret_cast<f32x4*>(to + i) = from ? *reinterpret_cast<const f32x4*>(from + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
+// ---- the backward ------------------------------------------------------------------
+// 1. What a tile's tokens give the gradient of the state that enters it:
+//    sum_t exp(A sum_(s<=t) delta_s) C_t dy_t.
+template <typename E, int N>
+__global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    const Place p = place_of(a, g, 1, 1);
+    if (!p.any) return;
+    const Params<N> par(a, p.c);
+    float r[N], sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) r[n] = 0.f;
+    Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t0);
+    if (q.first >= p.t0 || q.end <= p.t0) {     // the tile before this one gets nothing from it
+        sum = kCut;
+    } else {
+        const int e = min(q.end, p.t1);
+        const bool ends = q.end <= p.t1 && a.cu_seqlens;
+        const int64_t row = (int64_t)p.row * a.T;
+        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
+        const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
+        const E* d_out = a.d_out ? reinterpret_cast<const E*>(a.d_out) + row * a.D + p.c : nullptr;
+        constexpr int U = 4;
+        E gs[2][U], ds[2][U], zs[2][U];
+        auto fetch = [&](int t, E (&gv)[U], E (&dv)[U], E (&zv)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
+                gv[u] = d_out ? d_out[at] : (E)0.f;
+                dv[u] = dt[at];
+                zv[u] = z ? z[at] : (E)0.f;
+            }
+        };
+        auto tokens = [&](int t, const E (&gv)[U], const E (&dv)[U], const E (&zv)[U]) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= e) break;
+                Shared<E, N> C;
+                C.load(a.Cm, row + t + u);
+                sum += softplus(to_f32(dv[u]) + par.bias);
+                float dy = to_f32(gv[u]);
+                if (z) {
+                    const float zf = to_f32(zv[u]);
+                    dy *= zf * sigmoidf_(zf);
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) r[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), dy * C[n], r[n]);
+            }
+        };
+        fetch(p.t0, gs[0], ds[0], zs[0]);
+        for (int t = p.t0; t < e; t += 2 * U) {
+            fetch(t + U, gs[1], ds[1], zs[1]);
+            tokens(t, gs[0], ds[0], zs[0]);
+            if (t + U >= e) break;
+            fetch(t + 2 * U, gs[0], ds[0], zs[0]);
+            tokens(t + U, gs[1], ds[1], zs[1]);
+        }
+        if (ends) {
+            float s[N];
+            get_state<N>(a.d_state, q.s, a, p.c, s);
+#pragma unroll
+            for (int n = 0; n < N; ++n) r[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), s[n], r[n]);
+            sum = kCut;
+        }
+    }
+    ws.sums[p.at * 64 + (threadIdx.x & 63)] = sum;
+    put_kept<N>(ws.ends + p.at * N * 64, r);
+}
+
+// Sums over the 64 lanes of K values at once: halves of the lanes take halves of
+// the values, so that each step adds half as many.  The sum of value k ends in
+// the lanes whose bits say k: bit 5 of a lane is the value's highest, and so on.
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ float pair_sum(float x, float y, bool upper) {     // lanes of `upper` take y
+    return (upper ? y : x) + moved<CTRL>(upper ? x : y);
+}
+template <int K>
+__device__ __forceinline__ float sum_lanes(float (&v)[K]) {
+    constexpr int HALF_MIRROR = 0x141, ROR8 = 0x128, XOR2 = 0x4e, XOR1 = 0xb1;
+    const int lane = threadIdx.x & 63;
+    if constexpr (K >= 2) {
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) {
+            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + K / 2]), false, false);
+            v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+        }
+    }
+    if constexpr (K >= 4) {
+#pragma unroll
+        for (int i = 0; i < K / 4; ++i) {
+            const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + K / 4]), false, false);
+            v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+        }
+    }
+    if constexpr (K >= 8) {
+#pragma unroll
+        for (int i = 0; i < K / 8; ++i) v[i] = pair_sum<ROR8>(v[i], v[i + K / 8], lane & 8);
+    }
+    if constexpr (K >= 16) {
+#pragma unroll
+        for (int i = 0; i < K / 16; ++i) v[i] = pair_sum<HALF_MIRROR>(v[i], v[i + K / 16], lane & 4);
+    } else {
+        v[0] += moved<HALF_MIRROR>(v[0]);
+    }
+    if constexpr (K >= 32) {
+#pragma unroll
+        for (int i = 0; i < K / 32; ++i) v[i] = pair_sum<XOR2>(v[i], v[i + K / 32], lane & 2);
+    } else {
+        v[0] += moved<XOR2>(v[0]);
+    }
+    if constexpr (K >= 64) v[0] = pair_sum<XOR1>(v[0], v[1], lane & 1);
+    else v[0] += moved<XOR1>(v[0]);
+    return v[0];
+}
+
+// 2. Each tile from its last token to its first, kKeep tokens at a time, whose
+//    states are formed anew from the kept one.
+template <typename E, int N>
+__global__ __launch_bounds__(kScanWaves * 64, 2) void kda_selective_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    constexpr int KT = kKeep<N>;
+    const Place p = place_of(a, g);
+    if (!p.any) return;
+    const int lane = threadIdx.x & 63;
+    const Params<N> par(a, p.c);
+    const int64_t row = (int64_t)p.row * a.T, kept = (a.T + KT - 1) / KT;
+    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
+    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
+    const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
+    const E* d_out = a.d_out ? reinterpret_cast<const E*>(a.d_out) + row * a.D + p.c : nullptr;
+    float dA[N], dskip = 0.f, dbias = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) dA[n] = 0.f;
+    Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t1 - 1);
+    do {
+        const int b = max(q.first, p.t0), e = min(q.end, p.t1);
+        if (b >= e) continue;
+        float r[N];
+        if (q.end > p.t1 || (g.tiles > 1 && !a.cu_seqlens)) get_kept<N>(ws.ends + p.at * N * 64, r);
+        else get_state<N>(a.d_state, q.s, a, p.c, r);
+        for (int te = e; te > b;) {
+            const int k = (te - 1) / KT, tb = max(b, k * KT), m = te - tb;
+            float h[KT + 1][N], delta[KT];
+            E xs[KT], ds[KT], zs[KT], gs[KT];
+            if (tb == k * KT) get_kept<N>(ws.keep + ((p.row * kept + k) * g.blocks + p.block) * N * 64, h[0]);
+            else get_state<N>(a.state_in, q.s, a, p.c, h[0]);
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                const int64_t at = (int64_t)min(tb + u, te - 1) * a.D;
+                xs[u] = x[at];
+                ds[u] = dt[at];
+                zs[u] = z ? z[at] : (E)0.f;
+                gs[u] = d_out ? d_out[at] : (E)0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < KT; ++u) {
+                delta[u] = softplus(to_f32(ds[u]) + par.bias);
+                if (u < m) {
+                    Shared<E, N> B;
+                    B.load(a.Bm, row + tb + u);
+                    const float w = delta[u] * to_f32(xs[u]);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) h[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(delta[u] * par.A2[n]), h[u][n], w * B[n]);
+                }
+            }
+#pragma unroll
+            for (int u = KT - 1; u >= 0; --u) {
+                if (u >= m) continue;
+                const int t = tb + u;
+                Shared<E, N> B, C;
+                B.load(a.Bm, row + t);
+                C.load(a.Cm, row + t);
+                const float xf = to_f32(xs[u]), d = delta[u], w = d * xf, go = to_f32(gs[u]), zf = to_f32(zs[u]);
+                const float sig = sigmoidf_(zf), dy = z ? go * (zf * sig) : go;
+                float y = par.skip * xf, du = 0.f, dd = 0.f, v[2 * N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const float dh = fmaf(C[n], dy, r[n]);
+                    y = fmaf(C[n], h[u + 1][n], y);
+                    v[n] = dh * w;
+                    v[N + n] = dy * h[u + 1][n];
+                    du = fmaf(dh, B[n], du);
+                    r[n] = __builtin_amdgcn_exp2f(d * par.A2[n]) * dh;
+                    const float back = r[n] * h[u][n];
+                    dd = fmaf(back, par.A2[n], dd);
+                    dA[n] = fmaf(back, d, dA[n]);
+                }
+                if (!p.in) {
+#pragma unroll
+                    for (int i = 0; i < 2 * N; ++i) v[i] = 0.f;
+                }
+                const float s = sum_lanes<2 * N>(v);
+                const float ddelta = fmaf(du, xf, dd * kLn2);
+                const float ddt = ddelta * sigmoidf_(to_f32(ds[u]) + par.bias);
+                const int64_t at = (row + t) * a.D + p.c;
+                if (p.in) {
+                    reinterpret_cast<E*>(a.dx)[at] = from_f32<E>(fmaf(du, d, par.skip * dy));
+                    reinterpret_cast<E*>(a.ddt)[at] = from_f32<E>(ddt);
+                    if (z) reinterpret_cast<E*>(a.dz)[at] = from_f32<E>(go * y * (sig * fmaf(zf, 1.f - sig, 1.f)));
+                }
+                dskip = fmaf(dy, xf, dskip);
+                dbias += ddt;
+                // value i's sum is in the lanes from 64 / (2 N) i on
+                if (lane % (64 / (2 * N)) == 0) ws.shared[((int64_t)p.block * a.B * a.T + row + t) * (2 * N) + lane / (64 / (2 * N))] = s;
+            }
+            te = tb;
+        }
+        if (b == q.first && a.d_state_in && p.in) put_state<N>(a.d_state_in, q.s, a, p.c, r);
+    } while (q.first > p.t0 && q.previous());
+    if (p.in) {
+        float* to = ws.params + ((int64_t)p.row * g.tiles + p.i) * (N + 2) * a.D + p.c;
+#pragma unroll
+        for (int n = 0; n < N; ++n) to[n * a.D] = dA[n];
+        to[N * a.D] = dskip;
+        to[(N + 1) * a.D] = dbias;
+    }
+}
+
+// 3. The parameters' gradients: sums over the tiles in their order, in 64 bits,
+//    as there can be any number.
+__global__ __launch_bounds__(256) void kda_selective_param_sum_kernel(SelectiveArgs a, const float* parts, int64_t count, int blocks) {
+    __shared__ double sum[kScanWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c = (int64_t)(blockIdx.x % blocks) * 64 + lane;
+    const int j = blockIdx.x / blocks;
+    float* to = j < a.states ? a.dA + c * a.states + j : (j == a.states ? a.dskip : a.ddt_bias);
+    if (!to) return;
+    if (j >= a.states) to += c;
+    double s = 0.;
+    if (c < a.D) {
+        const float* from = parts + (int64_t)j * a.D + c;
+        const int64_t stride = (a.states + 2) * a.D;
+#pragma unroll 8
+        for (int64_t i = wave; i < count; i += kScanWaves) s += from[i * stride];
+    }
+    sum[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= a.D) return;
+#pragma unroll
+    for (int w = 1; w < kScanWaves; ++w) s += sum[w][lane];
+    *to = (float)s;
+}
+
+//    dB and dC: sums over the channel blocks in their order.
+template <typename E>
+__global__ __launch_bounds__(256) void kda_selective_shared_sum_kernel(SelectiveArgs a, const float* parts, int blocks) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int N = a.states;
+    const int64_t row = i / (2 * N), rows = a.B * a.T;
+    const int n = (int)(i - row * 2 * N);
+    if (row >= rows) return;
+    if (a.cu_seqlens) {                   // tokens of no sequence are left as they are
+        int64_t first, end, none;
+        seq_bounds(a.cu_seqlens, 0, a.T, first, none);
+        seq_bounds(a.cu_seqlens, a.n_seq - 1, a.T, none, end);
+        if (row < first || row >= end) return;
+    }
+    float s = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) s += parts[(b * rows + row) * 2 * N + n];
+    E* to = reinterpret_cast<E*>(n < N ? a.dB : a.dC);
+    to[row * N + (n < N ? n : n - N)] = from_f32<E>(s);
+}
+
+// ---- one token -----------------------------------------------------------------------
+// Four states a lane, so that a wave reads and writes whole lines of states.
+template <typename E, int N>
+__global__ __launch_bounds__(256) void kda_selective_step_kernel(SelectiveArgs a) {
+    constexpr int L = N / 4;             // lanes of a channel
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, e = i / L, row = e / a.D, c = e - row * a.D;
+    if (row >= a.B) return;
+    const int n0 = (int)(i % L) * 4;
+    f32x4* at = reinterpret_cast<f32x4*>(a.state_out + i * 4);
+    const f32x4 A = *reinterpret_cast<const f32x4*>(a.A + c * N + n0), B = ld4(reinterpret_cast<const E*>(a.Bm) + row * N + n0),
+                C = ld4(reinterpret_cast<const E*>(a.Cm) + row * N + n0);
+    f32x4 h = *at;
+    const float x = to_f32(reinterpret_cast<const E*>(a.x)[e]);
+    const float delta = softplus(to_f32(reinterpret_cast<const E*>(a.dt)[e]) + (a.dt_bias ? a.dt_bias[c] : 0.f)), w = delta * x;
+    float y = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        h[n] = fmaf(__builtin_amdgcn_exp2f(delta * (A[n] * kLog2e)), h[n], w * B[n]);
+        y = fmaf(C[n], h[n], y);
+    }
+    *at = h;
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) y += __shfl_xor(y, off);
+    if (n0 != 0) return;
+    if (a.skip) y = fmaf(a.skip[c], x, y);
+    if (a.z) {
+        const float z = to_f32(reinterpret_cast<const E*>(a.z)[e]);
+        y *= z * sigmoidf_(z);
+    }
+    reinterpret_cast<E*>(a.out)[e] = from_f32<E>(y);
+}
+
+// ---- host ------------------------------------------------------------------------------
+// Waves that a call is split into, where it has that many.
+constexpr int kWaves = 4096;
+
+ScanGrid scan_grid(const SelectiveArgs& a) {
+    ScanGrid g = {};
+    g.blocks = (int)((a.D + 63) / 64);
+    const int64_t alone = a.B * g.blocks;
+    int64_t tiles = alone > 0 ? (kWaves + alone / 2) / alone : 1;
+    if (tiles < 1) tiles = 1;
+    int64_t tile = (a.T + tiles - 1) / tiles;
+    // joining the tiles goes one by one
+    int64_t least = 32;
+    while (least * least * 4 < a.T) least += 16;
+    if (tile < least && tiles > 1) tile = least;
+    g.tile = (int)((tile + 15) / 16 * 16);
+    if (g.tile < 16) g.tile = 16;
+    g.tiles = (int)((a.T + g.tile - 1) / g.tile);
+    return g;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+int keep_of(int states) { return 128 / states; }
+
+size_t lay_out(const SelectiveArgs& a, bool backward, char* at, ScanWorkspace& ws) {
+    const ScanGrid g = scan_grid(a);
+    size_t used = 0;
+    auto take = [&](bool wanted, size_t floats) {
+        float* r = wanted && at ? reinterpret_cast<float*>(at + used) : nullptr;
+        if (wanted) used += round256(floats * sizeof(float));
+        return r;
+    };
+    const size_t tiles = (size_t)a.B * g.tiles, one = (size_t)g.blocks * a.states * 64;
+    const bool many = g.tiles > 1;
+    ws.sums = take(many, tiles * g.blocks * 64);
+    ws.ends = take(many, tiles * one);
+    ws.begins = take(many && a.cu_seqlens, tiles * one);
+    const size_t kept = (size_t)a.B * ((a.T + keep_of(a.states) - 1) / keep_of(a.states));
+    ws.keep = take(backward, kept * one);
+    ws.params = take(backward, tiles * (a.states + 2) * a.D);
+    ws.shared = take(backward, (size_t)g.blocks * a.B * a.T * 2 * a.states);
+    return used;
+}
+
+template <typename E, int N>
+hipError_t scan_forward(const SelectiveArgs& a, hipStream_t s) {
+    hipError_t e;
+    if (a.B > 0 && a.T > 0) {
+        const ScanGrid g = scan_grid(a);
+        ScanWorkspace ws;
+        lay_out(a, a.keep, a.ws, ws);
+        auto grid = [&](int64_t waves) { return dim3((unsigned)((waves + kScanWaves - 1) / kScanWaves)); };
+        const dim3 block(kScanWaves * 64);
+        if (g.tiles > 1) {
+            hipLaunchKernelGGL((kda_selective_local_kernel<E, N>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            hipLaunchKernelGGL((kda_selective_join_kernel<N, false>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        if (a.keep) hipLaunchKernelGGL((kda_selective_scan_kernel<E, N, true>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+        else hipLaunchKernelGGL((kda_selective_scan_kernel<E, N, false>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!a.state_out || a.state_out == a.state_in || a.n_seq == 0 || (!a.cu_seqlens && a.T > 0)) return hipSuccess;
+    hipLaunchKernelGGL((kda_selective_empty_kernel<N>), dim3((unsigned)((a.n_seq * a.D * N / 4 + 255) / 256)), dim3(256), 0, s, a, a.state_in, a.state_out);
+    return hipGetLastError();
+}
+
+template <typename E, int N>
+hipError_t scan_backward(const SelectiveArgs& a, hipStream_t s) {
+    hipError_t e;
+    const ScanGrid g = scan_grid(a);
+    ScanWorkspace ws;
+    lay_out(a, true, a.ws, ws);
+    auto grid = [&](int64_t waves) { return dim3((unsigned)((waves + kScanWaves - 1) / kScanWaves)); };
+    const dim3 block(kScanWaves * 64);
+    const bool any = a.B > 0 && a.T > 0 && a.n_seq > 0;
+    if (any) {
+        if (g.tiles > 1) {
+            hipLaunchKernelGGL((kda_selective_local_back_kernel<E, N>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            hipLaunchKernelGGL((kda_selective_join_kernel<N, true>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((kda_selective_back_kernel<E, N>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL((kda_selective_shared_sum_kernel<E>), dim3((unsigned)((a.B * a.T * 2 * N + 255) / 256)), dim3(256), 0, s, a, ws.shared, g.blocks);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kda_selective_param_sum_kernel, dim3((unsigned)(g.blocks * (N + 2))), dim3(256), 0, s, a, ws.params, any ? a.B * g.tiles : 0, g.blocks);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (!a.d_state_in || a.n_seq == 0 || (!a.cu_seqlens && a.T > 0)) return hipSuccess;
+    hipLaunchKernelGGL((kda_selective_empty_kernel<N>), dim3((unsigned)((a.n_seq * a.D * N / 4 + 255) / 256)), dim3(256), 0, s, a, a.d_state, a.d_state_in);
+    return hipGetLastError();
+}
+
+template <typename E, int N>
+hipError_t scan_step(const SelectiveArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((kda_selective_step_kernel<E, N>), dim3((unsigned)((a.B * a.D * (N / 4) + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename F>
+hipError_t by_states(bool bf16, int states, F&& f) {
+    auto typed = [&](auto e) {
+        if (states == 8) return f(e, std::integral_constant<int, 8>{});
+        if (states == 16) return f(e, std::integral_constant<int, 16>{});
+        return f(e, std::integral_constant<int, 32>{});
+    };
+    return bf16 ? typed(__bf16{}) : typed(float{});
+}
+
+}  // namespace
+
+bool selective_scan_fits(const SelectiveArgs& a) {
+    const ScanGrid g = scan_grid(a);
+    const int64_t most = UINT32_MAX / 256;      // workgroups of 256
+    return a.B * g.tiles * g.blocks / kScanWaves < most && a.B * g.blocks * a.states / kScanWaves < most && a.B * a.T * 2 * a.states / 256 < most &&
+           a.n_seq * a.D * (a.states / 4) / 256 < most && (int64_t)g.blocks * (a.states + 2) < most;
+}
+
+size_t selective_scan_workspace_bytes(const SelectiveArgs& a, bool backward) {
+    ScanWorkspace ws;
+    return lay_out(a, backward, nullptr, ws);
+}
+
+hipError_t launch_selective_scan(bool bf16, const SelectiveArgs& a, hipStream_t s) {
+    return by_states(bf16, a.states, [&](auto e, auto n) { return scan_forward<decltype(e), decltype(n)::value>(a, s); });
+}
+
+hipError_t launch_selective_scan_backward(bool bf16, const SelectiveArgs& a, hipStream_t s) {
+    return by_states(bf16, a.states, [&](auto e, auto n) { return scan_backward<decltype(e), decltype(n)::value>(a, s); });
+}
+
+hipError_t launch_selective_scan_step(bool bf16, const SelectiveArgs& a, hipStream_t s) {
+    return by_states(bf16, a.states, [&](auto e, auto n) { return scan_step<decltype(e), decltype(n)::value>(a, s); });
+}
+
+}  // namespace kda
