@@ -98,6 +98,23 @@ bool fits(const kda_cache4* c, const kda_cache4_attention_problem* p) {
     return no_rows(p) || cache4_attention_fits(p->io_dtype == KDA_BF16, c->d, attention_args(c, p));
 }
 
+// The shared form, whose groups are sequences of a launch of their own.
+kda_status check_shared(const kda_cache4* c, const kda_cache4_attention_problem* p, int64_t n_groups, int64_t max_prefix) {
+    kda_status st = check_attention(c, p);
+    if (st != KDA_OK) return st;
+    if (n_groups < 0 || max_prefix < 0) return KDA_ERR_INVALID_ARGUMENT;
+    // more groups than sequences only adds empty ones
+    if (n_groups > (1 << 23) || mul_sat(n_groups, p->heads) > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+Cache4SharedArgs shared_args(const kda_cache4* c, const kda_cache4_attention_problem* p, int64_t n_groups, int64_t max_prefix) {
+    Cache4SharedArgs s = {};
+    s.a = attention_args(c, p);
+    s.n_groups = n_groups; s.max_prefix = max_prefix;
+    return s;
+}
+
 kda_status check_recurrence(const kda_recurrence_problem* p) {
     if (!p || p->batch < 0 || p->seqlen < 0 || p->width <= 0 || p->n_seq < -1 || !ok_io(p->io_dtype))
         return KDA_ERR_INVALID_ARGUMENT;
@@ -224,6 +241,42 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
     a.q = q; a.g = g; a.out = out; a.block_table = block_table; a.total_lens = total_lens; a.cu_seqlens = cu_seqlens;
     return hip_status(launch_cache4_attention(p->io_dtype == KDA_BF16, c->d, a, static_cast<char*>(workspace),
                                               (hipStream_t)stream));
+}
+
+size_t kda_cache4_shared_attention_workspace_size(const kda_cache4* c, const kda_cache4_attention_problem* p,
+                                                  int64_t n_groups, int64_t max_prefix) {
+    if (check_shared(c, p, n_groups, max_prefix) != KDA_OK || no_rows(p)) return 0;
+    if (n_groups == 0) return kda_cache4_attention_workspace_size(c, p);
+    const Cache4SharedArgs s = shared_args(c, p, n_groups, max_prefix);
+    if (!cache4_shared_fits(p->io_dtype == KDA_BF16, c->d, s)) return 0;
+    return cache4_shared_workspace_bytes(p->io_dtype == KDA_BF16, c->d, s);
+}
+
+kda_status kda_cache4_shared_attention(const kda_cache4* c, const kda_cache4_attention_problem* p, const void* q,
+                                       const int32_t* block_table, const int32_t* total_lens, int64_t n_groups,
+                                       const int32_t* prefix_lens, const int32_t* group_offsets, int64_t max_prefix,
+                                       const int32_t* cu_seqlens, const void* g, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    kda_status st = check_shared(c, p, n_groups, max_prefix);
+    if (st != KDA_OK) return st;
+    if (n_groups == 0)
+        return kda_cache4_attention(c, p, q, block_table, total_lens, cu_seqlens, g, out, workspace, workspace_bytes, stream);
+    if (!cu_seqlens && p->tokens != p->n_seq) return KDA_ERR_INVALID_ARGUMENT;
+    if (no_rows(p)) return KDA_OK;
+    Cache4SharedArgs s = shared_args(c, p, n_groups, max_prefix);
+    if (!cache4_shared_fits(p->io_dtype == KDA_BF16, c->d, s)) return KDA_ERR_UNSUPPORTED;
+    const size_t need = kda_cache4_shared_attention_workspace_size(c, p, n_groups, max_prefix);
+    if (!ok_ptr(q, true) || !ok_elem(block_table, p->max_pages > 0, 4) || !ok_elem(total_lens, true, 4) ||
+        !ok_elem(prefix_lens, true, 4) || !ok_elem(group_offsets, true, 4) ||
+        (cu_seqlens && !ok_elem(cu_seqlens, true, 4)) || !ok_opt_ptr(g) || !ok_ptr(out, true) || !ok_ptr(workspace, true))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
+    if (out == q) return KDA_ERR_INVALID_ARGUMENT;       // several workgroups read a row of q
+    if ((st = device_ready()) != KDA_OK) return st;
+    s.a.q = q; s.a.g = g; s.a.out = out; s.a.block_table = block_table; s.a.total_lens = total_lens; s.a.cu_seqlens = cu_seqlens;
+    s.prefix_lens = prefix_lens; s.group_offsets = group_offsets;
+    return hip_status(launch_cache4_shared(p->io_dtype == KDA_BF16, c->d, s, static_cast<char*>(workspace),
+                                           (hipStream_t)stream));
 }
 
 size_t kda_recurrence_workspace_size(const kda_recurrence_problem* p) {

@@ -67,6 +67,15 @@ struct Cache4AttentionArgs {
     float to_log2, sign;
 };
 
+// Groups of sequences whose first tokens are the same.
+struct Cache4SharedArgs {
+    Cache4AttentionArgs a;       // max_len: of the tokens behind a prefix
+    int64_t n_groups;
+    int64_t max_prefix;
+    const int32_t* prefix_lens;
+    const int32_t* group_offsets;
+};
+
 struct RecurrenceArgs {
     int64_t B, T, D;
     int64_t n_seq;               // sequences of a packed batch; with cu_seqlens
@@ -105,6 +114,9 @@ hipError_t launch_cache4_read(bool bf16, int d, const Cache4RowsArgs& a, hipStre
 bool cache4_attention_fits(bool bf16, int d, const Cache4AttentionArgs& a);
 size_t cache4_attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a);
 hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& a, char* ws, hipStream_t s);
+bool cache4_shared_fits(bool bf16, int d, const Cache4SharedArgs& a);
+size_t cache4_shared_workspace_bytes(bool bf16, int d, const Cache4SharedArgs& a);
+hipError_t launch_cache4_shared(bool bf16, int d, const Cache4SharedArgs& a, char* ws, hipStream_t s);
 // backward: the workspace of the training pair; else of the prefill alone
 size_t recurrence_workspace_bytes(int64_t B, int64_t T, int64_t D, bool backward);
 hipError_t launch_recurrence(bool bf16, const RecurrenceArgs& a, hipStream_t s);

@@ -22,12 +22,14 @@ from typing import Optional
 from . import KdaError, _cu, _expect, _expect_workspace, _io_code, _stream, _torch, lib
 
 __all__ = ["HYBRID_EXPORTS", "Cache4", "plan_requests", "cache4_append", "cache4_read", "cache4_attention",
-           "cache4_attention_workspace_size", "recurrence_problem", "recurrence_workspace_size",
+           "cache4_attention_workspace_size", "cache4_shared_attention", "cache4_shared_attention_workspace_size",
+           "recurrence_problem", "recurrence_workspace_size",
            "recurrence_backward_workspace_size", "recurrence_prefill", "recurrence_prefill_for_backward",
            "recurrence_backward", "recurrence_autograd", "recurrence_step"]
 
 HYBRID_EXPORTS = ("kda_plan_requests", "kda_cache4_append", "kda_cache4_read", "kda_cache4_attention_workspace_size",
-                  "kda_cache4_attention", "kda_recurrence_workspace_size", "kda_recurrence_backward_workspace_size",
+                  "kda_cache4_attention", "kda_cache4_shared_attention_workspace_size",
+                  "kda_cache4_shared_attention", "kda_recurrence_workspace_size", "kda_recurrence_backward_workspace_size",
                   "kda_recurrence_prefill", "kda_recurrence_prefill_for_backward", "kda_recurrence_backward",
                   "kda_recurrence_step")
 PAGE_SIZES = (16, 32, 64, 128, 256)
@@ -65,6 +67,8 @@ def _hlib() -> ctypes.CDLL:
         L.kda_cache4_read.argtypes = [C, I64, I32, P, P, P, P]
         L.kda_cache4_attention_workspace_size.argtypes = [C, A]
         L.kda_cache4_attention.argtypes = [C, A, P, P, P, P, P, P, P, SZ, P]
+        L.kda_cache4_shared_attention_workspace_size.argtypes = [C, A, I64, I64]
+        L.kda_cache4_shared_attention.argtypes = [C, A, P, P, P, I64, P, P, I64, P, P, P, P, SZ, P]
         L.kda_recurrence_workspace_size.argtypes = [R]
         L.kda_recurrence_backward_workspace_size.argtypes = [R]
         L.kda_recurrence_prefill.argtypes = [R, P, P, P, P, P, P, P, P, SZ, P]
@@ -279,6 +283,57 @@ def cache4_attention(q, cache: Cache4, block_table, total_lens, cu_seqlens=None,
     c = cache._struct
     ws, ws_ptr, nbytes = _workspace(workspace, _hlib().kda_cache4_attention_workspace_size(c, p), dev, stream)
     _run("kda_cache4_attention", dev, stream, c, p, *ptrs, gate, to, ws_ptr, nbytes)
+    return out
+
+
+def _shared_problem(q, cache, block_table, total_lens, prefix_lens, group_offsets, cu_seqlens, scale, max_q, max_prefix,
+                    max_own):
+    """(problem, pointers as _attention_problem gives them, groups, max_prefix, pointers of prefix_lens and
+    group_offsets) of checked inputs."""
+    i32, dev = _torch().int32, cache.device
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens must be 1-D")
+    p, ptrs = _attention_problem(q, cache, block_table, total_lens, cu_seqlens, scale, max_q, max_own)
+    n = prefix_lens.shape[0]
+    if max_prefix is None:
+        max_prefix = block_table.shape[1] * cache.page_size
+    return p, ptrs, n, max(int(max_prefix), 0), (_in("prefix_lens", prefix_lens, (n,), i32, dev),
+                                                 _in("group_offsets", group_offsets, (n + 1,), i32, dev))
+
+
+def cache4_shared_attention_workspace_size(q, cache: Cache4, block_table, total_lens, prefix_lens, group_offsets,
+                                           cu_seqlens=None, max_q=None, max_prefix=None, max_own=None) -> int:
+    """Bytes of workspace that cache4_shared_attention needs for these arguments."""
+    p, _, n, most, _ = _shared_problem(q, cache, block_table, total_lens, prefix_lens, group_offsets, cu_seqlens, None,
+                                       max_q, max_prefix, max_own)
+    return _hlib().kda_cache4_shared_attention_workspace_size(cache._struct, p, n, most)
+
+
+def cache4_shared_attention(q, cache: Cache4, block_table, total_lens, prefix_lens, group_offsets, cu_seqlens=None,
+                            g=None, scale: Optional[float] = None, max_q: Optional[int] = None,
+                            max_prefix: Optional[int] = None, max_own: Optional[int] = None, out=None, workspace=None,
+                            stream=None):
+    """cache4_attention for groups of sequences that share their first tokens,
+    which are read once for a whole group (kda_cache4_shared_attention).
+
+    The sequences [group_offsets[j], group_offsets[j+1]) have the same first
+    prefix_lens[j] tokens (int32 [m+1] and [m]), in the pages of the group's first
+    sequence; sequences of no group attend by themselves.  total_lens counts all
+    tokens of a sequence, those of its prefix among them.  max_q, max_prefix and
+    max_own, about the most queries of a sequence, the longest prefix and the most
+    tokens of a sequence behind its prefix, steer how the work is split, and
+    nothing else.  The rest is as in cache4_attention.  Returns out [T, heads, d]."""
+    dev = cache.device
+    p, ptrs, n, most, groups = _shared_problem(q, cache, block_table, total_lens, prefix_lens, group_offsets,
+                                               cu_seqlens, scale, max_q, max_prefix, max_own)
+    gate = _in("g", g, q.shape, q.dtype, dev)
+    if out is None:
+        out = _torch().empty_like(q)
+    to = _in("out", out, q.shape, q.dtype, dev)
+    c = cache._struct
+    ws, ws_ptr, nbytes = _workspace(workspace, _hlib().kda_cache4_shared_attention_workspace_size(c, p, n, most), dev,
+                                    stream)
+    _run("kda_cache4_shared_attention", dev, stream, c, p, *ptrs[:3], n, *groups, most, ptrs[3], gate, to, ws_ptr, nbytes)
     return out
 
 

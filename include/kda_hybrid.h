@@ -132,6 +132,30 @@ kda_status kda_cache4_attention(const kda_cache4* c, const kda_cache4_attention_
                                 const int32_t* block_table, const int32_t* total_lens, const int32_t* cu_seqlens,
                                 const void* g, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The same for groups of sequences that share their first tokens, which are read
+ * once for all of a group's rows: the sequences [group_offsets[j],
+ * group_offsets[j+1]) have the same first prefix_lens[j] tokens, and those are
+ * read where the group's first sequence has them (the other rows of block_table
+ * need not name them; they may begin with the same pages).  Sequences of no
+ * group, and groups of one, attend by themselves.  Where prefix_lens[j] passes
+ * what a query of the group sees, or ends, only the tokens that all its queries
+ * have behind them count as shared: the tables of the others have to name the
+ * tokens from there on.
+ *   group_offsets: [n_groups + 1], prefix_lens: [n_groups] int32 in device
+ *   memory (bounded, as all indices are; offsets must not decrease, others give
+ *   unspecified rows).
+ *   p->max_len: about the most tokens of a sequence behind its prefix,
+ *   max_prefix: about the longest prefix, >= 0 (both steer the split only).
+ * n_groups == 0 is kda_cache4_attention; at most 2^23, and n_groups * p->heads at
+ * most 2^30 (more: KDA_ERR_UNSUPPORTED).  Everything else is as there. */
+size_t kda_cache4_shared_attention_workspace_size(const kda_cache4* c, const kda_cache4_attention_problem* p,
+                                                  int64_t n_groups, int64_t max_prefix);
+kda_status kda_cache4_shared_attention(const kda_cache4* c, const kda_cache4_attention_problem* p, const void* q,
+                                       const int32_t* block_table, const int32_t* total_lens, int64_t n_groups,
+                                       const int32_t* prefix_lens, const int32_t* group_offsets, int64_t max_prefix,
+                                       const int32_t* cu_seqlens, const void* g, void* out, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 /* ---- a gated linear recurrence -----------------------------------------------
  * Per batch row and channel, a state h (fp32), and for token t
  *   lambda = max(log_alpha_t, log_alpha_min)

@@ -217,3 +217,38 @@ def test_problem_constructors():
     assert kda.selective_scan_backward_workspace_size(q) > kda.selective_scan_workspace_size(q) > 0
     assert kda.selective_scan_workspace_size(kda.selective_scan_problem(1, 16, 64, 16, torch.float32)) == 0
     assert ctypes.sizeof(selective.KdaShortConvProblem) == 48 and ctypes.sizeof(selective.KdaSelectiveScanProblem) == 40
+
+
+def test_shared_attention_refusals(L):
+    from gated_delta_rule_91_amd import hybrid
+    H = hybrid._hlib()
+    cache = hybrid.KdaCache4(9, 64, 2, 128, FAKE, FAKE, FAKE, FAKE)
+    problem = lambda **kw: hybrid.KdaCache4AttentionProblem(*{**dict(n_seq=3, tokens=3, heads=8, max_pages=6, max_q=1, max_len=384, io_dtype=kda.KDA_BF16, scale=0.1), **kw}.values())
+    size = lambda p=None, n=2, most=100: H.kda_cache4_shared_attention_workspace_size(cache, p or problem(), n, most)
+    names = ["q", "table", "total", "n", "prefix", "offsets", "most", "cu", "g", "out", "ws"]
+    base = dict(q=FAKE, table=FAKE, total=FAKE, n=2, prefix=FAKE, offsets=FAKE, most=100, cu=None, g=None, out=2 * FAKE, ws=FAKE)
+    call = lambda p=None, nbytes=1 << 40, **kw: H.kda_cache4_shared_attention(cache, p or problem(), *[{**base, **kw}[k] for k in names], nbytes, None)
+    for kw in (dict(n_seq=-1), dict(heads=7), dict(max_q=0), dict(max_len=-1), dict(io_dtype=5), dict(scale=float("nan")), dict(tokens=4)):
+        assert call(p=problem(**kw)) == BAD, kw
+    for kw in (dict(n=-1), dict(most=-1), dict(q=None), dict(q=MISALIGNED), dict(table=None), dict(total=None), dict(prefix=None), dict(offsets=None),
+               dict(prefix=0x10002), dict(offsets=0x10001), dict(cu=0x10002), dict(g=MISALIGNED), dict(out=None), dict(ws=None), dict(ws=MISALIGNED), dict(out=FAKE)):
+        assert call(**kw) == BAD, kw
+    for kw in (dict(n=2 ** 23 + 1), dict(n=2 ** 40)):
+        assert call(**kw) == UNSUPPORTED and size(n=kw["n"]) == 0, kw
+    for kw in (dict(n_seq=2 ** 25, tokens=2 ** 25), dict(max_pages=2 ** 26)):
+        assert call(p=problem(**kw)) == UNSUPPORTED and size(problem(**kw)) == 0, kw
+    assert size() > 0 and call(nbytes=size() - 1) == SMALL and size(n=-1) == 0 and size(most=-1) == 0
+    assert size(n=0) == H.kda_cache4_attention_workspace_size(cache, problem())
+    assert call(p=problem(n_seq=0, tokens=0), q=None, table=None, total=None, out=None, ws=None, nbytes=0) == 0
+
+
+def test_shared_attention_binding_checks_tensors():
+    torch = pytest.importorskip("torch")
+    i32 = torch.int32
+    t = lambda *s, dtype=i32: torch.zeros(*s, dtype=dtype)
+    cache = kda.Cache4.empty(4, 16, 2, 64, device="cpu")
+    q = t(3, 4, 64, dtype=torch.float32)
+    for args in ((t(3, 2), t(3), t(2, 1), t(3)), (t(3, 2), t(3), t(2), t(2)), (t(3, 2), t(3), t(2), t(3, dtype=torch.int64)), (t(3, 2), t(2), t(2), t(3)),
+                 (t(3, 2), t(3), t(2, dtype=torch.float32), t(3)), (t(3, 2), t(3), t(2), t(3))):       # the last: not on a GPU
+        with pytest.raises((ValueError, TypeError)):
+            kda.cache4_shared_attention(q, cache, *args)
