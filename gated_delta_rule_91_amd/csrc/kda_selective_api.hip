@@ -20,12 +20,12 @@ int64_t mul_sat(int64_t a, int64_t b) {
     return __builtin_mul_overflow(a, b, &r) ? INT64_MAX : r;
 }
 
-// What both operators ask of their rows.  Token indices are 32-bit in the
-// kernels, elements 64-bit.
+// What both operators ask of their rows.  Token indices and a row's bytes are
+// 32-bit in the kernels, elements 64-bit.
 kda_status check_rows(int64_t batch, int64_t seqlen, int64_t width, int64_t n_seq, kda_dtype io) {
     if (batch < 0 || seqlen < 0 || width <= 0 || n_seq < -1 || !ok_io(io)) return KDA_ERR_INVALID_ARGUMENT;
     if (n_seq >= 0 && batch != 1) return KDA_ERR_INVALID_ARGUMENT;
-    if (seqlen > (1 << 30) || width > (1 << 30) || batch > (1 << 24) || n_seq > (1 << 24) ||
+    if (seqlen > (1 << 30) || width > (1 << 28) || batch > (1 << 24) || n_seq > (1 << 24) ||
         mul_sat(mul_sat(batch, seqlen), width) > ((int64_t)1 << 40))
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;

@@ -35,6 +35,7 @@ namespace kda {
 namespace {
 
 constexpr int kScanWaves = 4;
+constexpr int kXcds = 8;             // a launch over tiles has a multiple of as many workgroups
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 // A tile whose incoming state does not reach its end has this for its sum of delta.
 constexpr float kCut = -1.f;
@@ -52,13 +53,16 @@ template <int N> constexpr int kKeep = 128 / N;
 struct Place {
     int row, i, block;   // of batch, tile, channel block
     int t0, t1;
-    int64_t c;           // a lane's channel, the last one where it has none
+    uint32_t c;          // a lane's channel, the last one where it has none
     bool in;             // whether it has
     bool any;
     int64_t at;          // index of (row, tile, block)
 };
 __device__ __forceinline__ Place place_of(const SelectiveArgs& a, const ScanGrid& g, int skipped_tiles = 0, int first_tile = 0) {
-    const int64_t w = (int64_t)blockIdx.x * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Workgroups go to the XCDs in turn: each XCD gets a stretch of them, so that
+    // those of a tile, which read the same rows of B and C, share its L2.
+    const int64_t block = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    const int64_t w = block * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = g.tiles - skipped_tiles;
     Place p;
     p.block = (int)(w % g.blocks);
@@ -70,31 +74,41 @@ __device__ __forceinline__ Place place_of(const SelectiveArgs& a, const ScanGrid
     p.t1 = (int)min((int64_t)p.t0 + g.tile, a.T);
     const int64_t c = (int64_t)p.block * 64 + (threadIdx.x & 63);
     p.in = c < a.D;
-    p.c = min(c, a.D - 1);
+    p.c = (uint32_t)min(c, a.D - 1);
     p.at = ((int64_t)p.row * g.tiles + p.i) * g.blocks + p.block;
     return p;
 }
 
-// softplus(y) to half an ulp or so of itself, also where it is next to 0: with
-// e = exp(-|y|), max(y, 0) + log(1 + e) = max(y, 0) + 2 atanh(e / (2 + e)), whose
-// series is taken to the 15th power (the rest is below 2^-27 of it).
-__device__ __forceinline__ float exp_of(float y) {        // y <= 0
-    const float t = y * kLog2e;
-    const float lost = fmaf(y, kLog2e, -t) + y * 1.92596303e-8f;   // of the product, and of log2 e itself
-    const float e = __builtin_amdgcn_exp2f(t);
-    return t <= -150.f ? 0.f : fmaf(e * kLn2, lost, e);    // also for -inf, where `lost` is NaN
+// A lane's channel of a token's row, which is the same address in all lanes: a
+// scalar base and a 32-bit offset, one for all arrays of a type.  (The empty
+// assembly keeps the two apart: else each array gets a 64-bit address a lane.)
+template <typename T> using Global = __attribute__((address_space(1))) T;
+template <typename T> __device__ __forceinline__ T get_at(const T* row, uint32_t c) {
+    const Global<char>* base = (const Global<char>*)row;
+    asm("" : "+s"(base));
+    return *(const Global<T>*)(base + (uint32_t)(c * sizeof(T)));
 }
+template <typename T> __device__ __forceinline__ void put_at(T* row, uint32_t c, T x) {
+    Global<char>* base = (Global<char>*)row;
+    asm("" : "+s"(base));
+    *(Global<T>*)(base + (uint32_t)(c * sizeof(T))) = x;
+}
+
+// softplus(y) to a few ulps of itself, also where it is next to 0: with e =
+// exp(-|y|), max(y, 0) + log(1 + e) = max(y, 0) + 2 atanh(s), s = e / (2 + e) <= 1/3.
+// exp takes what the product with log2 e and that number itself lose; atanh(s) =
+// s + s^3 p(s^2) with p, of degree 3, through the Chebyshev nodes of [0, 1/9]
+// (2^-25.9 of the value at most).
 __device__ __forceinline__ float softplus(float y) {
-    const float e = exp_of(-fabsf(y));
+    const float m = __builtin_amdgcn_fmed3f(-fabsf(y), -150.f, 0.f);      // -inf would lose itself; NaN stays in y
+    const float t = m * kLog2e, lost = fmaf(m, 1.92596303e-8f, fmaf(m, kLog2e, -t));
+    const float e0 = __builtin_amdgcn_exp2f(t), e = fmaf(e0, kLn2 * lost, e0);
     const float s = e * __builtin_amdgcn_rcpf(2.f + e), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    return fmaxf(y, 0.f) + 2.f * fmaf(p * q, s, s);
+    float p = 0.1342574954f;
+    p = fmaf(p, q, 0.1411830932f);
+    p = fmaf(p, q, 0.2000378072f);
+    p = fmaf(p, q, 0.3333331943f);
+    return fmaf(2.f, fmaf(p * q, s, s), __builtin_elementwise_maximum(y, 0.f));
 }
 
 // One row of B or C, in scalar registers.
@@ -102,11 +116,18 @@ typedef const __attribute__((address_space(4))) uint32_t* scalar_words;
 template <typename E, int N>
 struct Shared {
     static constexpr int WORDS = N * sizeof(E) / 4;
+    static constexpr bool AHEAD = WORDS <= 8;      // whether two rows of B and of C fit the scalar registers
     uint32_t w[WORDS];
-    __device__ __forceinline__ void load(const void* base, int64_t row) {
-        const scalar_words p = (scalar_words)(uintptr_t)(reinterpret_cast<const E*>(base) + row * N);
+    __device__ __forceinline__ void load(const E* row) {
+        const scalar_words p = (scalar_words)(uintptr_t)row;
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) w[i] = p[i];
+    }
+    // Waits for the row.  Scalar loads come back in any order, so a wait is for
+    // all of them.
+    __device__ __forceinline__ void wait() {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 8) asm volatile("" : "+s"(w[i]));
     }
     __device__ __forceinline__ float operator[](int n) const {
         if constexpr (sizeof(E) == 4) return __uint_as_float(w[n]);
@@ -114,13 +135,36 @@ struct Shared {
     }
 };
 
+// The rows of a walk along the tokens, the next one sent for behind the wait for
+// this one, so that it is there when a token's work is done.
+template <typename E, int N>
+struct SharedWalk {
+    static constexpr bool AHEAD = Shared<E, N>::AHEAD;
+    const E* at;
+    Shared<E, N> now[AHEAD ? 2 : 1];
+    __device__ __forceinline__ explicit SharedWalk(const E* first) : at(first) {
+        if constexpr (AHEAD) now[0].load(at);
+    }
+    // The row of this token, the u-th of an even number; `step` elements further
+    // lies the next one's, if there is `more`.
+    __device__ __forceinline__ void begin(int u) {
+        if constexpr (AHEAD) now[u & 1].wait();
+        else now[0].load(at);
+    }
+    __device__ __forceinline__ void go_on(int u, int step, bool more) {
+        if (more) at += step;
+        if constexpr (AHEAD) now[(u + 1) & 1].load(at);
+    }
+    __device__ __forceinline__ const Shared<E, N>& row(int u) const { return now[AHEAD ? u & 1 : 0]; }
+};
+
 // A lane's parameters: A in powers of two.
 template <int N>
 struct Params {
     float A2[N], skip, bias;
-    __device__ __forceinline__ Params(const SelectiveArgs& a, int64_t c) {
+    __device__ __forceinline__ Params(const SelectiveArgs& a, uint32_t c) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) A2[n] = a.A[c * N + n] * kLog2e;
+        for (int n = 0; n < N; ++n) A2[n] = a.A[(int64_t)c * N + n] * kLog2e;
         skip = a.skip ? a.skip[c] : 0.f;
         bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     }
@@ -129,7 +173,7 @@ struct Params {
 // N states of a lane's channel as the caller has them, and as the workspace
 // does: [N][64 lanes].
 template <int N>
-__device__ __forceinline__ void get_state(const float* state, int64_t s, const SelectiveArgs& a, int64_t c, float (&h)[N]) {
+__device__ __forceinline__ void get_state(const float* state, int64_t s, const SelectiveArgs& a, uint32_t c, float (&h)[N]) {
 #pragma unroll
     for (int n = 0; n < N; n += 4) {
         const f32x4 x = state ? *reinterpret_cast<const f32x4*>(state + (s * a.D + c) * N + n) : f32x4{0.f, 0.f, 0.f, 0.f};
@@ -138,7 +182,7 @@ __device__ __forceinline__ void get_state(const float* state, int64_t s, const S
     }
 }
 template <int N>
-__device__ __forceinline__ void put_state(float* state, int64_t s, const SelectiveArgs& a, int64_t c, const float (&h)[N]) {
+__device__ __forceinline__ void put_state(float* state, int64_t s, const SelectiveArgs& a, uint32_t c, const float (&h)[N]) {
 #pragma unroll
     for (int n = 0; n < N; n += 4)
         *reinterpret_cast<f32x4*>(state + (s * a.D + c) * N + n) = f32x4{h[n], h[n + 1], h[n + 2], h[n + 3]};
@@ -162,6 +206,7 @@ struct ScanWorkspace {
     float* sums;         // [row][tile][block][64]
     float* ends;         // [row][tile][block][N][64]
     float* begins;       // the same
+    float* delta;        // [row][T][D], of the tokens that step 1 passes; with a backward of all
     float* keep;         // [row][T / kKeep][block][N][64]
     float* params;       // [row][tile][N + 2][D]: sums for dA, dskip, ddt_bias
     float* shared;       // [block][row][T][2 N]: sums for dB, dC
@@ -184,27 +229,33 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_kernel(Se
     } else {
         const int b = max(q.first, p.t0);
         const int64_t row = (int64_t)p.row * a.T;
-        const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
-        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
+        const E* x = reinterpret_cast<const E*>(a.x) + row * a.D;
+        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D;
+        float* deltas = ws.delta + row * a.D;
         constexpr int U = 4;
         E xs[2][U], ds[2][U];
         auto fetch = [&](int t, E (&xv)[U], E (&dv)[U]) {     // tokens t - 1, t - 2, ...
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t at = (int64_t)max(t - 1 - u, b) * a.D;
-                xv[u] = x[at];
-                dv[u] = dt[at];
+                xv[u] = get_at(x + at, p.c);
+                dv[u] = get_at(dt + at, p.c);
             }
         };
+        SharedWalk<E, N> B(reinterpret_cast<const E*>(a.Bm) + (row + p.t1 - 1) * N);
+        float* to = deltas + (int64_t)(p.t1 - 1) * a.D;
         auto tokens = [&](int t, const E (&xv)[U], const E (&dv)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t - 1 - u < b) break;
-                Shared<E, N> B;
-                B.load(a.Bm, row + t - 1 - u);
+                B.begin(u);
+                B.go_on(u, -N, t - 1 - u > b);
+                __builtin_amdgcn_sched_barrier(0);
                 const float delta = softplus(to_f32(dv[u]) + par.bias), w = delta * to_f32(xv[u]);
+                if (p.in) put_at(to, p.c, delta);
+                to -= a.D;
 #pragma unroll
-                for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), w * B[n], h[n]);
+                for (int n = 0; n < N; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), w * B.row(u)[n], h[n]);
                 sum += delta;
             }
         };
@@ -269,16 +320,17 @@ __global__ __launch_bounds__(256) void kda_selective_join_kernel(SelectiveArgs a
 }
 
 // ---- 3. each tile from its true state ---------------------------------------------
-template <typename E, int N, bool KEEP>
+template <typename E, int N, bool GATE, bool KEEP>
 __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
     const Place p = place_of(a, g);
     if (!p.any) return;
     const Params<N> par(a, p.c);
     const int64_t row = (int64_t)p.row * a.T;
-    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
-    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
-    const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
-    E* out = reinterpret_cast<E*>(a.out) + row * a.D + p.c;
+    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D;
+    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D;
+    const E* z = reinterpret_cast<const E*>(a.z) + row * a.D;
+    E* out = reinterpret_cast<E*>(a.out) + row * a.D;
+    float* deltas = ws.delta + row * a.D;
     Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t0);
     do {
         const int b = max(q.first, p.t0), e = min(q.end, p.t1);
@@ -288,53 +340,76 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(Sel
         else if (q.end > p.t1) get_kept<N>(ws.begins + p.at * N * 64, h);
         else get_state<N>(a.state_in, q.s, a, p.c, h);
 
-        constexpr int U = 4;
-        E xs[2][U], ds[2][U], zs[2][U];
-        auto fetch = [&](int t, E (&xv)[U], E (&dv)[U], E (&zv)[U]) {
+        // HAVE: step 1 has left delta
+        auto run = [&](auto have) {
+            constexpr bool HAVE = decltype(have)::value;
+            typedef typename std::conditional<HAVE, float, E>::type DE;
+            const DE* from;
+            if constexpr (HAVE) from = deltas;
+            else from = dt;
+            constexpr int U = 4;
+            E xs[2][U], zs[2][U];
+            DE ds[2][U];
+            auto fetch = [&](int t, E (&xv)[U], DE (&dv)[U], E (&zv)[U]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
-                xv[u] = x[at];
-                dv[u] = dt[at];
-                zv[u] = z ? z[at] : (E)0.f;
-            }
-        };
-        auto tokens = [&](int t, const E (&xv)[U], const E (&dv)[U], const E (&zv)[U]) {
+                for (int u = 0; u < U; ++u) {
+                    const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
+                    xv[u] = get_at(x + at, p.c);
+                    dv[u] = get_at(from + at, p.c);
+                    if constexpr (GATE) zv[u] = get_at(z + at, p.c);
+                }
+            };
+            SharedWalk<E, N> B(reinterpret_cast<const E*>(a.Bm) + (row + b) * N), C(reinterpret_cast<const E*>(a.Cm) + (row + b) * N);
+            E* to = out + (int64_t)b * a.D;
+            auto tokens = [&](int t, const E (&xv)[U], const DE (&dv)[U], const E (&zv)[U]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (t + u >= e) break;
-                if constexpr (KEEP) {
-                    if ((t + u) % kKeep<N> == 0) {
-                        const int64_t kept = (a.T + kKeep<N> - 1) / kKeep<N>;
-                        put_kept<N>(ws.keep + ((p.row * kept + (t + u) / kKeep<N>) * g.blocks + p.block) * N * 64, h);
+                for (int u = 0; u < U; ++u) {
+                    if (t + u >= e) break;
+                    B.begin(u);
+                    C.begin(u);
+                    B.go_on(u, N, t + u + 1 < e);
+                    C.go_on(u, N, t + u + 1 < e);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (KEEP) {
+                        if ((t + u) % kKeep<N> == 0) {
+                            const int64_t kept = (a.T + kKeep<N> - 1) / kKeep<N>;
+                            put_kept<N>(ws.keep + ((p.row * kept + (t + u) / kKeep<N>) * g.blocks + p.block) * N * 64, h);
+                        }
                     }
-                }
-                Shared<E, N> B, C;
-                B.load(a.Bm, row + t + u);
-                C.load(a.Cm, row + t + u);
-                const float xf = to_f32(xv[u]), delta = softplus(to_f32(dv[u]) + par.bias), w = delta * xf;
-                float y[4] = {par.skip * xf, 0.f, 0.f, 0.f};
+                    float delta = to_f32(dv[u]);
+                    if constexpr (!HAVE) {
+                        delta = softplus(delta + par.bias);
+                        if constexpr (KEEP) {
+                            if (p.in) put_at(deltas + (int64_t)(t + u) * a.D, p.c, delta);
+                        }
+                    }
+                    const float xf = to_f32(xv[u]), w = delta * xf;
+                    float y[4] = {par.skip * xf, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    h[n] = fmaf(__builtin_amdgcn_exp2f(delta * par.A2[n]), h[n], w * B[n]);
-                    y[n & 3] = fmaf(C[n], h[n], y[n & 3]);
+                    for (int n = 0; n < N; ++n) {
+                        h[n] = fmaf(__builtin_amdgcn_exp2f(delta * par.A2[n]), h[n], w * B.row(u)[n]);
+                        y[n & 3] = fmaf(C.row(u)[n], h[n], y[n & 3]);
+                    }
+                    float o = (y[0] + y[1]) + (y[2] + y[3]);
+                    if constexpr (GATE) {
+                        const float zf = to_f32(zv[u]);
+                        o *= zf * sigmoidf_(zf);
+                    }
+                    if (p.in) put_at(to, p.c, from_f32<E>(o));
+                    to += a.D;
                 }
-                float o = (y[0] + y[1]) + (y[2] + y[3]);
-                if (z) {
-                    const float zf = to_f32(zv[u]);
-                    o *= zf * sigmoidf_(zf);
-                }
-                if (p.in) out[(int64_t)(t + u) * a.D] = from_f32<E>(o);
+            };
+            fetch(b, xs[0], ds[0], zs[0]);
+            for (int t = b; t < e; t += 2 * U) {
+                fetch(t + U, xs[1], ds[1], zs[1]);
+                tokens(t, xs[0], ds[0], zs[0]);
+                if (t + U >= e) break;
+                fetch(t + 2 * U, xs[0], ds[0], zs[0]);
+                tokens(t + U, xs[1], ds[1], zs[1]);
             }
         };
-        fetch(b, xs[0], ds[0], zs[0]);
-        for (int t = b; t < e; t += 2 * U) {
-            fetch(t + U, xs[1], ds[1], zs[1]);
-            tokens(t, xs[0], ds[0], zs[0]);
-            if (t + U >= e) break;
-            fetch(t + 2 * U, xs[0], ds[0], zs[0]);
-            tokens(t + U, xs[1], ds[1], zs[1]);
-        }
+        if (q.end > p.t1) run(std::true_type{});
+        else run(std::false_type{});
         if (a.state_out && e == q.end && p.in) put_state<N>(a.state_out, q.s, a, p.c, h);
     } while (q.end < p.t1 && q.next());
 }
@@ -354,7 +429,7 @@ __global__ __launch_bounds__(256) void kda_selective_empty_kernel(SelectiveArgs 
 // ---- the backward ------------------------------------------------------------------
 // 1. What a tile's tokens give the gradient of the state that enters it:
 //    sum_t exp(A sum_(s<=t) delta_s) C_t dy_t.
-template <typename E, int N>
+template <typename E, int N, bool GATE>
 __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
     const Place p = place_of(a, g, 1, 1);
     if (!p.any) return;
@@ -369,34 +444,37 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kern
         const int e = min(q.end, p.t1);
         const bool ends = q.end <= p.t1 && a.cu_seqlens;
         const int64_t row = (int64_t)p.row * a.T;
-        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
-        const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
-        const E* d_out = a.d_out ? reinterpret_cast<const E*>(a.d_out) + row * a.D + p.c : nullptr;
+        const float* deltas = ws.delta + row * a.D;
+        const E* z = reinterpret_cast<const E*>(a.z) + row * a.D;
+        const E* d_out = reinterpret_cast<const E*>(a.d_out ? a.d_out : a.x) + row * a.D;      // any that is there
         constexpr int U = 4;
-        E gs[2][U], ds[2][U], zs[2][U];
-        auto fetch = [&](int t, E (&gv)[U], E (&dv)[U], E (&zv)[U]) {
+        E gs[2][U], zs[2][U];
+        float ds[2][U];
+        auto fetch = [&](int t, E (&gv)[U], float (&dv)[U], E (&zv)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
-                gv[u] = d_out ? d_out[at] : (E)0.f;
-                dv[u] = dt[at];
-                zv[u] = z ? z[at] : (E)0.f;
+                gv[u] = get_at(d_out + at, p.c);
+                dv[u] = get_at(deltas + at, p.c);
+                if constexpr (GATE) zv[u] = get_at(z + at, p.c);
             }
         };
-        auto tokens = [&](int t, const E (&gv)[U], const E (&dv)[U], const E (&zv)[U]) {
+        SharedWalk<E, N> C(reinterpret_cast<const E*>(a.Cm) + (row + p.t0) * N);
+        auto tokens = [&](int t, const E (&gv)[U], const float (&dv)[U], const E (&zv)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (t + u >= e) break;
-                Shared<E, N> C;
-                C.load(a.Cm, row + t + u);
-                sum += softplus(to_f32(dv[u]) + par.bias);
-                float dy = to_f32(gv[u]);
-                if (z) {
+                C.begin(u);
+                C.go_on(u, N, t + u + 1 < e);
+                __builtin_amdgcn_sched_barrier(0);
+                sum += dv[u];
+                float dy = a.d_out ? to_f32(gv[u]) : 0.f;
+                if constexpr (GATE) {
                     const float zf = to_f32(zv[u]);
                     dy *= zf * sigmoidf_(zf);
                 }
 #pragma unroll
-                for (int n = 0; n < N; ++n) r[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), dy * C[n], r[n]);
+                for (int n = 0; n < N; ++n) r[n] = fmaf(__builtin_amdgcn_exp2f(sum * par.A2[n]), dy * C.row(u)[n], r[n]);
             }
         };
         fetch(p.t0, gs[0], ds[0], zs[0]);
@@ -422,6 +500,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kern
 // Sums over the 64 lanes of K values at once: halves of the lanes take halves of
 // the values, so that each step adds half as many.  The sum of value k ends in
 // the lanes whose bits say k: bit 5 of a lane is the value's highest, and so on.
+// halves() is the first step, of values k and k + K / 2; sum_lanes takes its K / 2
+// results.
 template <int CTRL>
 __device__ __forceinline__ float moved(float x) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
@@ -430,34 +510,25 @@ template <int CTRL>
 __device__ __forceinline__ float pair_sum(float x, float y, bool upper) {     // lanes of `upper` take y
     return (upper ? y : x) + moved<CTRL>(upper ? x : y);
 }
+__device__ __forceinline__ float halves(float x, float y) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+__device__ __forceinline__ float quarters(float x, float y) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
 template <int K>
-__device__ __forceinline__ float sum_lanes(float (&v)[K]) {
+__device__ __forceinline__ float sum_lanes(float (&v)[K / 2]) {
+    static_assert(K == 16 || K == 32 || K == 64, "each lane, or 2 or 4 of them, end with a sum");
     constexpr int HALF_MIRROR = 0x141, ROR8 = 0x128, XOR2 = 0x4e, XOR1 = 0xb1;
     const int lane = threadIdx.x & 63;
-    if constexpr (K >= 2) {
 #pragma unroll
-        for (int i = 0; i < K / 2; ++i) {
-            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + K / 2]), false, false);
-            v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-        }
-    }
-    if constexpr (K >= 4) {
+    for (int i = 0; i < K / 4; ++i) v[i] = quarters(v[i], v[i + K / 4]);
 #pragma unroll
-        for (int i = 0; i < K / 4; ++i) {
-            const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + K / 4]), false, false);
-            v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-        }
-    }
-    if constexpr (K >= 8) {
+    for (int i = 0; i < K / 8; ++i) v[i] = pair_sum<ROR8>(v[i], v[i + K / 8], lane & 8);
 #pragma unroll
-        for (int i = 0; i < K / 8; ++i) v[i] = pair_sum<ROR8>(v[i], v[i + K / 8], lane & 8);
-    }
-    if constexpr (K >= 16) {
-#pragma unroll
-        for (int i = 0; i < K / 16; ++i) v[i] = pair_sum<HALF_MIRROR>(v[i], v[i + K / 16], lane & 4);
-    } else {
-        v[0] += moved<HALF_MIRROR>(v[0]);
-    }
+    for (int i = 0; i < K / 16; ++i) v[i] = pair_sum<HALF_MIRROR>(v[i], v[i + K / 16], lane & 4);
     if constexpr (K >= 32) {
 #pragma unroll
         for (int i = 0; i < K / 32; ++i) v[i] = pair_sum<XOR2>(v[i], v[i + K / 32], lane & 2);
@@ -469,20 +540,22 @@ __device__ __forceinline__ float sum_lanes(float (&v)[K]) {
     return v[0];
 }
 
-// 2. Each tile from its last token to its first, kKeep tokens at a time, whose
-//    states are formed anew from the kept one.
-template <typename E, int N>
-__global__ __launch_bounds__(kScanWaves * 64, 2) void kda_selective_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
-    constexpr int KT = kKeep<N>;
+// 2. Each tile from its last token to its first, half of kKeep tokens at a time,
+//    whose states are formed anew from the kept one and stay in registers.
+template <typename E, int N, bool GATE>
+__global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selective_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    constexpr int KT = kKeep<N>, HT = KT / 2;
     const Place p = place_of(a, g);
     if (!p.any) return;
     const int lane = threadIdx.x & 63;
     const Params<N> par(a, p.c);
-    const int64_t row = (int64_t)p.row * a.T, kept = (a.T + KT - 1) / KT;
-    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D + p.c;
-    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D + p.c;
-    const E* z = a.z ? reinterpret_cast<const E*>(a.z) + row * a.D + p.c : nullptr;
-    const E* d_out = a.d_out ? reinterpret_cast<const E*>(a.d_out) + row * a.D + p.c : nullptr;
+    const int64_t row = (int64_t)p.row * a.T, kept = (a.T + KT - 1) / KT, at0 = row * a.D;
+    const E* x = reinterpret_cast<const E*>(a.x) + at0;
+    const E* dt = reinterpret_cast<const E*>(a.dt) + at0;
+    const E* z = reinterpret_cast<const E*>(a.z) + at0;
+    const E* d_out = reinterpret_cast<const E*>(a.d_out ? a.d_out : a.x) + at0;      // any that is there
+    const float* deltas = ws.delta + at0;
+    const E *Bp = reinterpret_cast<const E*>(a.Bm) + row * N, *Cp = reinterpret_cast<const E*>(a.Cm) + row * N;
     float dA[N], dskip = 0.f, dbias = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n) dA[n] = 0.f;
@@ -494,64 +567,85 @@ __global__ __launch_bounds__(kScanWaves * 64, 2) void kda_selective_back_kernel(
         if (q.end > p.t1 || (g.tiles > 1 && !a.cu_seqlens)) get_kept<N>(ws.ends + p.at * N * 64, r);
         else get_state<N>(a.d_state, q.s, a, p.c, r);
         for (int te = e; te > b;) {
-            const int k = (te - 1) / KT, tb = max(b, k * KT), m = te - tb;
-            float h[KT + 1][N], delta[KT];
-            E xs[KT], ds[KT], zs[KT], gs[KT];
-            if (tb == k * KT) get_kept<N>(ws.keep + ((p.row * kept + k) * g.blocks + p.block) * N * 64, h[0]);
-            else get_state<N>(a.state_in, q.s, a, p.c, h[0]);
+            const int k = (te - 1) / KT, t0 = max(b, k * KT);
+            const int tb = te - t0 > HT ? t0 + HT : t0, m = te - tb;      // the tokens of this turn
+            float h[HT + 1][N], delta[HT];
+            E xs[HT], ds[HT], zs[HT], gs[HT];
 #pragma unroll
-            for (int u = 0; u < KT; ++u) {
+            for (int u = 0; u < HT; ++u) {
                 const int64_t at = (int64_t)min(tb + u, te - 1) * a.D;
-                xs[u] = x[at];
-                ds[u] = dt[at];
-                zs[u] = z ? z[at] : (E)0.f;
-                gs[u] = d_out ? d_out[at] : (E)0.f;
+                xs[u] = get_at(x + at, p.c);
+                delta[u] = get_at(deltas + at, p.c);
+                ds[u] = get_at(dt + at, p.c);
+                if constexpr (GATE) zs[u] = get_at(z + at, p.c);
+                gs[u] = get_at(d_out + at, p.c);
             }
+            if (t0 == k * KT) get_kept<N>(ws.keep + ((p.row * kept + k) * g.blocks + p.block) * N * 64, h[0]);
+            else get_state<N>(a.state_in, q.s, a, p.c, h[0]);
+            if (tb > t0) {                // over the first half, to the state that the second begins with
+                E xf[HT];
+                float df[HT];
 #pragma unroll
-            for (int u = 0; u < KT; ++u) {
-                delta[u] = softplus(to_f32(ds[u]) + par.bias);
-                if (u < m) {
+                for (int u = 0; u < HT; ++u) {
+                    xf[u] = get_at(x + (int64_t)(t0 + u) * a.D, p.c);
+                    df[u] = get_at(deltas + (int64_t)(t0 + u) * a.D, p.c);
+                }
+#pragma unroll
+                for (int u = 0; u < HT; ++u) {
+                    __builtin_amdgcn_sched_barrier(0);
                     Shared<E, N> B;
-                    B.load(a.Bm, row + tb + u);
-                    const float w = delta[u] * to_f32(xs[u]);
+                    B.load(Bp + (int64_t)(t0 + u) * N);
+                    const float w = df[u] * to_f32(xf[u]);
 #pragma unroll
-                    for (int n = 0; n < N; ++n) h[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(delta[u] * par.A2[n]), h[u][n], w * B[n]);
+                    for (int n = 0; n < N; ++n) h[0][n] = fmaf(__builtin_amdgcn_exp2f(df[u] * par.A2[n]), h[0][n], w * B[n]);
                 }
             }
 #pragma unroll
-            for (int u = KT - 1; u >= 0; --u) {
+            for (int u = 0; u < HT; ++u) {
                 if (u >= m) continue;
+                __builtin_amdgcn_sched_barrier(0);
+                Shared<E, N> B;
+                B.load(Bp + (int64_t)(tb + u) * N);
+                const float w = delta[u] * to_f32(xs[u]);
+#pragma unroll
+                for (int n = 0; n < N; ++n) h[u + 1][n] = fmaf(__builtin_amdgcn_exp2f(delta[u] * par.A2[n]), h[u][n], w * B[n]);
+            }
+#pragma unroll
+            for (int u = HT - 1; u >= 0; --u) {
+                if (u >= m) continue;
+                __builtin_amdgcn_sched_barrier(0);       // one token's values at a time: together they spill
                 const int t = tb + u;
                 Shared<E, N> B, C;
-                B.load(a.Bm, row + t);
-                C.load(a.Cm, row + t);
-                const float xf = to_f32(xs[u]), d = delta[u], w = d * xf, go = to_f32(gs[u]), zf = to_f32(zs[u]);
-                const float sig = sigmoidf_(zf), dy = z ? go * (zf * sig) : go;
-                float y = par.skip * xf, du = 0.f, dd = 0.f, v[2 * N];
+                B.load(Bp + (int64_t)t * N);
+                C.load(Cp + (int64_t)t * N);
+                const float xf = to_f32(xs[u]), d = delta[u], w = d * xf, go = a.d_out ? to_f32(gs[u]) : 0.f;
+                float zf = 0.f, sig = 0.f, dy = go;
+                if constexpr (GATE) {
+                    zf = to_f32(zs[u]);
+                    sig = sigmoidf_(zf);
+                    dy = go * (zf * sig);
+                }
+                // lanes without a channel add nothing to the sums over channels
+                const float wv = p.in ? w : 0.f, dyv = p.in ? dy : 0.f;
+                float y = GATE ? par.skip * xf : 0.f, du = 0.f, dd = 0.f, v[N];
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const float dh = fmaf(C[n], dy, r[n]);
-                    y = fmaf(C[n], h[u + 1][n], y);
-                    v[n] = dh * w;
-                    v[N + n] = dy * h[u + 1][n];
+                    if constexpr (GATE) y = fmaf(C[n], h[u + 1][n], y);
+                    v[n] = halves(dh * wv, dyv * h[u + 1][n]);
                     du = fmaf(dh, B[n], du);
                     r[n] = __builtin_amdgcn_exp2f(d * par.A2[n]) * dh;
                     const float back = r[n] * h[u][n];
                     dd = fmaf(back, par.A2[n], dd);
                     dA[n] = fmaf(back, d, dA[n]);
                 }
-                if (!p.in) {
-#pragma unroll
-                    for (int i = 0; i < 2 * N; ++i) v[i] = 0.f;
-                }
                 const float s = sum_lanes<2 * N>(v);
-                const float ddelta = fmaf(du, xf, dd * kLn2);
-                const float ddt = ddelta * sigmoidf_(to_f32(ds[u]) + par.bias);
-                const int64_t at = (row + t) * a.D + p.c;
+                const float ddt = fmaf(du, xf, dd * kLn2) * sigmoidf_(to_f32(ds[u]) + par.bias);
+                const int64_t at = at0 + (int64_t)t * a.D;
                 if (p.in) {
-                    reinterpret_cast<E*>(a.dx)[at] = from_f32<E>(fmaf(du, d, par.skip * dy));
-                    reinterpret_cast<E*>(a.ddt)[at] = from_f32<E>(ddt);
-                    if (z) reinterpret_cast<E*>(a.dz)[at] = from_f32<E>(go * y * (sig * fmaf(zf, 1.f - sig, 1.f)));
+                    put_at(reinterpret_cast<E*>(a.dx) + at, p.c, from_f32<E>(fmaf(du, d, par.skip * dy)));
+                    put_at(reinterpret_cast<E*>(a.ddt) + at, p.c, from_f32<E>(ddt));
+                    if constexpr (GATE) put_at(reinterpret_cast<E*>(a.dz) + at, p.c, from_f32<E>(go * y * (sig * fmaf(zf, 1.f - sig, 1.f))));
                 }
                 dskip = fmaf(dy, xf, dskip);
                 dbias += ddt;
@@ -563,11 +657,11 @@ __global__ __launch_bounds__(kScanWaves * 64, 2) void kda_selective_back_kernel(
         if (b == q.first && a.d_state_in && p.in) put_state<N>(a.d_state_in, q.s, a, p.c, r);
     } while (q.first > p.t0 && q.previous());
     if (p.in) {
-        float* to = ws.params + ((int64_t)p.row * g.tiles + p.i) * (N + 2) * a.D + p.c;
+        float* to = ws.params + ((int64_t)p.row * g.tiles + p.i) * (N + 2) * a.D;
 #pragma unroll
-        for (int n = 0; n < N; ++n) to[n * a.D] = dA[n];
-        to[N * a.D] = dskip;
-        to[(N + 1) * a.D] = dbias;
+        for (int n = 0; n < N; ++n) put_at(to + n * a.D, p.c, dA[n]);
+        put_at(to + N * a.D, p.c, dskip);
+        put_at(to + (N + 1) * a.D, p.c, dbias);
     }
 }
 
@@ -686,11 +780,17 @@ size_t lay_out(const SelectiveArgs& a, bool backward, char* at, ScanWorkspace& w
     ws.sums = take(many, tiles * g.blocks * 64);
     ws.ends = take(many, tiles * one);
     ws.begins = take(many && a.cu_seqlens, tiles * one);
+    ws.delta = take(many || backward, (size_t)a.B * a.T * a.D);
     const size_t kept = (size_t)a.B * ((a.T + keep_of(a.states) - 1) / keep_of(a.states));
     ws.keep = take(backward, kept * one);
     ws.params = take(backward, tiles * (a.states + 2) * a.D);
     ws.shared = take(backward, (size_t)g.blocks * a.B * a.T * 2 * a.states);
     return used;
+}
+
+dim3 grid(int64_t waves) {
+    const int64_t blocks = (waves + kScanWaves - 1) / kScanWaves;
+    return dim3((unsigned)((blocks + kXcds - 1) / kXcds * kXcds));
 }
 
 template <typename E, int N>
@@ -700,7 +800,6 @@ hipError_t scan_forward(const SelectiveArgs& a, hipStream_t s) {
         const ScanGrid g = scan_grid(a);
         ScanWorkspace ws;
         lay_out(a, a.keep, a.ws, ws);
-        auto grid = [&](int64_t waves) { return dim3((unsigned)((waves + kScanWaves - 1) / kScanWaves)); };
         const dim3 block(kScanWaves * 64);
         if (g.tiles > 1) {
             hipLaunchKernelGGL((kda_selective_local_kernel<E, N>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
@@ -708,8 +807,9 @@ hipError_t scan_forward(const SelectiveArgs& a, hipStream_t s) {
             hipLaunchKernelGGL((kda_selective_join_kernel<N, false>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        if (a.keep) hipLaunchKernelGGL((kda_selective_scan_kernel<E, N, true>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
-        else hipLaunchKernelGGL((kda_selective_scan_kernel<E, N, false>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+        const auto kernel = a.z ? (a.keep ? kda_selective_scan_kernel<E, N, true, true> : kda_selective_scan_kernel<E, N, true, false>)
+                                : (a.keep ? kda_selective_scan_kernel<E, N, false, true> : kda_selective_scan_kernel<E, N, false, false>);
+        hipLaunchKernelGGL(kernel, grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!a.state_out || a.state_out == a.state_in || a.n_seq == 0 || (!a.cu_seqlens && a.T > 0)) return hipSuccess;
@@ -723,17 +823,16 @@ hipError_t scan_backward(const SelectiveArgs& a, hipStream_t s) {
     const ScanGrid g = scan_grid(a);
     ScanWorkspace ws;
     lay_out(a, true, a.ws, ws);
-    auto grid = [&](int64_t waves) { return dim3((unsigned)((waves + kScanWaves - 1) / kScanWaves)); };
     const dim3 block(kScanWaves * 64);
     const bool any = a.B > 0 && a.T > 0 && a.n_seq > 0;
     if (any) {
         if (g.tiles > 1) {
-            hipLaunchKernelGGL((kda_selective_local_back_kernel<E, N>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
+            hipLaunchKernelGGL((a.z ? kda_selective_local_back_kernel<E, N, true> : kda_selective_local_back_kernel<E, N, false>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
             if ((e = hipGetLastError()) != hipSuccess) return e;
             hipLaunchKernelGGL((kda_selective_join_kernel<N, true>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((kda_selective_back_kernel<E, N>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+        hipLaunchKernelGGL((a.z ? kda_selective_back_kernel<E, N, true> : kda_selective_back_kernel<E, N, false>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL((kda_selective_shared_sum_kernel<E>), dim3((unsigned)((a.B * a.T * 2 * N + 255) / 256)), dim3(256), 0, s, a, ws.shared, g.blocks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -766,7 +865,7 @@ hipError_t by_states(bool bf16, int states, F&& f) {
 bool selective_scan_fits(const SelectiveArgs& a) {
     const ScanGrid g = scan_grid(a);
     const int64_t most = UINT32_MAX / 256;      // workgroups of 256
-    return a.B * g.tiles * g.blocks / kScanWaves < most && a.B * g.blocks * a.states / kScanWaves < most && a.B * a.T * 2 * a.states / 256 < most &&
+    return a.B * g.tiles * g.blocks / kScanWaves < most - kXcds && a.B * g.blocks * a.states / kScanWaves < most - kXcds && a.B * a.T * 2 * a.states / 256 < most &&
            a.n_seq * a.D * (a.states / 4) / 256 < most && (int64_t)g.blocks * (a.states + 2) < most;
 }
 
