@@ -50,6 +50,19 @@ struct ScanGrid {
 // forms the states between them anew in registers.
 template <int N> constexpr int kKeep = 128 / N;
 
+// The states of sequences without tokens, and their gradients, go through: what
+// the workgroups behind those of the tiles do, a wave for each sequence.
+template <int N>
+__device__ __forceinline__ void pass_through(const SelectiveArgs& a, int64_t block, const float* from, float* to) {
+    const int64_t s = block * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), each = a.D * N;
+    if (s >= a.n_seq) return;
+    int64_t first = 0, end = a.T;
+    if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.T, first, end);
+    if (first < end) return;
+    for (int64_t i = (threadIdx.x & 63) * 4; i < each; i += 256)
+        *reinterpret_cast<f32x4*>(to + s * each + i) = from ? *reinterpret_cast<const f32x4*>(from + s * each + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
 struct Place {
     int row, i, block;   // of batch, tile, channel block
     int t0, t1;
@@ -58,10 +71,11 @@ struct Place {
     bool any;
     int64_t at;          // index of (row, tile, block)
 };
-__device__ __forceinline__ Place place_of(const SelectiveArgs& a, const ScanGrid& g, int skipped_tiles = 0, int first_tile = 0) {
+// `blocks`: workgroups of the tiles, a multiple of kXcds.
+__device__ __forceinline__ Place place_of(const SelectiveArgs& a, const ScanGrid& g, unsigned blocks, int skipped_tiles = 0, int first_tile = 0) {
     // Workgroups go to the XCDs in turn: each XCD gets a stretch of them, so that
     // those of a tile, which read the same rows of B and C, share its L2.
-    const int64_t block = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    const int64_t block = (int64_t)(blockIdx.x % kXcds) * (blocks / kXcds) + blockIdx.x / kXcds;
     const int64_t w = block * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = g.tiles - skipped_tiles;
     Place p;
@@ -215,7 +229,7 @@ struct ScanWorkspace {
 // ---- 1. each tile's state from nothing ------------------------------------------
 template <typename E, int N>
 __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
-    const Place p = place_of(a, g, 1);
+    const Place p = place_of(a, g, gridDim.x, 1);
     if (!p.any) return;
     const Params<N> par(a, p.c);
     float h[N], sum = 0.f;
@@ -229,21 +243,22 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_kernel(Se
     } else {
         const int b = max(q.first, p.t0);
         const int64_t row = (int64_t)p.row * a.T;
-        const E* x = reinterpret_cast<const E*>(a.x) + row * a.D;
-        const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D;
-        float* deltas = ws.delta + row * a.D;
+        const E* x = reinterpret_cast<const E*>(a.x) + (row + p.t1 - 1) * a.D;
+        const E* dt = reinterpret_cast<const E*>(a.dt) + (row + p.t1 - 1) * a.D;
         constexpr int U = 4;
         E xs[2][U], ds[2][U];
-        auto fetch = [&](int t, E (&xv)[U], E (&dv)[U]) {     // tokens t - 1, t - 2, ...
+        auto fetch = [&](int t, E (&xv)[U], E (&dv)[U]) {     // tokens t - 1, t - 2, ..., called in that order
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = (int64_t)max(t - 1 - u, b) * a.D;
-                xv[u] = get_at(x + at, p.c);
-                dv[u] = get_at(dt + at, p.c);
+                xv[u] = get_at(x, p.c);
+                dv[u] = get_at(dt, p.c);
+                const int64_t step = t - 1 - u > b ? a.D : 0;
+                x -= step;
+                dt -= step;
             }
         };
         SharedWalk<E, N> B(reinterpret_cast<const E*>(a.Bm) + (row + p.t1 - 1) * N);
-        float* to = deltas + (int64_t)(p.t1 - 1) * a.D;
+        float* to = ws.delta + (row + p.t1 - 1) * a.D;
         auto tokens = [&](int t, const E (&xv)[U], const E (&dv)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -281,56 +296,69 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_kernel(Se
 }
 
 // ---- 2. the tiles joined, in their order or from the last to the first -----------
-// A thread has one state of one channel of a row.  Tile i's state becomes the
-// one that enters it.
-template <int N, bool BACK>
-__global__ __launch_bounds__(256) void kda_selective_join_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
-    const int64_t w = (int64_t)blockIdx.x * kScanWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63, n = (int)(w % N), block = (int)(w / N % g.blocks);
-    const int64_t row = w / N / g.blocks, c = min((int64_t)block * 64 + lane, a.D - 1);
-    if (row >= a.B) return;
+// A workgroup has one state of 64 channels of a row, a wave kJoin tiles at a time,
+// all of which are on their way together: their latency is what bounds this.  The
+// waves' maps h -> A h + H are joined through LDS.  Tile i's state becomes the one
+// that enters it.
+constexpr int kJoin = 16;
+
+template <int N, bool BACK, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void kda_selective_join_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+    __shared__ float sA[WAVES][64], sH[WAVES][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n = (int)(blockIdx.x % N), block = (int)(blockIdx.x / N % g.blocks);
+    const int64_t row = blockIdx.x / N / g.blocks, c = min((int64_t)block * 64 + lane, a.D - 1);
     const float A2 = a.A[c * N + n] * kLog2e;
     const float* from = BACK ? a.d_state : a.state_in;
-    float h = !a.cu_seqlens && from ? from[(row * a.D + c) * N + n] : 0.f;
+    float in = !a.cu_seqlens && from ? from[(row * a.D + c) * N + n] : 0.f;       // enters the tiles of a turn
     auto place = [&](int i) { return (row * g.tiles + (BACK ? g.tiles - 1 - i : i)) * g.blocks + block; };
-    constexpr int U = 8;
-    int i = 0;
-    for (; i + U < g.tiles; i += U) {
-        float e[U], s[U];
+    const int last = g.tiles - 1;        // has no state of its own: nothing goes on behind it
+    for (int first = 0; first <= last; first += WAVES * kJoin) {
+        const int i0 = first + wave * kJoin;
+        float e[kJoin], f[kJoin];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            e[u] = ws.ends[(place(i + u) * N + n) * 64 + lane];
-            s[u] = ws.sums[place(i + u) * 64 + lane];
+        for (int u = 0; u < kJoin; ++u) {
+            const int64_t at = place(min(i0 + u, last - 1));
+            e[u] = ws.ends[(at * N + n) * 64 + lane];
+            f[u] = ws.sums[at * 64 + lane];
+        }
+        float A = 1.f, H = 0.f;
+#pragma unroll
+        for (int u = 0; u < kJoin; ++u) {
+            f[u] = f[u] < 0.f ? 0.f : __builtin_amdgcn_exp2f(f[u] * A2);
+            A *= f[u];
+            H = fmaf(f[u], H, e[u]);
+        }
+        sA[wave][lane] = A;
+        sH[wave][lane] = H;
+        __syncthreads();
+        float h = in;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            in = fmaf(sA[w][lane], in, sH[w][lane]);
+            if (w + 1 == wave) h = in;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            ws.ends[(place(i + u) * N + n) * 64 + lane] = h;
-            h = s[u] < 0.f ? e[u] : fmaf(__builtin_amdgcn_exp2f(s[u] * A2), h, e[u]);
+        for (int u = 0; u < kJoin; ++u) {
+            if (i0 + u > last) break;
+            ws.ends[(place(i0 + u) * N + n) * 64 + lane] = h;
+            h = fmaf(f[u], h, e[u]);
         }
-    }
-    for (; i < g.tiles; ++i) {
-        float e = 0.f, s = 0.f;
-        if (i + 1 < g.tiles) {
-            e = ws.ends[(place(i) * N + n) * 64 + lane];
-            s = ws.sums[place(i) * 64 + lane];
-        }
-        ws.ends[(place(i) * N + n) * 64 + lane] = h;
-        h = s < 0.f ? e : fmaf(__builtin_amdgcn_exp2f(s * A2), h, e);
+        __syncthreads();                 // before the next turn's maps
     }
 }
 
 // ---- 3. each tile from its true state ---------------------------------------------
 template <typename E, int N, bool GATE, bool KEEP>
-__global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
-    const Place p = place_of(a, g);
+__global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws, unsigned blocks) {
+    if (blockIdx.x >= blocks) {
+        pass_through<N>(a, blockIdx.x - blocks, a.state_in, a.state_out);
+        return;
+    }
+    const Place p = place_of(a, g, blocks);
     if (!p.any) return;
     const Params<N> par(a, p.c);
     const int64_t row = (int64_t)p.row * a.T;
-    const E* x = reinterpret_cast<const E*>(a.x) + row * a.D;
-    const E* dt = reinterpret_cast<const E*>(a.dt) + row * a.D;
-    const E* z = reinterpret_cast<const E*>(a.z) + row * a.D;
-    E* out = reinterpret_cast<E*>(a.out) + row * a.D;
-    float* deltas = ws.delta + row * a.D;
     Sequences q(a.cu_seqlens, a.n_seq, a.T, p.row, p.t0);
     do {
         const int b = max(q.first, p.t0), e = min(q.end, p.t1);
@@ -344,23 +372,29 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(Sel
         auto run = [&](auto have) {
             constexpr bool HAVE = decltype(have)::value;
             typedef typename std::conditional<HAVE, float, E>::type DE;
+            const int64_t first = (row + b) * a.D;
+            const E *x = reinterpret_cast<const E*>(a.x) + first, *z = reinterpret_cast<const E*>(a.z) + first;
+            float* deltas = ws.delta + first;
+            E* to = reinterpret_cast<E*>(a.out) + first;
             const DE* from;
             if constexpr (HAVE) from = deltas;
-            else from = dt;
+            else from = reinterpret_cast<const E*>(a.dt) + first;
             constexpr int U = 4;
             E xs[2][U], zs[2][U];
             DE ds[2][U];
-            auto fetch = [&](int t, E (&xv)[U], DE (&dv)[U], E (&zv)[U]) {
+            auto fetch = [&](int t, E (&xv)[U], DE (&dv)[U], E (&zv)[U]) {      // called in the order of the tokens
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
-                    xv[u] = get_at(x + at, p.c);
-                    dv[u] = get_at(from + at, p.c);
-                    if constexpr (GATE) zv[u] = get_at(z + at, p.c);
+                    xv[u] = get_at(x, p.c);
+                    dv[u] = get_at(from, p.c);
+                    if constexpr (GATE) zv[u] = get_at(z, p.c);
+                    const int64_t step = t + u + 1 < e ? a.D : 0;
+                    x += step;
+                    from += step;
+                    z += step;
                 }
             };
             SharedWalk<E, N> B(reinterpret_cast<const E*>(a.Bm) + (row + b) * N), C(reinterpret_cast<const E*>(a.Cm) + (row + b) * N);
-            E* to = out + (int64_t)b * a.D;
             auto tokens = [&](int t, const E (&xv)[U], const DE (&dv)[U], const E (&zv)[U]) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -380,7 +414,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(Sel
                     if constexpr (!HAVE) {
                         delta = softplus(delta + par.bias);
                         if constexpr (KEEP) {
-                            if (p.in) put_at(deltas + (int64_t)(t + u) * a.D, p.c, delta);
+                            if (p.in) put_at(deltas, p.c, delta);
+                            deltas += a.D;
                         }
                     }
                     const float xf = to_f32(xv[u]), w = delta * xf;
@@ -414,24 +449,12 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_scan_kernel(Sel
     } while (q.end < p.t1 && q.next());
 }
 
-// The states of sequences without tokens, and their gradients: as they came.
-template <int N>
-__global__ __launch_bounds__(256) void kda_selective_empty_kernel(SelectiveArgs a, const float* from, float* to) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    const int64_t s = i / (a.D * N);
-    if (s >= a.n_seq) return;
-    int64_t first = 0, end = a.T;
-    if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.T, first, end);
-    if (first < end) return;
-    *reinterpret_cast<f32x4*>(to + i) = from ? *reinterpret_cast<const f32x4*>(from + i) : f32x4{0.f, 0.f, 0.f, 0.f};
-}
-
 // ---- the backward ------------------------------------------------------------------
 // 1. What a tile's tokens give the gradient of the state that enters it:
 //    sum_t exp(A sum_(s<=t) delta_s) C_t dy_t.
 template <typename E, int N, bool GATE>
 __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
-    const Place p = place_of(a, g, 1, 1);
+    const Place p = place_of(a, g, gridDim.x, 1, 1);
     if (!p.any) return;
     const Params<N> par(a, p.c);
     float r[N], sum = 0.f;
@@ -444,19 +467,23 @@ __global__ __launch_bounds__(kScanWaves * 64) void kda_selective_local_back_kern
         const int e = min(q.end, p.t1);
         const bool ends = q.end <= p.t1 && a.cu_seqlens;
         const int64_t row = (int64_t)p.row * a.T;
-        const float* deltas = ws.delta + row * a.D;
-        const E* z = reinterpret_cast<const E*>(a.z) + row * a.D;
-        const E* d_out = reinterpret_cast<const E*>(a.d_out ? a.d_out : a.x) + row * a.D;      // any that is there
+        const int64_t first = (row + p.t0) * a.D;
+        const float* deltas = ws.delta + first;
+        const E* z = reinterpret_cast<const E*>(a.z) + first;
+        const E* d_out = reinterpret_cast<const E*>(a.d_out ? a.d_out : a.x) + first;      // any that is there
         constexpr int U = 4;
         E gs[2][U], zs[2][U];
         float ds[2][U];
         auto fetch = [&](int t, E (&gv)[U], float (&dv)[U], E (&zv)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
-                gv[u] = get_at(d_out + at, p.c);
-                dv[u] = get_at(deltas + at, p.c);
-                if constexpr (GATE) zv[u] = get_at(z + at, p.c);
+                gv[u] = get_at(d_out, p.c);
+                dv[u] = get_at(deltas, p.c);
+                if constexpr (GATE) zv[u] = get_at(z, p.c);
+                const int64_t step = t + u + 1 < e ? a.D : 0;
+                d_out += step;
+                deltas += step;
+                z += step;
             }
         };
         SharedWalk<E, N> C(reinterpret_cast<const E*>(a.Cm) + (row + p.t0) * N);
@@ -543,9 +570,13 @@ __device__ __forceinline__ float sum_lanes(float (&v)[K / 2]) {
 // 2. Each tile from its last token to its first, half of kKeep tokens at a time,
 //    whose states are formed anew from the kept one and stay in registers.
 template <typename E, int N, bool GATE>
-__global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selective_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws) {
+__global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selective_back_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws, unsigned blocks) {
+    if (blockIdx.x >= blocks) {
+        pass_through<N>(a, blockIdx.x - blocks, a.d_state, a.d_state_in);
+        return;
+    }
     constexpr int KT = kKeep<N>, HT = KT / 2;
-    const Place p = place_of(a, g);
+    const Place p = place_of(a, g, blocks);
     if (!p.any) return;
     const int lane = threadIdx.x & 63;
     const Params<N> par(a, p.c);
@@ -592,7 +623,6 @@ __global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selectiv
                 }
 #pragma unroll
                 for (int u = 0; u < HT; ++u) {
-                    __builtin_amdgcn_sched_barrier(0);
                     Shared<E, N> B;
                     B.load(Bp + (int64_t)(t0 + u) * N);
                     const float w = df[u] * to_f32(xf[u]);
@@ -603,7 +633,6 @@ __global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selectiv
 #pragma unroll
             for (int u = 0; u < HT; ++u) {
                 if (u >= m) continue;
-                __builtin_amdgcn_sched_barrier(0);
                 Shared<E, N> B;
                 B.load(Bp + (int64_t)(tb + u) * N);
                 const float w = delta[u] * to_f32(xs[u]);
@@ -613,7 +642,6 @@ __global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selectiv
 #pragma unroll
             for (int u = HT - 1; u >= 0; --u) {
                 if (u >= m) continue;
-                __builtin_amdgcn_sched_barrier(0);       // one token's values at a time: together they spill
                 const int t = tb + u;
                 Shared<E, N> B, C;
                 B.load(Bp + (int64_t)t * N);
@@ -665,13 +693,14 @@ __global__ __launch_bounds__(kScanWaves * 64, N == 32 ? 1 : 2) void kda_selectiv
     }
 }
 
-// 3. The parameters' gradients: sums over the tiles in their order, in 64 bits,
-//    as there can be any number.
-__global__ __launch_bounds__(256) void kda_selective_param_sum_kernel(SelectiveArgs a, const float* parts, int64_t count, int blocks) {
+// 3. The parameters' gradients: sums over the tiles in their order, 64 channels of
+//    one a workgroup, whose waves have every fourth tile.  In 64 bits, as there can
+//    be any number.
+__device__ __forceinline__ void sum_params(const SelectiveArgs& a, const ScanGrid& g, const float* parts, int64_t count, unsigned block) {
     __shared__ double sum[kScanWaves][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t c = (int64_t)(blockIdx.x % blocks) * 64 + lane;
-    const int j = blockIdx.x / blocks;
+    const int64_t c = (int64_t)(block % g.blocks) * 64 + lane;
+    const int j = block / g.blocks;
     float* to = j < a.states ? a.dA + c * a.states + j : (j == a.states ? a.dskip : a.ddt_bias);
     if (!to) return;
     if (j >= a.states) to += c;
@@ -690,11 +719,17 @@ __global__ __launch_bounds__(256) void kda_selective_param_sum_kernel(SelectiveA
     *to = (float)s;
 }
 
-//    dB and dC: sums over the channel blocks in their order.
+//    dB and dC: sums over the channel blocks in their order, by the workgroups
+//    behind those of the parameters.
 template <typename E>
-__global__ __launch_bounds__(256) void kda_selective_shared_sum_kernel(SelectiveArgs a, const float* parts, int blocks) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void kda_selective_sum_kernel(SelectiveArgs a, ScanGrid g, ScanWorkspace ws, int64_t count) {
     const int N = a.states;
+    const unsigned params = (unsigned)g.blocks * (N + 2);
+    if (blockIdx.x < params) {
+        sum_params(a, g, ws.params, count, blockIdx.x);
+        return;
+    }
+    const int64_t i = (int64_t)(blockIdx.x - params) * 256 + threadIdx.x;
     const int64_t row = i / (2 * N), rows = a.B * a.T;
     const int n = (int)(i - row * 2 * N);
     if (row >= rows) return;
@@ -706,7 +741,7 @@ __global__ __launch_bounds__(256) void kda_selective_shared_sum_kernel(Selective
     }
     float s = 0.f;
 #pragma unroll 8
-    for (int b = 0; b < blocks; ++b) s += parts[(b * rows + row) * 2 * N + n];
+    for (int b = 0; b < g.blocks; ++b) s += ws.shared[(b * rows + row) * 2 * N + n];
     E* to = reinterpret_cast<E*>(n < N ? a.dB : a.dC);
     to[row * N + (n < N ? n : n - N)] = from_f32<E>(s);
 }
@@ -788,32 +823,46 @@ size_t lay_out(const SelectiveArgs& a, bool backward, char* at, ScanWorkspace& w
     return used;
 }
 
-dim3 grid(int64_t waves) {
+unsigned tile_blocks(int64_t waves) {
     const int64_t blocks = (waves + kScanWaves - 1) / kScanWaves;
-    return dim3((unsigned)((blocks + kXcds - 1) / kXcds * kXcds));
+    return (unsigned)((blocks + kXcds - 1) / kXcds * kXcds);
+}
+
+// Workgroups for the sequences that may have no tokens, where their states go
+// from one array to another.
+unsigned through_blocks(const SelectiveArgs& a, const float* from, const float* to) {
+    const bool some = to && from != to && a.n_seq > 0 && (a.cu_seqlens || a.T == 0);
+    return some ? (unsigned)((a.n_seq + kScanWaves - 1) / kScanWaves) : 0u;
+}
+
+// Two waves have 32 tiles at a time, which is all of them in a training pass of 4 x
+// 4096 tokens of 2048 channels (10 us; eight waves 21); eight 128 (16384 tokens of
+// 515 channels, 256 tiles: 7 us; two 23).
+template <int N, bool BACK>
+hipError_t launch_join(const SelectiveArgs& a, const ScanGrid& g, const ScanWorkspace& ws, hipStream_t s) {
+    const dim3 grid((unsigned)(a.B * g.blocks * N));
+    if (g.tiles <= 4 * kJoin) hipLaunchKernelGGL((kda_selective_join_kernel<N, BACK, 2>), grid, dim3(128), 0, s, a, g, ws);
+    else hipLaunchKernelGGL((kda_selective_join_kernel<N, BACK, 8>), grid, dim3(512), 0, s, a, g, ws);
+    return hipGetLastError();
 }
 
 template <typename E, int N>
 hipError_t scan_forward(const SelectiveArgs& a, hipStream_t s) {
     hipError_t e;
-    if (a.B > 0 && a.T > 0) {
-        const ScanGrid g = scan_grid(a);
-        ScanWorkspace ws;
-        lay_out(a, a.keep, a.ws, ws);
-        const dim3 block(kScanWaves * 64);
-        if (g.tiles > 1) {
-            hipLaunchKernelGGL((kda_selective_local_kernel<E, N>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            hipLaunchKernelGGL((kda_selective_join_kernel<N, false>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
-        const auto kernel = a.z ? (a.keep ? kda_selective_scan_kernel<E, N, true, true> : kda_selective_scan_kernel<E, N, true, false>)
-                                : (a.keep ? kda_selective_scan_kernel<E, N, false, true> : kda_selective_scan_kernel<E, N, false, false>);
-        hipLaunchKernelGGL(kernel, grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+    const ScanGrid g = scan_grid(a);
+    ScanWorkspace ws;
+    lay_out(a, a.keep, a.ws, ws);
+    const dim3 block(kScanWaves * 64);
+    if (g.tiles > 1) {
+        hipLaunchKernelGGL((kda_selective_local_kernel<E, N>), dim3(tile_blocks(a.B * (g.tiles - 1) * g.blocks)), block, 0, s, a, g, ws);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        if ((e = launch_join<N, false>(a, g, ws, s)) != hipSuccess) return e;
     }
-    if (!a.state_out || a.state_out == a.state_in || a.n_seq == 0 || (!a.cu_seqlens && a.T > 0)) return hipSuccess;
-    hipLaunchKernelGGL((kda_selective_empty_kernel<N>), dim3((unsigned)((a.n_seq * a.D * N / 4 + 255) / 256)), dim3(256), 0, s, a, a.state_in, a.state_out);
+    const unsigned blocks = tile_blocks(a.B * g.tiles * g.blocks), more = through_blocks(a, a.state_in, a.state_out);
+    if (blocks + more == 0) return hipSuccess;
+    const auto kernel = a.z ? (a.keep ? kda_selective_scan_kernel<E, N, true, true> : kda_selective_scan_kernel<E, N, true, false>)
+                            : (a.keep ? kda_selective_scan_kernel<E, N, false, true> : kda_selective_scan_kernel<E, N, false, false>);
+    hipLaunchKernelGGL(kernel, dim3(blocks + more), block, 0, s, a, g, ws, blocks);
     return hipGetLastError();
 }
 
@@ -824,23 +873,21 @@ hipError_t scan_backward(const SelectiveArgs& a, hipStream_t s) {
     ScanWorkspace ws;
     lay_out(a, true, a.ws, ws);
     const dim3 block(kScanWaves * 64);
-    const bool any = a.B > 0 && a.T > 0 && a.n_seq > 0;
-    if (any) {
-        if (g.tiles > 1) {
-            hipLaunchKernelGGL((a.z ? kda_selective_local_back_kernel<E, N, true> : kda_selective_local_back_kernel<E, N, false>), grid(a.B * (g.tiles - 1) * g.blocks), block, 0, s, a, g, ws);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            hipLaunchKernelGGL((kda_selective_join_kernel<N, true>), grid(a.B * g.blocks * N), block, 0, s, a, g, ws);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
-        hipLaunchKernelGGL((a.z ? kda_selective_back_kernel<E, N, true> : kda_selective_back_kernel<E, N, false>), grid(a.B * g.tiles * g.blocks), block, 0, s, a, g, ws);
+    const int64_t waves = a.n_seq > 0 ? a.B * g.tiles * g.blocks : 0;
+    if (waves > 0 && g.tiles > 1) {
+        hipLaunchKernelGGL((a.z ? kda_selective_local_back_kernel<E, N, true> : kda_selective_local_back_kernel<E, N, false>),
+                           dim3(tile_blocks(a.B * (g.tiles - 1) * g.blocks)), block, 0, s, a, g, ws);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL((kda_selective_shared_sum_kernel<E>), dim3((unsigned)((a.B * a.T * 2 * N + 255) / 256)), dim3(256), 0, s, a, ws.shared, g.blocks);
+        if ((e = launch_join<N, true>(a, g, ws, s)) != hipSuccess) return e;
+    }
+    const unsigned blocks = tile_blocks(waves), more = through_blocks(a, a.d_state, a.d_state_in);
+    if (blocks + more > 0) {
+        hipLaunchKernelGGL((a.z ? kda_selective_back_kernel<E, N, true> : kda_selective_back_kernel<E, N, false>), dim3(blocks + more), block, 0, s, a, g, ws,
+                           blocks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kda_selective_param_sum_kernel, dim3((unsigned)(g.blocks * (N + 2))), dim3(256), 0, s, a, ws.params, any ? a.B * g.tiles : 0, g.blocks);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (!a.d_state_in || a.n_seq == 0 || (!a.cu_seqlens && a.T > 0)) return hipSuccess;
-    hipLaunchKernelGGL((kda_selective_empty_kernel<N>), dim3((unsigned)((a.n_seq * a.D * N / 4 + 255) / 256)), dim3(256), 0, s, a, a.d_state, a.d_state_in);
+    const int64_t rows = waves > 0 ? (a.B * a.T * 2 * N + 255) / 256 : 0;
+    hipLaunchKernelGGL((kda_selective_sum_kernel<E>), dim3((unsigned)(g.blocks * (N + 2) + rows)), dim3(256), 0, s, a, g, ws, waves > 0 ? a.B * g.tiles : 0);
     return hipGetLastError();
 }
 
@@ -864,9 +911,9 @@ hipError_t by_states(bool bf16, int states, F&& f) {
 
 bool selective_scan_fits(const SelectiveArgs& a) {
     const ScanGrid g = scan_grid(a);
-    const int64_t most = UINT32_MAX / 256;      // workgroups of 256
-    return a.B * g.tiles * g.blocks / kScanWaves < most - kXcds && a.B * g.blocks * a.states / kScanWaves < most - kXcds && a.B * a.T * 2 * a.states / 256 < most &&
-           a.n_seq * a.D * (a.states / 4) / 256 < most && (int64_t)g.blocks * (a.states + 2) < most;
+    const int64_t most = UINT32_MAX / 256 - kXcds;      // workgroups of 256
+    return a.B * g.tiles * g.blocks / kScanWaves + a.n_seq / kScanWaves < most && (g.tiles < 2 || a.B * g.blocks * a.states < most / 2) &&
+           a.B * a.T * 2 * a.states / 256 + (int64_t)g.blocks * (a.states + 2) < most;
 }
 
 size_t selective_scan_workspace_bytes(const SelectiveArgs& a, bool backward) {

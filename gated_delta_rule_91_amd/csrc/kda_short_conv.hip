@@ -108,8 +108,37 @@ __device__ __forceinline__ void convolve(const Filter<W, V>& f, float (&win)[W -
     }
 }
 
+// The last W - 1 inputs of every sequence, a channel a thread.  state_out may
+// be state_in: a thread reads all that it needs of a state before it writes.
+template <typename E, int W>
+__device__ __forceinline__ void write_states(const ShortConvArgs& a, int64_t block) {
+    const int64_t i = block * 256 + threadIdx.x;
+    const int64_t s = i / a.D, c = i % a.D;
+    if (s >= a.n_seq) return;
+    int64_t first = 0, end = a.T, base = s * a.T * a.D;
+    if (a.cu_seqlens) {
+        seq_bounds(a.cu_seqlens, s, a.T, first, end);
+        base = 0;
+    }
+    E last[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t at = end - (W - 1) + j;
+        last[j] = (E)0.f;
+        if (at >= first) last[j] = reinterpret_cast<const E*>(a.x)[base + at * a.D + c];
+        else if (a.state_in) last[j] = reinterpret_cast<const E*>(a.state_in)[(s * (W - 1) + (at - first + W - 1)) * a.D + c];
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) reinterpret_cast<E*>(a.state_out)[(s * (W - 1) + j) * a.D + c] = last[j];
+}
+
+// The workgroups from `blocks` on write the states.
 template <typename E, int W, int V>
-__global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_kernel(ShortConvArgs a, int tile, int tiles, int chunks) {
+__global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_kernel(ShortConvArgs a, int tile, int tiles, int chunks, unsigned blocks) {
+    if (blockIdx.x >= blocks) {
+        write_states<E, W>(a, blockIdx.x - blocks);
+        return;
+    }
     const ConvTile r = conv_tile<V>(a, tile, tiles, chunks);
     if (!r.any) return;
     const int64_t base = (int64_t)r.row * a.T * a.D;
@@ -151,30 +180,6 @@ __global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_kernel(ShortCo
     } while (q.end < r.t1 && q.next());
 }
 
-// The last W - 1 inputs of every sequence, a channel a thread.  state_out may
-// be state_in: a thread reads all that it needs of a state before it writes.
-template <typename E, int W>
-__global__ __launch_bounds__(256) void kda_short_conv_state_kernel(ShortConvArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t s = i / a.D, c = i % a.D;
-    if (s >= a.n_seq) return;
-    int64_t first = 0, end = a.T, base = s * a.T * a.D;
-    if (a.cu_seqlens) {
-        seq_bounds(a.cu_seqlens, s, a.T, first, end);
-        base = 0;
-    }
-    E last[W - 1];
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int64_t at = end - (W - 1) + j;
-        last[j] = (E)0.f;
-        if (at >= first) last[j] = reinterpret_cast<const E*>(a.x)[base + at * a.D + c];
-        else if (a.state_in) last[j] = reinterpret_cast<const E*>(a.state_in)[(s * (W - 1) + (at - first + W - 1)) * a.D + c];
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) reinterpret_cast<E*>(a.state_out)[(s * (W - 1) + j) * a.D + c] = last[j];
-}
-
 // A tile's tokens [b, e) of a sequence need d up to e + W - 2, as dx_p does.
 // Walking t from b on, the newest d gives dx of p = t - (W - 1), which before a
 // sequence's first token is the gradient of its state.
@@ -201,43 +206,38 @@ __global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_backward_kerne
         for (int j = 0; j < W - 1; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) dwin[j][v] = 0.f;
-        const int64_t at0 = base + r.c;
-        const E* x = reinterpret_cast<const E*>(a.x) + at0;
-        const E* g = reinterpret_cast<const E*>(a.d_out);
+        const E* x = reinterpret_cast<const E*>(a.x) + base + r.c;
+        const E* g = reinterpret_cast<const E*>(a.d_out ? a.d_out : a.x) + base + r.c;       // any that is there
         const bool begins = b == q.first;
         const int behind = q.end - (W - 1);         // the first of the last W - 1 inputs
-        // d of token t, 0 behind the last; COUNTS: t is one of the tile's own
-        auto token = [&](int t, bool counts, const Channels<E, V>& xin, const Channels<E, V>& gin) {
-            float d[V];
-            if (t < q.end) {
-                float now[V], y[V], old[W - 1][V];
+        // d of a token; OWN: it is one of the tile's
+        auto gradient = [&](auto own, const Channels<E, V>& xin, const Channels<E, V>& gin, float (&d)[V]) {
+            float now[V], y[V], old[W - 1][V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                now[v] = xin[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) old[j][v] = win[j][v];
+            }
+            convolve<W, V>(f, win, now, y);
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = a.d_out ? gin[v] : 0.f;
+            if (a.silu) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] *= silu_slope(y[v]);
+            }
+            if constexpr (decltype(own)::value) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    now[v] = xin[v];
+                    db[v] += d[v];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) old[j][v] = win[j][v];
+                    for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(d[v], old[j][v], dw[j][v]);
+                    dw[W - 1][v] = fmaf(d[v], now[v], dw[W - 1][v]);
                 }
-                convolve<W, V>(f, win, now, y);
-#pragma unroll
-                for (int v = 0; v < V; ++v) d[v] = g ? gin[v] : 0.f;
-                if (a.silu) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) d[v] *= silu_slope(y[v]);
-                }
-                if (counts) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        db[v] += d[v];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][v] = fmaf(d[v], old[j][v], dw[j][v]);
-                        dw[W - 1][v] = fmaf(d[v], now[v], dw[W - 1][v]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) d[v] = 0.f;
             }
-            const int p = t - (W - 1);
+        };
+        // the gradient of the input at p = t - (W - 1), from d of token t on
+        auto emit = [&](int p, const float (&d)[V]) {
             if (p >= b || begins) {
                 float s[V];
 #pragma unroll
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_backward_kerne
 #pragma unroll
                     for (int v = 0; v < V; ++v) s[v] += more[v];
                 }
-                if (p >= q.first) put_channels<E, V>(reinterpret_cast<E*>(a.dx) + at0 + (int64_t)p * a.D, s);
+                if (p >= q.first) put_channels<E, V>(reinterpret_cast<E*>(a.dx) + base + r.c + (int64_t)p * a.D, s);
                 else if (a.d_state_in) put_channels<E, V>(reinterpret_cast<E*>(a.d_state_in) + ((int64_t)q.s * (W - 1) + (p - q.first + W - 1)) * a.D + r.c, s);
             }
 #pragma unroll
@@ -261,19 +261,37 @@ __global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_backward_kerne
                 dwin[W - 2][v] = d[v];
             }
         };
-        constexpr int U = 4;
-        const int stop = e + W - 1;
-        for (int t = b; t < stop; t += U) {
-            Channels<E, V> xin[U] = {}, gin[U] = {};
+        constexpr int U = 8;                // tokens on their way together
+        for (int t = b; t < e; t += U) {
+            Channels<E, V> xin[U], gin[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < min(stop, q.end)) {
-                    xin[u] = get_channels<E, V>(x + (int64_t)(t + u) * a.D);
-                    if (g) gin[u] = get_channels<E, V>(g + at0 + (int64_t)(t + u) * a.D);
-                }
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)min(t + u, e - 1) * a.D;
+                xin[u] = get_channels<E, V>(x + at);
+                gin[u] = get_channels<E, V>(g + at);
+            }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < stop) token(t + u, t + u < e, xin[u], gin[u]);
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= e) break;
+                float d[V];
+                gradient(std::true_type{}, xin[u], gin[u], d);
+                emit(t + u - (W - 1), d);
+            }
+        }
+        Channels<E, V> xin[W - 1], gin[W - 1];
+#pragma unroll
+        for (int u = 0; u < W - 1; ++u) {
+            const int64_t at = (int64_t)min(e + u, q.end - 1) * a.D;
+            xin[u] = get_channels<E, V>(x + at);
+            gin[u] = get_channels<E, V>(g + at);
+        }
+#pragma unroll
+        for (int u = 0; u < W - 1; ++u) {
+            float d[V];
+            gradient(std::false_type{}, xin[u], gin[u], d);
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = e + u < q.end ? d[v] : 0.f;
+            emit(e + u - (W - 1), d);
         }
     } while (q.end < r.t1 && q.next());
     // [tile][weights, bias][channel]
@@ -283,33 +301,30 @@ __global__ __launch_bounds__(kConvWaves * 64) void kda_short_conv_backward_kerne
     put_channels<float, V>(to + W * a.D, db);
 }
 
-// The gradient of the state of a sequence without tokens.
+// The weights' gradients: sums over the tiles in their order, 64 channels of one
+// weight a workgroup, whose waves have every fourth tile.  In 64 bits, as there
+// can be any number.  The workgroups behind those pass the gradients of the states
+// of sequences without tokens through, a wave for each sequence.
 template <typename E, int W>
-__global__ __launch_bounds__(256) void kda_short_conv_empty_kernel(ShortConvArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t s = i / a.D, c = i % a.D;
-    if (s >= a.n_seq) return;
-    int64_t first = 0, end = a.T;
-    if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.T, first, end);
-    if (first < end) return;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int64_t at = (s * (W - 1) + j) * a.D + c;
-        reinterpret_cast<E*>(a.d_state_in)[at] = a.d_state ? reinterpret_cast<const E*>(a.d_state)[at] : (E)0.f;
-    }
-}
-
-// Sums over the tiles in their order, 64 channels of one weight a workgroup,
-// whose waves have every fourth tile.  In 64 bits, as there can be any number.
-__global__ __launch_bounds__(256) void kda_short_conv_sum_kernel(ShortConvArgs a, int64_t parts, int blocks) {
+__global__ __launch_bounds__(256) void kda_short_conv_sum_kernel(ShortConvArgs a, int64_t parts, int blocks, unsigned sums) {
     __shared__ double sum[kConvWaves][64];
     const int lane = threadIdx.x & 63, wave = wave_of_block();
+    if (blockIdx.x >= sums) {
+        const int64_t s = (int64_t)(blockIdx.x - sums) * kConvWaves + wave, each = (W - 1) * a.D;
+        if (s >= a.n_seq) return;
+        int64_t first = 0, end = a.T;
+        if (a.cu_seqlens) seq_bounds(a.cu_seqlens, s, a.T, first, end);
+        if (first < end) return;
+        for (int64_t i = s * each + lane; i < (s + 1) * each; i += 64)
+            reinterpret_cast<E*>(a.d_state_in)[i] = a.d_state ? reinterpret_cast<const E*>(a.d_state)[i] : (E)0.f;
+        return;
+    }
     const int64_t c = (int64_t)(blockIdx.x % blocks) * 64 + lane;
     const int j = blockIdx.x / blocks;
     double s = 0.;
     if (c < a.D) {
         const float* from = a.parts + (int64_t)j * a.D + c;
-        const int64_t stride = (a.taps + 1) * a.D;
+        const int64_t stride = (W + 1) * a.D;
 #pragma unroll 8
         for (int64_t i = wave; i < parts; i += kConvWaves) s += from[i * stride];
     }
@@ -318,7 +333,7 @@ __global__ __launch_bounds__(256) void kda_short_conv_sum_kernel(ShortConvArgs a
     if (wave != 0 || c >= a.D) return;
 #pragma unroll
     for (int w = 1; w < kConvWaves; ++w) s += sum[w][lane];
-    if (j < a.taps) a.dweight[c * a.taps + j] = (float)s;
+    if (j < W) a.dweight[c * W + j] = (float)s;
     else a.dbias[c] = (float)s;
 }
 
@@ -365,23 +380,17 @@ ConvPlan conv_plan(const ShortConvArgs& a, int vec) {
 }
 
 template <typename E, int W>
-hipError_t conv_states(const ShortConvArgs& a, hipStream_t s) {
-    if (!a.state_out || a.n_seq == 0) return hipSuccess;
-    hipLaunchKernelGGL((kda_short_conv_state_kernel<E, W>), dim3((unsigned)((a.n_seq * a.D + 255) / 256)), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-template <typename E, int W>
 hipError_t conv_forward(const ShortConvArgs& a, hipStream_t s) {
-    if (a.B > 0 && a.T > 0 && a.n_seq > 0) {
-        const ConvPlan p = conv_plan(a, kForward<E>);
-        const dim3 grid((unsigned)p.blocks), block(kConvWaves * 64);
-        if (a.D >= kForward<E>) hipLaunchKernelGGL((kda_short_conv_kernel<E, W, kForward<E>>), grid, block, 0, s, a, p.tile, p.tiles, p.chunks);
-        else hipLaunchKernelGGL((kda_short_conv_kernel<E, W, 1>), grid, block, 0, s, a, p.tile, p.tiles, p.chunks);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return conv_states<E, W>(a, s);
+    const ConvPlan p = conv_plan(a, kForward<E>);
+    const unsigned blocks = a.n_seq > 0 ? (unsigned)p.blocks : 0u, states = a.state_out ? (unsigned)((a.n_seq * a.D + 255) / 256) : 0u;
+    const auto kernel = a.D >= kForward<E> ? kda_short_conv_kernel<E, W, kForward<E>> : kda_short_conv_kernel<E, W, 1>;
+    // a state that is written in place may still be read by the tiles
+    const bool apart = a.state_out == a.state_in && blocks > 0 && states > 0;
+    if (blocks + states > 0) hipLaunchKernelGGL(kernel, dim3(apart ? blocks : blocks + states), dim3(kConvWaves * 64), 0, s, a, p.tile, p.tiles, p.chunks, blocks);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !apart) return e;
+    hipLaunchKernelGGL(kernel, dim3(states), dim3(kConvWaves * 64), 0, s, a, p.tile, p.tiles, p.chunks, 0u);
+    return hipGetLastError();
 }
 
 template <typename E, int W>
@@ -396,10 +405,9 @@ hipError_t conv_backward(const ShortConvArgs& a, hipStream_t s) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int blocks = (int)((a.D + 63) / 64);
-    hipLaunchKernelGGL(kda_short_conv_sum_kernel, dim3((unsigned)(blocks * (W + (a.dbias ? 1 : 0)))), dim3(256), 0, s, a, any ? a.B * p.tiles : 0, blocks);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (a.d_state_in && a.n_seq > 0 && (a.cu_seqlens || a.T == 0))
-        hipLaunchKernelGGL((kda_short_conv_empty_kernel<E, W>), dim3((unsigned)((a.n_seq * a.D + 255) / 256)), dim3(256), 0, s, a);
+    const unsigned sums = (unsigned)(blocks * (W + (a.dbias ? 1 : 0)));
+    const unsigned through = a.d_state_in && (a.cu_seqlens || a.T == 0) ? (unsigned)((a.n_seq + kConvWaves - 1) / kConvWaves) : 0u;
+    hipLaunchKernelGGL((kda_short_conv_sum_kernel<E, W>), dim3(sums + through), dim3(256), 0, s, a, any ? a.B * p.tiles : 0, blocks, sums);
     return hipGetLastError();
 }
 
@@ -424,8 +432,8 @@ hipError_t by_taps(int taps, F&& f) {
 
 bool short_conv_fits(const ShortConvArgs& a, bool bf16) {
     const int64_t most = UINT32_MAX / (kConvWaves * 64);
-    return conv_plan(a, bf16 ? kForward<__bf16> : kForward<float>).blocks <= most && conv_plan(a, kBackward).blocks <= most &&
-           (a.n_seq * a.D + 255) / 256 <= most && (a.D + 63) / 64 * (a.taps + 1) <= most;
+    return conv_plan(a, bf16 ? kForward<__bf16> : kForward<float>).blocks + (a.n_seq * a.D + 255) / 256 <= most &&
+           conv_plan(a, kBackward).blocks <= most && (a.D + 63) / 64 * (a.taps + 1) + a.n_seq / kConvWaves < most;
 }
 
 size_t short_conv_backward_workspace_bytes(const ShortConvArgs& a, bool) {
