@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.hip", "kda_prepare.hip", "kda_scan.hip", "kda_scan_wave.hip", "kda_decode.hip", "kda_combine.hip", "kda_backward.hip",
-           "kda_hybrid_api.hip", "kda_plan.hip", "kda_cache4.hip", "kda_cache4_attention.hip", "kda_cache4_shared.hip", "kda_recurrence.hip",
+           "kda_hybrid_api.hip", "kda_plan.hip", "kda_cache4.hip", "kda_cache4_attention.hip", "kda_cache4_shared.hip",
+           "kda_cache4_shared_f32.hip", "kda_recurrence.hip",
            "kda_selective_api.hip", "kda_short_conv.hip", "kda_selective_scan.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -46,9 +46,9 @@
 // does not hold whole is a part; a second kernel joins the parts.
 //
 // A prefix that several sequences share is taken apart: over its tokens a group of
-// sequences is one with all their queries, which see all of it (PREFIX: a row's
-// maximum, sum and channels go to an array), over the others each is by itself
-// from its start on (OWN: joined with what the array holds).
+// sequences is one with all their queries, which see all of it (PREFIX), over the
+// others each is by itself from its start on (OWN).  A row's maximum, sum and
+// channels of either go to arrays, which kda_cache4_shared.hpp joins.
 #pragma once
 
 #include <type_traits>
@@ -75,6 +75,9 @@ constexpr int kUnit = 128;         // tokens that are dealt out at once
 // 256 ragged contexts above take 83 us with 2, 77 with 3, 82 with 6, the
 // prompts 195, 201 and 204.
 constexpr int kBlockCost = 4;
+// The same where waves work alone: 256 sequences of up to 1000 tokens behind 8192,
+// 32 heads over 8 of 128, take 84 us with 1, 86 with 2, 87 with 4.
+constexpr int kAloneCost = 1;
 constexpr int kMaxDealt = 4096;    // row blocks whose prefix sums lie in LDS; more fill the card as they are
 // Units that can be dealt out: a workgroup's end, at most a unit for each of
 // the workgroups (768) past all of them, is a 32-bit number too.
@@ -90,8 +93,14 @@ struct PartArgs : Cache4AttentionArgs {
     const int32_t* starts;       // OWN: the first token that counts, of each sequence
     const int32_t* table_rows;   // PREFIX: the row of block_table of each group
     int tables;                  // rows of block_table
-    float* row_o;                // [tokens, heads, d]: sums over the prefix
-    float* row_sums;             // [tokens, heads, 2]: their maxima and sums of weights
+    float* row_o;                // [tokens, heads, d]: weighted values of rows that one workgroup has, unless output
+    struct Row* rows;            // [tokens, heads]
+};
+// What a launch over a part of the tokens leaves of a row and head.
+struct __align__(16) Row {
+    float mx, sum;   // where one workgroup has it: maximum and sum of weights
+    int first;       // the place of its first part where several have it (see Layout)
+    int count;       // 1, or its parts, 0: it is output already; OWN: negative, there is no prefix
 };
 template <Which W> struct ArgsOf { typedef PartArgs type; };
 template <> struct ArgsOf<WHOLE> { typedef Cache4AttentionArgs type; };
@@ -109,13 +118,13 @@ struct Layout {
 // 2 w + 1 of one that begins in it and goes on.  Part i of row r of a block and
 // key/value head h is at (i * heads + h) * rows + r.  The second kernel finds
 // the blocks that several workgroups have by their cuts, of which there are
-// as many as slots or workgroups, whichever are fewer.
+// as many as slots or workgroups, whichever are fewer; those of a part of the
+// tokens by what it leaves of each row.
 struct Cut {
     int row0;        // first row of q of its sequence
     int n_rows;      // (query, head) rows of its sequence, 0: there is no such block
     int begin;       // its first one of them
     int from, last;  // first and last workgroup that have a part of it
-    int start;       // OWN: the first token that counts
 };
 struct Parts {
     Cut* cut;        // [slots or groups]
@@ -198,7 +207,7 @@ __device__ __forceinline__ int place_of(const Cache4AttentionArgs& a, int row0, 
 // those of all.  A block with rows has one of its own at least, though its
 // output may be zeros.  of[i]: the sequence of slot i.  cu: LDS for n_seq + 1
 // offsets, which are searched there.
-template <Which W>
+template <Which W, int COST>
 __device__ int deal_out(const typename ArgsOf<W>::type& a, const Layout& l, int32_t* before, uint16_t* of, int32_t* cu) {
     __shared__ int32_t part[kWaves];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -213,7 +222,7 @@ __device__ int deal_out(const typename ArgsOf<W>::type& a, const Layout& l, int3
             const int s = sequence_at(a, l, cu, base + t);
             const Block b = block_of<W>(a, l, s, base + t);
             of[base + t] = (uint16_t)s;
-            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) - b.tile0() + kUnit - 1) / kUnit, 1) + kBlockCost;
+            if (b.any) c = max((end_of(a, b, min(b.begin + l.rows, b.n_rows) - 1) - b.tile0() + kUnit - 1) / kUnit, 1) + COST;
         }
         int in = c;
 #pragma unroll
@@ -514,37 +523,29 @@ constexpr int waves_of(bool bf16, int d, int r) {
     return r == 2 && d == 128 ? 1 : 2;
 }
 
-// N channels from c0 on of a row's share of a prefix, for the launch that
-// computes the rest; mx and sum stand before the channels' array.
-template <int D, int N>
-__device__ __forceinline__ void put_row(const PartArgs& a, int64_t at, int c0, const float (&y)[N], float mx, float sum) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) a.row_o[at * D + c0 + e] = y[e];
-    if (c0 == 0) *reinterpret_cast<f32x2*>(a.row_sums + 2 * at) = f32x2{mx, sum};
-}
+// LDS of a workgroup besides its dynamic part.
+template <int D, int R, bool SPLITW>
+struct Room {
+    static constexpr int ROWS = 16 * R, LD = D + 4;
+    alignas(16) float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD];
+    float sm[SPLITW ? kWaves : 1][ROWS], ss[SPLITW ? kWaves : 1][ROWS];
+    int odd[2][2];              // many rows: whether values of 32 tokens were left out (see below)
+};
 
-// The same joined with the rest's, y, mx and sum.
-template <int D, int N>
-__device__ __forceinline__ void join_row(const PartArgs& a, int64_t at, int c0, float (&y)[N], float mx, float& sum) {
-    const f32x2 other = *reinterpret_cast<const f32x2*>(a.row_sums + 2 * at);
-    const float most = fmaxf(mx, other[0]);
-    const float w0 = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - most), w1 = other[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(other[0] - most);
-    sum = w0 * sum + w1 * other[1];
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = w0 * y[e] + w1 * a.row_o[at * D + c0 + e];
-}
-
-template <typename E, int D, int R, bool SPLITW, Which W>
-__global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void kda_cache4_attention_kernel(typename ArgsOf<W>::type a, Layout l, Parts parts) {
+// ALONE: the waves of a workgroup have units of their own.
+template <typename E, int D, int R, bool SPLITW, bool ALONE, Which W>
+__device__ __forceinline__ void attend(const typename ArgsOf<W>::type& a, const Layout& l, const Parts& parts, Room<D, R, SPLITW>& room, char* dynamic,
+                                       unsigned workgroup) {
     constexpr int PARTS = sizeof(E) == 2 ? 1 : 3;
     constexpr int KS = D / 32;          // MFMA steps over the channels
     constexpr int VJ = D / 16;          // MFMAs of a value tile
     constexpr int PER = D / 4;          // channels of a lane's result
     constexpr int ROWS = 16 * R;        // rows of a wave
-    constexpr int LD = D + 4;
-    __shared__ __align__(16) float so[SPLITW ? kWaves : 1][SPLITW ? ROWS : 1][LD], sm[kWaves][ROWS], ss[kWaves][ROWS];
-    // many rows: the converted tiles, two of 64 tokens in turn; then the prefix sums
-    extern __shared__ __align__(16) char dynamic[];
+    constexpr int COST = ALONE ? kAloneCost : kBlockCost;
+    auto& so = room.so;
+    auto& sm = room.sm;
+    auto& ss = room.ss;
+    // dynamic: many rows' converted tiles, two of 64 tokens in turn; then the prefix sums
     int32_t* before = reinterpret_cast<int32_t*>(dynamic + (SPLITW ? 0 : shared_tiles(D)));
     uint16_t* of = reinterpret_cast<uint16_t*>(before + l.slots + 1);
     static_assert((SPLITW ? sizeof(so) : shared_tiles(D)) >= (kMaxDealt + 1) * sizeof(int32_t), "the offsets lie there for a while");
@@ -552,16 +553,20 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
 
     // key/value heads alternate fastest, so workgroups that share keys and
     // values lie on one XCD where there are 8 heads
-    const int kvh = (int)(blockIdx.x % a.c.heads), group = (int)(blockIdx.x / a.c.heads);
+    const int kvh = (int)(workgroup % a.c.heads);
+    const int group = (int)(workgroup / a.c.heads) * (ALONE ? kWaves : 1) + (ALONE ? wave : 0);
+    const int thread = ALONE ? lane : threadIdx.x, threads = ALONE ? 64 : kWaves * 64;       // of those that have the same units
     int slot = group;
     int at = 0, stop = 1, each = 1;     // this workgroup's units
     if (l.groups > 0) {
-        const int all = deal_out<W>(a, l, before, of, reinterpret_cast<int32_t*>(SPLITW ? reinterpret_cast<char*>(so) : dynamic));
+        const int all = deal_out<W, COST>(a, l, before, of, reinterpret_cast<int32_t*>(SPLITW ? reinterpret_cast<char*>(so) : dynamic));
         each = max((all + l.groups - 1) / l.groups, 1);
-        if (kvh == 0 && !l.by_slot) {
-            if (threadIdx.x == 0) parts.cut[group] = Cut{};
+        if (W != WHOLE) {
+            // rows tell where their parts are
+        } else if (kvh == 0 && !l.by_slot) {
+            if (thread == 0) parts.cut[group] = Cut{};
         } else if (kvh == 0 && group == 0) {
-            for (int i = threadIdx.x; i < l.slots; i += kWaves * 64)
+            for (int i = thread; i < l.slots; i += threads)
                 if (before[i] == before[i + 1]) parts.cut[i] = Cut{};      // the others have a workgroup that writes them
         }
         at = (int)min((int64_t)group * each, (int64_t)all);
@@ -580,10 +585,10 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
         const Block b = block_of<W>(a, l, l.groups > 0 ? __builtin_amdgcn_readfirstlane(of[slot]) : sequence_at(a, l, a.cu_seqlens, slot), slot);
         const int n_rows = b.n_rows;
         const int start = W == OWN ? b.start : INT32_MIN;       // a comparison that falls away elsewhere
-        int lo = b.tile0(), lim = b.total, part = -1;
+        int lo = b.tile0(), lim = b.total, part = -1, several = 0;      // several: a block that begins here and goes on, its parts
         if (l.groups > 0) {
             // the block's own units are [p0, p1)
-            const int p0 = __builtin_amdgcn_readfirstlane(before[slot]) + kBlockCost, p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
+            const int p0 = __builtin_amdgcn_readfirstlane(before[slot]) + COST, p1 = __builtin_amdgcn_readfirstlane(before[slot + 1]);
             const int from = max(at, p0), to = min(stop, p1);
             at = max(at, min(stop, p1));
             if (to <= from) continue;       // no rows, or the next workgroup has them all
@@ -591,8 +596,9 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
             lo += (from - p0) * kUnit;
             const bool begins = from == p0, goes_on = to < p1;
             if (!begins || goes_on) part = 2 * group + (begins ? 1 : 0);
-            if (begins && (goes_on || l.by_slot) && kvh == 0 && threadIdx.x == 0)
-                parts.cut[l.by_slot ? slot : group] = goes_on ? Cut{b.row0, n_rows, b.begin, group, (p1 - 1) / each, start} : Cut{};
+            if (W != WHOLE) several = begins && goes_on ? (p1 - 1) / each - group + 1 : 0;
+            else if (begins && (goes_on || l.by_slot) && kvh == 0 && thread == 0)
+                parts.cut[l.by_slot ? slot : group] = goes_on ? Cut{b.row0, n_rows, b.begin, group, (p1 - 1) / each} : Cut{};
         } else {
             at = stop;
             if (!b.any) continue;
@@ -788,9 +794,9 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
                 stage.done();
             };
             // the next tile is on its way while one is worked on
-            constexpr int STEP = 32 * kWaves;
+            constexpr int STEP = 32 * (ALONE ? 1 : kWaves);
             const int plain = min(all_see, hi) - 32;       // last tile that every row sees
-            int t0 = lo + 32 * wave;
+            int t0 = lo + (ALONE ? 0 : 32 * wave);
             if (t0 < hi) {
                 Raw<D> x;
                 load_raw<D>(a, pages, kvh, t0, lane, x);
@@ -816,7 +822,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
             // 64 lanes x 16 bytes.  Wave w converts the keys of its 16 tokens and half
             // of the channels of the values of 32, while the last 64 tokens' are used.
             constexpr int KB = 4 * KS, OPS = KB + 2 * VJ;
-            __shared__ int odd[2][2];       // whether values of 32 tokens were left out (see below)
+            auto& odd = room.odd;
             bf16x8* ops = reinterpret_cast<bf16x8*>(dynamic);
             const int half = wave >> 1;
             const int hi_all = min(end_of(a, b, min(b.begin + l.rows, n_rows) - 1), lim), see_all = end_of(a, b, b.begin);
@@ -1004,23 +1010,30 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
                 float* po = parts.o + i * D + c0;
                 *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
                 *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
-                if (c0 == 0) { parts.sums[2 * i] = mx; parts.sums[2 * i + 1] = sm; }
+                if (c0 == 0) {
+                    parts.sums[2 * i] = mx;
+                    parts.sums[2 * i + 1] = sm;
+                    if constexpr (W != WHOLE) {
+                        if (several > 0) a.rows[place_of(a, b.row0, kvh, row)] = Row{0.f, 0.f, (int)i, W == OWN && start <= 0 ? -several : several};
+                    }
+                }
                 return;
             }
             const int64_t at = place_of(a, b.row0, kvh, row);
-            if constexpr (W == PREFIX) {
-                put_row<D>(a, at, c0, y, mx, sm);
-                return;
-            }
-            float z[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = y[e];
-            if constexpr (W == OWN) {
-                if (start > 0) join_row<D>(a, at, c0, z, mx, sm);
+            if constexpr (W != WHOLE) {
+                const bool joined = W == PREFIX || start > 0;
+                if (c0 == 0) a.rows[at] = Row{mx, sm, 0, joined ? 1 : 0};
+                if (joined) {
+                    float* po = a.row_o + at * D + c0;
+                    *reinterpret_cast<f32x4*>(po) = f32x4{y[0], y[1], y[2], y[3]};
+                    *reinterpret_cast<f32x4*>(po + 4) = f32x4{y[4], y[5], y[6], y[7]};
+                    return;
+                }
             }
             const float f = sm == 0.f ? 0.f : 1.f / sm;
+            float z[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] *= f;
+            for (int e = 0; e < 8; ++e) z[e] = y[e] * f;
             if (a.g) {
                 const E* gp = reinterpret_cast<const E*>(a.g) + at * D + c0;
 #pragma unroll
@@ -1031,7 +1044,7 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
             st4(op + 4, f32x4{z[4], z[5], z[6], z[7]});
         };
 
-        if constexpr (!SPLITW) {
+        if constexpr (!SPLITW || ALONE) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = row0 + 16 * r + n;
@@ -1081,12 +1094,19 @@ __global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void
     }
 }
 
+template <typename E, int D, int R, bool SPLITW>
+__global__ __launch_bounds__(kWaves * 64, (waves_of(sizeof(E) == 2, D, R))) void kda_cache4_attention_kernel(Cache4AttentionArgs a, Layout l, Parts parts) {
+    __shared__ Room<D, R, SPLITW> room;
+    extern __shared__ __align__(16) char dynamic[];
+    attend<E, D, R, SPLITW, false, WHOLE>(a, l, parts, room, dynamic, blockIdx.x);
+}
+
 // Joins the parts of the block that begins in a workgroup of the first kernel
 // and goes on, row by row: weights 2^(m_i - max m).  WAVES waves take turns at
 // the parts of a row, and their sums are joined through LDS in the order of
 // the waves.
-template <typename E, int D, int WAVES, Which W>
-__global__ __launch_bounds__((WAVES > kWaves ? WAVES : kWaves) * 64) void kda_cache4_combine_kernel(typename ArgsOf<W>::type a, Layout l, Parts parts, int chunks) {
+template <typename E, int D, int WAVES>
+__global__ __launch_bounds__((WAVES > kWaves ? WAVES : kWaves) * 64) void kda_cache4_combine_kernel(Cache4AttentionArgs a, Layout l, Parts parts, int chunks) {
     constexpr int PER = D / 64;
     constexpr int ROWS = WAVES > kWaves ? 1 : kWaves / WAVES;      // rows of a workgroup at a time
     __shared__ __align__(16) float acc[ROWS * WAVES][D];
@@ -1156,16 +1176,6 @@ __global__ __launch_bounds__((WAVES > kWaves ? WAVES : kWaves) * 64) void kda_ca
         for (int e = 0; e < PER; ++e) {
             if constexpr (PER == 2) y[e] = o[e];
             else y[e] = o;
-        }
-        if constexpr (W == PREFIX) {
-            put_row<D>(a, at, lane * PER, y, mx, sum);
-            continue;
-        }
-        if constexpr (W == OWN) {
-            if (cut.start > 0) join_row<D>(a, at, lane * PER, y, mx, sum);
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
             y[e] = sum == 0.f ? 0.f : y[e] / sum;
             if (a.g) y[e] *= sigmoidf_(to_f32(gate[e]));
             reinterpret_cast<E*>(a.out)[at * D + lane * PER + e] = from_f32<E>(y[e]);
@@ -1188,15 +1198,18 @@ constexpr int kWideWaves = 8;
 
 struct Plan {
     Layout l;
-    bool splitw;
+    bool splitw, alone;
     int r;
 };
 
-Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a) {
+Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a, Which w) {
     Plan p = {};
     const int64_t rows = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
     p.splitw = rows <= split_max_rows(bf16);
-    p.r = p.splitw ? (rows <= 16 ? 1 : 2) : rows_r(bf16);
+    // Rows of one tile behind a shared prefix go to waves alone: there are many
+    // sequences then, and few tokens of each.  A prefix has no form for one tile.
+    p.alone = w == OWN && rows <= 16;
+    p.r = p.splitw ? (rows <= 16 && (w == WHOLE || p.alone) ? 1 : 2) : rows_r(bf16);
     p.l.rows = p.splitw ? 16 * p.r : 16 * p.r * kWaves;
     p.l.per_seq = (a.group + p.l.rows - 1) / p.l.rows;
     // with or without offsets: enough slots for both
@@ -1213,11 +1226,17 @@ Plan plan_of(bool bf16, int d, const Cache4AttentionArgs& a) {
     int64_t groups = (256 * (p.splitw && waves_of(bf16, d, p.r) == 3 ? 3 : 2) + a.c.heads - 1) / a.c.heads;
     groups = groups < units ? groups : units;
     const bool dealt = p.l.slots <= kMaxDealt && (int64_t)p.l.slots * (cap / kUnit + 1 + kBlockCost) <= kMaxUnits;
+    if (p.alone) groups *= kWaves;
     p.l.groups = dealt ? (int)(groups < 1 ? 1 : groups) : 0;
     p.l.by_slot = p.l.slots < p.l.groups;
     return p;
 }
 
+// Workgroups of a key/value head.
+int64_t workgroups(const Plan& p) {
+    const int64_t n = p.l.groups > 0 ? p.l.groups : p.l.slots;
+    return p.alone ? (n + kWaves - 1) / kWaves : n;
+}
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int cuts(const Plan& p) { return p.l.by_slot ? p.l.slots : p.l.groups; }
 size_t cut_bytes(const Plan& p) { return round256((size_t)cuts(p) * sizeof(Cut)); }
@@ -1225,60 +1244,30 @@ size_t part_places(const Cache4AttentionArgs& a, const Plan& p) {
     return 2 * (size_t)p.l.groups * (size_t)a.c.heads * (size_t)p.l.rows;
 }
 
-template <typename E, int D, int R, bool SPLITW, Which W>
-hipError_t launch_attention_r(const typename ArgsOf<W>::type& a, const Plan& p, const Parts& parts, hipStream_t s) {
-    const int64_t blocks = (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads;
-    const unsigned lds = (SPLITW ? 0u : (unsigned)shared_tiles(D)) + (p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * (unsigned)(sizeof(int32_t) + sizeof(uint16_t)) : 0u);
-    hipLaunchKernelGGL((kda_cache4_attention_kernel<E, D, R, SPLITW, W>), dim3((unsigned)blocks), dim3(kWaves * 64), lds, s, a, p.l,
-                       parts);
-    return hipGetLastError();
+// Bytes of dynamic LDS.
+unsigned dynamic_lds(const Plan& p, int d) {
+    return (p.splitw ? 0u : (unsigned)shared_tiles(d)) + (p.l.groups > 0 ? (unsigned)(p.l.slots + 1) * (unsigned)(sizeof(int32_t) + sizeof(uint16_t)) : 0u);
 }
 
-template <typename E, int D, Which W>
-hipError_t launch_attention_t(const typename ArgsOf<W>::type& a, char* ws, hipStream_t s) {
-    constexpr bool bf16 = sizeof(E) == 2;
-    const Plan p = plan_of(bf16, D, a);
+Parts parts_at(const Cache4AttentionArgs& a, const Plan& p, int d, char* ws) {
     Parts parts = {};
     if (p.l.groups > 0) {
         parts.cut = reinterpret_cast<Cut*>(ws);
         parts.o = reinterpret_cast<float*>(ws + cut_bytes(p));
-        parts.sums = parts.o + part_places(a, p) * D;
+        parts.sums = parts.o + part_places(a, p) * d;
     }
-    hipError_t e;
-    if (!p.splitw) e = launch_attention_r<E, D, rows_r(bf16), false, W>(a, p, parts, s);
-    else if (p.r == 1) e = launch_attention_r<E, D, 1, true, W>(a, p, parts, s);
-    else e = launch_attention_r<E, D, 2, true, W>(a, p, parts, s);
-    if (e != hipSuccess || p.l.groups < 2) return e;
-    // Where a block has many parts, kWideWaves waves share those of a row:
-    // both kernels take 10.7 us instead of 13.3 for one of 4097 tokens (37
-    // parts), 16 instead of 18 for 4 of 8192 (16 parts), 28 instead of 112 for
-    // one head's 50000; with 4 parts 33 instead of 23 for 8 of 4096, 32 rows.
-    const int64_t most = a.group * (a.max_q < a.tokens ? a.max_q : a.tokens);
-    const int rows = (int)(most < p.l.rows ? most : p.l.rows);
-    const bool wide = p.l.slots * 8 <= p.l.groups;
-    const int chunks = wide ? rows : (rows + kWaves - 1) / kWaves;
-    const dim3 grid((unsigned)(cuts(p) * a.c.heads * chunks));
-    if (wide) hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, kWideWaves, W>), grid, dim3(kWideWaves * 64), 0, s, a, p.l, parts, chunks);
-    else hipLaunchKernelGGL((kda_cache4_combine_kernel<E, D, 1, W>), grid, dim3(kWaves * 64), 0, s, a, p.l, parts, chunks);
-    return hipGetLastError();
+    return parts;
 }
 
 // Whether a launch can have as many threads as the problem takes.
-bool attention_fits(bool bf16, int d, const Cache4AttentionArgs& a) {
-    const Plan p = plan_of(bf16, d, a);
-    return (int64_t)(p.l.groups > 0 ? p.l.groups : p.l.slots) * a.c.heads <= UINT32_MAX / (kWaves * 64);
+bool attention_fits(bool bf16, int d, const Cache4AttentionArgs& a, Which w) {
+    return workgroups(plan_of(bf16, d, a, w)) * a.c.heads <= UINT32_MAX / (kWaves * 64);
 }
 
-size_t attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a) {
-    const Plan p = plan_of(bf16, d, a);
+size_t attention_workspace_bytes(bool bf16, int d, const Cache4AttentionArgs& a, Which w) {
+    const Plan p = plan_of(bf16, d, a, w);
     if (p.l.groups == 0) return 0;
     return cut_bytes(p) + part_places(a, p) * (size_t)(d + 2) * sizeof(float);
-}
-
-template <Which W>
-hipError_t launch_attention(bool bf16, int d, const typename ArgsOf<W>::type& a, char* ws, hipStream_t s) {
-    if (bf16) return d == 128 ? launch_attention_t<__bf16, 128, W>(a, ws, s) : launch_attention_t<__bf16, 64, W>(a, ws, s);
-    return d == 128 ? launch_attention_t<float, 128, W>(a, ws, s) : launch_attention_t<float, 64, W>(a, ws, s);
 }
 
 }  // namespace

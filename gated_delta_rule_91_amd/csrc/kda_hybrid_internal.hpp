@@ -117,6 +117,7 @@ hipError_t launch_cache4_attention(bool bf16, int d, const Cache4AttentionArgs& 
 bool cache4_shared_fits(bool bf16, int d, const Cache4SharedArgs& a);
 size_t cache4_shared_workspace_bytes(bool bf16, int d, const Cache4SharedArgs& a);
 hipError_t launch_cache4_shared(bool bf16, int d, const Cache4SharedArgs& a, char* ws, hipStream_t s);
+hipError_t launch_cache4_shared_f32(int d, const Cache4SharedArgs& a, char* ws, hipStream_t s);
 // backward: the workspace of the training pair; else of the prefill alone
 size_t recurrence_workspace_bytes(int64_t B, int64_t T, int64_t D, bool backward);
 hipError_t launch_recurrence(bool bf16, const RecurrenceArgs& a, hipStream_t s);
