@@ -82,8 +82,8 @@ kda_status kda_short_conv_step(int64_t N, int64_t width, int32_t taps, int32_t s
  *   h_n   <- exp(delta A[d, n]) h_n + delta x_t B_t[n]
  *   y_t   = sum_n C_t[n] h_n + skip x_t
  *   out_t = y_t z_t sigmoid(z_t)        (z NULL: out_t = y_t)
- * B_t and C_t are shared by a row's channels.  A is at most 0 (not checked): a
- * state then fades.  States, sums and the gradients' sums are fp32. */
+ * B_t and C_t are shared by a row's channels.  A is finite and at most 0 (not
+ * checked): a state then fades.  States, sums and the gradients' sums are fp32. */
 typedef struct {
     int64_t batch;          /* rows; 1 for a packed batch                        */
     int64_t seqlen;         /* tokens of a row                                   */

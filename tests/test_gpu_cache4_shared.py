@@ -143,6 +143,19 @@ def test_many_sequences_and_a_long_prefix():
     check(b, "bf16", decode=True)
 
 
+@pytest.mark.parametrize("heads", [2, 17])
+def test_more_sequences_than_are_dealt_out(heads):
+    """Blocks past 4096 are a workgroup's, or a wave's, each."""
+    n = 4400
+    offsets = list(range(0, n + 1, 2))
+    check(build(offsets, [5 + j % 30 for j in range(n // 2)], [1 + s % 7 for s in range(n)], [1] * n, heads, 1, 64, 16, "bf16", gate=False), "bf16",
+          decode=True)
+
+
+def test_sequences_without_queries():
+    check(build([0, 4, 6], [40, 21], [9, 20, 3, 5, 2, 2], [0, 20, 3, 0, 0, 0], 8, 2, 128, 16, "bf16"), "bf16")
+
+
 def test_more_groups_than_sequences_and_none():
     """Empty groups, groups that hold nothing but queries of nobody, and no group at all."""
     b = build([0, 0, 2, 2, 2, 3], [5, 40, 7, 9, 30], [4, 5, 6], [1, 1, 1], 4, 2, 64, 16, "f32")

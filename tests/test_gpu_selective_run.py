@@ -175,6 +175,20 @@ def test_training_pass_in_a_graph(packed):
         replays(graph, lambda: None, res, expected)
 
 
+def test_backward_twice():
+    """What the forward call keeps serves a second backward, with the same results."""
+    i = made(2, 900, 70, 16, "bf16")
+    leaves = [i[k].requires_grad_() for k in ("x", "dt", "A", "B", "C", "skip", "z", "dt_bias", "state")]
+    weight = gpu_random(1)(70, 4).requires_grad_()
+    x, _ = kda.short_conv_autograd(leaves[0], weight)
+    out, state = kda.selective_scan_autograd(x, *leaves[1:])
+    loss = (out.float() * i["d_out"]).sum() + (state * i["d_state"]).sum()
+    first = torch.autograd.grad(loss, leaves + [weight], retain_graph=True)
+    second = torch.autograd.grad(loss, leaves + [weight])
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+
+
 def test_two_graphs_with_one_workspace():
     """Replayed in turn on a stream, each is as alone: nothing lives in a workspace from one call to the next but what the
     training pair keeps there."""
