@@ -1,5 +1,5 @@
 // kda_cache4_attention.hpp -- the kernels of causal grouped-query attention over
-// the paged 4-bit cache, for kda_cache4_attention.hip and kda_cache4_shared.hip.
+// the paged 4-bit cache, for kda_cache4_attention.hip and kda_cache4_shared.hpp.
 //
 //   out = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),  s_t = scale q . K_t,
 //   m = max s_t, kept as a running maximum and sum in fp32.

@@ -11,6 +11,14 @@
 // that its rows call for, and workgroups of one launch: neither waits for the
 // other, and what each waits for (offsets, tables, its first tiles) passes
 // meanwhile.  A second kernel joins what they leave of a row.
+//
+// 256 requests of one query on 8192 shared tokens and up to 1000 of their own, 32 heads
+// over 8 of 128, bf16, take 5 us for the groups, 86 for both sides and 12 for joining;
+// two launches for the sides, each with a second kernel for its parts, took 115.  The
+// prefix is bound by what prompts are bound by (55 us of it), the rest by HBM (27 us at
+// the rate of a copy): the two overlap only where workgroups of both are on a CU.
+// 4 prompts of 500 on 65536 shared tokens take 5 + 737 + 15, 785 TFLOP/s; 48
+// requests in 5 groups on 20000 tokens, 24 heads over 4 of 64, fp32, 4 + 41 + 11.
 #pragma once
 
 #include "kda_cache4_attention.hpp"
@@ -120,7 +128,8 @@ __device__ __forceinline__ Share share_of(const Side& side, int64_t at, const Ro
 
 // Joins what the two sides leave, row by row: weights 2^(m_i - max m).  WAVES waves
 // take turns at a row's entries, and their sums are joined through LDS in the
-// order of the waves.
+// order of the waves.  Latency bounds it: a row's entries tell where its parts are
+// (12 us above; found through its sequence, group and cuts it took 19).
 template <typename E, int D, int WAVES>
 __global__ __launch_bounds__((WAVES > kWaves ? WAVES : kWaves) * 64) void kda_cache4_join_kernel(Side prefix, Side own) {
     constexpr int PER = D / 64;
