@@ -16,7 +16,7 @@
 // over 8 of 128, bf16, take 5 us for the groups, 86 for both sides and 12 for joining;
 // two launches for the sides, each with a second kernel for its parts, took 115.  The
 // prefix is bound by what prompts are bound by (55 us of it), the rest by HBM (27 us at
-// the rate of a copy): the two overlap only where workgroups of both are on a CU.
+// the rate of a copy) and by converting what it reads.
 // 4 prompts of 500 on 65536 shared tokens take 5 + 737 + 15, 785 TFLOP/s; 48
 // requests in 5 groups on 20000 tokens, 24 heads over 4 of 64, fp32, 4 + 41 + 11.
 #pragma once
@@ -297,11 +297,17 @@ hipError_t launch_shared(const Cache4SharedArgs& s, char* ws, hipStream_t stream
     if (!l.prefix.splitw) e = launch_own<E, D, rows_r(bf16), false>(prefix, own, l, stream);
     else e = launch_own<E, D, 2, true>(prefix, own, l, stream);
     if (e != hipSuccess) return e;
-    // rows whose prefix is in many parts, as where kda_cache4_attention.hip joins them
-    const bool wide = l.prefix.l.slots * 8 <= l.prefix.l.groups;
-    const int64_t rows = s.a.tokens * s.a.heads, turns = wide ? rows : (rows + kWaves - 1) / kWaves;
+    // Where a row has many parts, several waves share them, as where
+    // kda_cache4_attention.hip joins them: 8 where rows are few, 4 where there are
+    // waves enough.  240 rows take 6.0 us with 8 and 9.2 with 4 (28.5 with 1), 1152
+    // 9.7 and 6.2, 2048 15.8 and 10.
+    constexpr int SOME = 4;
+    const int64_t rows = s.a.tokens * s.a.heads;
+    const bool many = l.prefix.l.slots * 8 <= l.prefix.l.groups, few = rows <= 512;
+    const int64_t turns = many ? rows : (rows + kWaves - 1) / kWaves;
     const dim3 grid((unsigned)(turns < (1 << 20) ? turns : (1 << 20)));
-    if (wide) hipLaunchKernelGGL((kda_cache4_join_kernel<E, D, kWideWaves>), grid, dim3(kWideWaves * 64), 0, stream, prefix, own);
+    if (many && few) hipLaunchKernelGGL((kda_cache4_join_kernel<E, D, kWideWaves>), grid, dim3(kWideWaves * 64), 0, stream, prefix, own);
+    else if (many) hipLaunchKernelGGL((kda_cache4_join_kernel<E, D, SOME>), grid, dim3(SOME * 64), 0, stream, prefix, own);
     else hipLaunchKernelGGL((kda_cache4_join_kernel<E, D, 1>), grid, dim3(kWaves * 64), 0, stream, prefix, own);
     return hipGetLastError();
 }

@@ -143,6 +143,13 @@ def test_many_sequences_and_a_long_prefix():
     check(b, "bf16", decode=True)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n,heads,kv,d", [(64, 16, 2, 64), (40, 16, 1, 128), (20, 16, 1, 64)])
+def test_rows_in_many_parts(n, heads, kv, d, io):
+    """More than 512 rows, and fewer, of a long prefix that many workgroups share."""
+    check(build([0, n], [2900], [1 + s % 5 for s in range(n)], [1] * n, heads, kv, d, 16, io), io, decode=True)
+
+
 @pytest.mark.parametrize("heads", [2, 17])
 def test_more_sequences_than_are_dealt_out(heads):
     """Blocks past 4096 are a workgroup's, or a wave's, each."""
